@@ -335,6 +335,89 @@ wush_status wush_fixed_transforms(int kind, int64_t C, int G, double* T, void* T
  * aligned, dst 2-byte aligned; they must not overlap. */
 wush_status wush_f64_to_bf16(const double* src, int64_t n, void* dst, hipStream_t stream);
 
+/* ---- Decoding: the quantized weights with a few tokens --------------------
+ *
+ * These entries serve what a model with weights in the formats above runs per
+ * generated token.  The pages define none of them; they are interfaces of this
+ * library.  Beyond the conventions above, some need a caller-owned
+ * workspace: a 16-byte aligned device buffer of at least the size that the
+ * entry's *_workspace function returns (0: none, NULL is fine).  Its content
+ * is not read before it is written and means nothing afterwards; two calls
+ * in flight at the same time need one each. */
+
+/* Linear layer with 4-bit weights and bf16 activations:
+ *     Y[m][n] = sum_k x'[m][k] w[n][k],
+ * w the values that codes and scales stand for (as in wush_dequant), x' = x
+ * without T, or the block transform T_c x_c of the format's group size G (as
+ * in wush_transform_f32) for weights quantized with the matching weight-side
+ * transform.  Products are exact, sums fp32; x' is kept to 16 significant bits for a
+ * bf16 Y and to fp32 accuracy for an fp32 Y.
+ *   X: bf16 [M][K], row m at X + m * ldx elements (ldx >= K, a multiple of 8;
+ *      16-byte aligned).  T: bf16 [K/G][G][G], 16-byte aligned, or NULL.
+ *   codes u8 [N][K/2], 8-byte aligned; scales [N][K/G] (fp16 for INT4).
+ *   global_scale: device fp32, NVFP4 only (wush_nvfp4_global_scale).
+ *   Y: [M][N] fp32 or bf16 (out_type as in wush_gemm_mxfp4).
+ * K is a positive multiple of G; any M and N >= 0 (0 is a no-op), M up to
+ * about a million.  It is meant for few tokens: from about a hundred on,
+ * quantized activations and wush_gemm_mxfp4 are faster.
+ * workspace: needed with T only. */
+wush_status wush_linear_w4(int fmt, const void* X, int64_t ldx, const void* T, const void* codes, const void* scales,
+                           const float* global_scale, int64_t M, int64_t N, int64_t K, void* Y, int out_type,
+                           void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t wush_linear_w4_workspace(int64_t M, int64_t K, int out_type);
+
+/* Mixture-of-experts layer with 4-bit expert weights, for a few tokens.  Per
+ * token x:
+ *   l_e = sum_k router[e][k] x[k] (fp32);  ids = the topk largest l_e, largest
+ *   first, ties to the lower e;  weights = softmax over all experts, or over the
+ *   chosen ones if renormalize != 0, of l at ids;
+ *   h_e = T_mid[e] (silu(gate_e x') * (up_e x')),  x' = T_in x;
+ *   y = sum over ids of weights * down_e h_e.
+ * T_in (shared by the experts) and T_mid (one bank per expert) are block
+ * transforms as in wush_linear_w4; either may be NULL (none).
+ *   X: bf16 [M][H] with row stride ldx, as in wush_linear_w4.
+ *   router: bf16 [E][H], 16-byte aligned.
+ *   gate_up_codes u8 [E][2 I][H/2], gate_up_scales [E][2 I][H/G]: I gate rows,
+ *   then I up rows.  down_codes u8 [E][H][I/2], down_scales [E][H][I/G].
+ *   gate_up_global, down_global: device fp32 [E], NVFP4 only.
+ *   T_in: bf16 [H/G][G][G].  T_mid: bf16 [E][I/G][G][G].
+ *   Y: [M][H] fp32 or bf16; ids: int32 [M][topk]; weights: fp32 [M][topk].
+ * H and I are positive multiples of G, at most 2^24; 1 <= E <= 1024;
+ * 1 <= topk <= min(E, 32).  M >= 0; tokens are taken 64 at a time.  A NaN
+ * logit ranks below every number; results are then NaN but all accesses stay in
+ * range.
+ * Results repeat bit for bit.  transform: whether T_in is given. */
+wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router, const void* gate_up_codes,
+                        const void* gate_up_scales, const float* gate_up_global, const void* T_in,
+                        const void* down_codes, const void* down_scales, const float* down_global, const void* T_mid,
+                        int64_t M, int64_t E, int topk, int renormalize, int64_t H, int64_t I, void* Y, int out_type,
+                        int32_t* ids, float* weights, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t wush_moe_w4_workspace(int64_t M, int64_t E, int topk, int64_t H, int64_t I, int transform, int out_type);
+
+/* Element type of wush_token_logprobs' logits. */
+typedef enum { WUSH_LOGITS_F32 = 0, WUSH_LOGITS_BF16 = 1, WUSH_LOGITS_F16 = 2 } wush_logit_type;
+
+/* Log probabilities of given tokens, entropies and the most likely
+ * alternatives, per row l of logits:
+ *   logprob = l[target] - log sum_v exp(l[v]),
+ *   entropy = -sum_v p_v log p_v (natural logarithm; p_v = 0 adds 0),
+ *   top_ids, top_logprobs = the `top` largest l, largest first, ties to the
+ *   lower index, with their log probabilities.
+ * Logits of -inf (masked tokens) have probability 0 and are never listed: rows
+ * with fewer others end in id -1 and log probability -inf.  A row of nothing
+ * but -inf has logprob -inf and entropy 0.  A row with a NaN or +inf has NaN
+ * for every value and -1 for every id.  A negative target is not scored
+ * (logprob 0); a target of V or more gives NaN.
+ *   logits: fp32, bf16 or fp16 [R][V], row r at r * ld elements (ld >= V),
+ *   aligned to their elements.  targets: int64 [R].
+ *   logprob, entropy: fp32 [R]; top_ids: int32 [R][top]; top_logprobs:
+ *   fp32 [R][top] (both unused for top = 0).
+ * 1 <= V < 2^31, 0 <= top <= 32, R >= 0 (0 is a no-op) and at most 2^24. */
+wush_status wush_token_logprobs(const void* logits, int logit_type, int64_t ld, int64_t R, int64_t V,
+                                const int64_t* targets, int top, float* logprob, float* entropy, int32_t* top_ids,
+                                float* top_logprobs, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t wush_token_logprobs_workspace(int64_t R, int64_t V, int logit_type, int top);
+
 /* Status text, and the detail of the last failure on this thread.  Library
  * interfaces; nothing on the pages corresponds. */
 const char* wush_status_string(wush_status status);

@@ -13,13 +13,18 @@ from ._lib import FMT, LIB_PATH, WushError, load  # noqa: F401
 __all__ = [
     "load", "WushError", "quant", "quant_mxfp4", "quant_nvfp4", "quant_int4", "transform_f32",
     "absmax_transformed", "nvfp4_global_scale", "e2m1_encode", "build_transforms", "fixed_transforms",
-    "f64_to_bf16", "dequant", "gemm_mxfp4",
+    "f64_to_bf16", "dequant", "gemm_mxfp4", "linear_w4", "moe_w4", "token_logprobs", "W4Experts", "MoeResult",
+    "TokenLogprobs",
 ]
+
+_DECODE = {"linear_w4", "moe_w4", "token_logprobs", "W4Experts", "MoeResult", "TokenLogprobs"}
 
 
 def __getattr__(name):
     # torch-dependent wrappers are imported on first use
     if name in __all__:
-        from . import ops
-        return getattr(ops, name)
+        from . import decode, ops
+        value = getattr(decode if name in _DECODE else ops, name)
+        globals()[name] = value  # later look-ups find it without this function
+        return value
     raise AttributeError(name)

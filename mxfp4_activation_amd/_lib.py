@@ -38,6 +38,13 @@ SIGNATURES = {
     "wush_f64_to_bf16": (_c_int, [_vp, _i64, _vp, _vp]),
     "wush_nvfp4_global_scale": (_c_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "wush_e2m1_encode": (_c_int, [_vp, _i64, _vp, _vp]),
+    "wush_linear_w4": (_c_int, [_c_int, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _c_int, _vp, _i64, _vp]),
+    "wush_linear_w4_workspace": (_i64, [_i64, _i64, _c_int]),
+    "wush_moe_w4": (_c_int, [_c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _c_int, _c_int,
+                             _i64, _i64, _vp, _c_int, _vp, _vp, _vp, _i64, _vp]),
+    "wush_moe_w4_workspace": (_i64, [_i64, _i64, _c_int, _i64, _i64, _c_int, _c_int]),
+    "wush_token_logprobs": (_c_int, [_vp, _c_int, _i64, _i64, _i64, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "wush_token_logprobs_workspace": (_i64, [_i64, _i64, _c_int, _c_int]),
     "wush_status_string": (ctypes.c_char_p, [_c_int]),
     "wush_last_error": (ctypes.c_char_p, []),
     "wush_abi_version": (_c_int, []),
