@@ -93,7 +93,7 @@ wush_status launched(hipError_t e) {
 int64_t moe_chunk(int64_t M) { return M < wush::kMoeTokens ? M : wush::kMoeTokens; }
 
 struct MoeWorkspace {
-  uint64_t planes, logits, h, slots, n_tiles, tiles, total;
+  uint64_t planes, h, part, logits, slots, n_tiles, tiles, total;
 };
 
 MoeWorkspace moe_workspace(int64_t M, int64_t E, int topk, int64_t H, int64_t I, bool transform, int out_type) {
@@ -101,7 +101,8 @@ MoeWorkspace moe_workspace(int64_t M, int64_t E, int topk, int64_t H, int64_t I,
   MoeWorkspace w;
   w.planes = 0;
   w.h = w.planes + (transform ? round16(terms * c * H * 2) : 0);
-  w.logits = w.h + round16(terms * slots * I * 2);
+  w.part = w.h + round16(terms * slots * I * 2);
+  w.logits = w.part + round16(slots * H * 4);
   w.slots = w.logits + round16(c * E * 4);
   w.n_tiles = w.slots + round16(slots * 4);
   w.tiles = w.n_tiles + 16;
@@ -269,9 +270,12 @@ wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router,
   a.H = H;
   a.I = I;
   a.renorm = renormalize != 0;
-  a.h_terms = terms_of(out_type);
+  a.terms = terms_of(out_type);
   a.bf16_out = out_type == WUSH_OUT_BF16;
+  a.T_in = static_cast<const uint16_t*>(T_in);
+  a.xt = reinterpret_cast<uint16_t*>(ws + w.planes);
   a.h = reinterpret_cast<uint16_t*>(ws + w.h);
+  a.part = reinterpret_cast<float*>(ws + w.part);
   a.logits = reinterpret_cast<float*>(ws + w.logits);
   a.slots = reinterpret_cast<int32_t*>(ws + w.slots);
   a.n_tiles = reinterpret_cast<int32_t*>(ws + w.n_tiles);
@@ -282,21 +286,6 @@ wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router,
     a.Y = static_cast<uint8_t*>(Y) + m0 * H * out_bytes_of(out_type);
     a.ids = ids + m0 * topk;
     a.weights = weights + m0 * topk;
-    a.x = wush::Planes{a.X, a.ldx, 0, 1};
-    if (T_in) {
-      wush::SplitArgs t{};
-      t.X = a.X;
-      t.ldx = a.ldx;
-      t.T = static_cast<const uint16_t*>(T_in);
-      t.out = reinterpret_cast<uint16_t*>(ws + w.planes);
-      t.M = a.M;
-      t.K = H;
-      t.G = G;
-      t.terms = terms_of(out_type);
-      st = launched(wush::launch_split(t, stream));
-      if (st != WUSH_OK) return st;
-      a.x = wush::Planes{t.out, H, a.M * H, t.terms};
-    }
     st = launched(wush::launch_moe(a, stream));
     if (st != WUSH_OK) return st;
   }

@@ -1,8 +1,8 @@
 // A mixture-of-experts layer on 4-bit weights for a few tokens:
 //   l = Wr x,  the topk largest l_e (ties: lowest e),  softmax weights w_e,
 //   y = sum_e w_e Wd_e T_mid,e (silu(Wg_e x') * (Wu_e x')),  x' = x or T_in x.
-// Four launches on one stream: the router's logits; the choice of experts and the
-// grouping of tokens by expert; gate, up and their product; down and the
+// Launches on one stream: the router's logits (and T_in x); the choice of
+// experts and the grouping of tokens by expert; gate, up and their product; down; the
 // weighted sum.  Every sum has a fixed order, so results repeat bit for bit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -17,27 +17,57 @@ using namespace w4;
 
 // ------------------------------------------------------------ router
 //
-// Logits of 16 experts for 16 tokens per workgroup, K split over the waves.
+// Logits of 16 experts for 16 tokens per workgroup, K split over the waves.  The
+// workgroups behind those transform: each wave 32 channels of 16 tokens.
 constexpr int kRouterWaves = 16;
 
-__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a, int router_tiles) {
   __shared__ float red[kRouterWaves][16][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-  const int e0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+  const int m0 = blockIdx.y * 16;
+  if ((int)blockIdx.x >= router_tiles) {
+    const int64_t panel = (int64_t)(blockIdx.x - router_tiles) * kRouterWaves + wave;
+    if (panel * 32 < a.H)
+      split_panel(SplitArgs{a.X, a.ldx, a.T_in, a.xt, a.M, a.H, a.fmt == kNV ? 16 : 32, a.terms}, panel, m0);
+    return;
+  }
+  const int e0 = blockIdx.x * 16;
   const int rows = a.M - m0 < 16 ? a.M - m0 : 16;
   const int e = e0 + n < a.E ? e0 + n : a.E - 1;
-  const uint8_t* cp[1] = {reinterpret_cast<const uint8_t*>(a.router + e * a.H)};
-  const uint8_t* sp[1] = {nullptr};
-  const uint16_t* xp[1] = {a.X + (int64_t)(m0 + (n < rows ? n : 0)) * a.ldx};
-  f32x4 acc[1][1] = {{f32x4{0, 0, 0, 0}}};
-  wave_dot<kBF, 1, 1, 1>(acc, cp, sp, xp, 0, (int)a.H, wave, kRouterWaves);
+  const uint16_t* w = a.router + (int64_t)e * a.H + 8 * q;
+  const uint16_t* x = a.X + (int64_t)(m0 + (n < rows ? n : 0)) * a.ldx + 8 * q;
+  f32x4 acc = {0, 0, 0, 0};
+  const int vecs = (int)(a.H / 32);  // instructions of 32 elements; H may end in half of one
+  constexpr int kBatch = 8;          // their loads are on their way together
+  for (int i0 = wave; i0 < vecs; i0 += kBatch * kRouterWaves) {
+    bf16x8 xv[kBatch], wv[kBatch];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[wave][4 * q + i][n] = acc[0][0][i];
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kRouterWaves, at = 32 * (i < vecs ? i : wave);
+      xv[b] = *reinterpret_cast<const bf16x8*>(x + at);
+      wv[b] = *reinterpret_cast<const bf16x8*>(w + at);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (i0 + b * kRouterWaves < vecs) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[b], wv[b], acc, 0, 0, 0);
+  }
+  if (a.H % 32 != 0 && wave == vecs % kRouterWaves) {
+    u32x4 xv = {0, 0, 0, 0}, wv = {0, 0, 0, 0};
+    if (q < 2) {
+      xv = *reinterpret_cast<const u32x4*>(x + 32 * vecs);
+      wv = *reinterpret_cast<const u32x4*>(w + 32 * vecs);
+    }
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv), __builtin_bit_cast(bf16x8, wv), acc,
+                                                  0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[wave][4 * q + i][n] = acc[i];
   __syncthreads();
   if (threadIdx.x < 256) {
     const int m = threadIdx.x >> 4, c = threadIdx.x & 15;
     float v = 0.0f;
-    for (int w = 0; w < kRouterWaves; ++w) v += red[w][m][c];
+#pragma unroll
+    for (int k = 0; k < kRouterWaves; ++k) v += red[k][m][c];
     if (m < rows && e0 + c < a.E) a.logits[(int64_t)(m0 + m) * a.E + e0 + c] = v;
   }
 }
@@ -45,26 +75,10 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a) {
 // ------------------------------------------------------------ choice
 //
 // One workgroup.  A wave chooses a token's experts: every lane holds the
-// logits of experts lane, lane + 64, ... as keys (ordered logit, then lower
-// index first), and the largest key of the wave is taken topk times.  Then
-// one thread per expert collects its tokens in order.
+// logits of experts lane, lane + 64, ...; topk times the largest of the wave
+// is found, and among its equals the lowest expert.  Then expert e's tokens are
+// the set bits of a 64-bit mask, in order.
 constexpr int kRouteThreads = 1024;
-
-// Order-preserving: larger float, larger key; NaN below everything.
-__device__ __forceinline__ uint32_t order_bits(float v) {
-  const uint32_t b = __float_as_uint(v);
-  if (v != v) return 0u;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)v, d);
-    v = o > v ? o : v;
-  }
-  return v;
-}
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -72,36 +86,73 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// Largest v of the wave, in all lanes.
+__device__ __forceinline__ float wave_max(float v) {
+#define WUSH_MAX_DPP(ctrl, rows)                                                                                    \
+  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(v), __float_as_uint(v), ctrl, rows, 0xf, \
+                                                           false)))
+  WUSH_MAX_DPP(0x111, 0xf);  // row_shr 1, 2, 4, 8: lane 15 of every row has the row's
+  WUSH_MAX_DPP(0x112, 0xf);
+  WUSH_MAX_DPP(0x114, 0xf);
+  WUSH_MAX_DPP(0x118, 0xf);
+  WUSH_MAX_DPP(0x142, 0xa);  // row_bcast 15: into rows 1 and 3
+  WUSH_MAX_DPP(0x143, 0xc);  // row_bcast 31: into rows 2 and 3
+#undef WUSH_MAX_DPP
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
 template <int J>  // experts per lane
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a, int tile_tokens) {
-  __shared__ int ids[kMoeTokens * kMoeMaxTopK];
-  __shared__ int scan_slots[kRouteThreads], scan_tiles[kRouteThreads];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n_slots = a.M * a.topk;
+  __shared__ unsigned long long tokens[kMoeMaxExperts];  // of each expert
+  __shared__ int start[kMoeMaxExperts];
+  __shared__ int wave_slots[16], wave_tiles[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = threadIdx.x;
+  tokens[e] = 0;
+  __syncthreads();
   for (int m = wave; m < a.M; m += kRouteThreads / 64) {
-    float l[J];
-    uint64_t key[J];
+    const float* logits = a.logits + (int64_t)m * a.E;
+    float l[J], left[J];
+    uint32_t taken = 0;  // bit j: expert lane + 64 j is taken, or there is none
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int e = lane + 64 * j;
-      l[j] = e < a.E ? a.logits[(int64_t)m * a.E + e] : 0.0f;
-      key[j] = e < a.E ? ((uint64_t)order_bits(l[j]) << 32) | (0xFFFFFFFFu - (uint32_t)e) : 0u;
+      const int k = lane + 64 * j;
+      l[j] = k < a.E ? logits[k] : 0.0f;
+      left[j] = l[j] == l[j] ? l[j] : -__builtin_inff();  // NaN ranks below every number
+      if (k >= a.E) taken |= 1u << j;
     }
     int my_id = 0;
     for (int p = 0; p < a.topk; ++p) {
-      uint64_t best = key[0];
-#pragma unroll
-      for (int j = 1; j < J; ++j) best = key[j] > best ? key[j] : best;
-      best = wave_max_u64(best);
+      float best = -__builtin_inff();
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (key[j] == best) key[j] = 0;
-      if (lane == p) my_id = (int)(0xFFFFFFFFu - (uint32_t)best);
+        if (!(taken >> j & 1u)) best = fmaxf(best, left[j]);
+      best = wave_max(best);
+      int id = -1;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const uint64_t at = __ballot(!(taken >> j & 1u) && left[j] == best);
+        if (id < 0 && at != 0) id = 64 * j + __ffsll((unsigned long long)at) - 1;
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (id == lane + 64 * j) taken |= 1u << j;
+      if (lane == p) my_id = id;
     }
     const bool mine = lane < a.topk;
-    const float lp = mine ? a.logits[(int64_t)m * a.E + my_id] : 0.0f;
-    const float top = __shfl(lp, 0);
-    const float w = mine ? expf(lp - top) : 0.0f;
+    const float my_l = mine ? logits[my_id] : 0.0f;
+    const float top = __shfl(my_l, 0);
+    const float w = mine ? expf(my_l - top) : 0.0f;
     float part = w;
     if (!a.renorm) {
       part = 0.0f;
@@ -113,273 +164,246 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a, int til
     if (mine) {
       a.ids[m * a.topk + lane] = my_id;
       a.weights[m * a.topk + lane] = w / total;
-      ids[m * a.topk + lane] = my_id;
+      atomicOr(&tokens[my_id], 1ull << m);
     }
   }
   __syncthreads();
-  // Thread e: expert e's slots, in order of the tokens.
-  const int e = threadIdx.x;
-  int count = 0;
-  if (e < a.E)
-    for (int s = 0; s < n_slots; ++s) count += ids[s] == e;
-  const int tiles = (count + tile_tokens - 1) / tile_tokens;
-  scan_slots[e] = count;
-  scan_tiles[e] = tiles;
-  __syncthreads();
-  for (int d = 1; d < kRouteThreads; d <<= 1) {
-    const int s = e >= d ? scan_slots[e - d] : 0, t = e >= d ? scan_tiles[e - d] : 0;
-    __syncthreads();
-    scan_slots[e] += s;
-    scan_tiles[e] += t;
-    __syncthreads();
+  // Thread e: expert e's slots and tiles; their places by a prefix sum over experts.
+  const unsigned long long mask = tokens[e];
+  const int count = __popcll(mask), tiles = (count + tile_tokens - 1) / tile_tokens;
+  const int slots_to = wave_scan(count), tiles_to = wave_scan(tiles);
+  if (lane == 63) {
+    wave_slots[wave] = slots_to;
+    wave_tiles[wave] = tiles_to;
   }
-  int at = scan_slots[e] - count;
+  __syncthreads();
+  int slots_before = 0, tiles_before = 0;
+  for (int k = 0; k < wave; ++k) {
+    slots_before += wave_slots[k];
+    tiles_before += wave_tiles[k];
+  }
+  const int first = slots_before + slots_to - count;
+  start[e] = first;
   for (int t = 0; t < tiles; ++t) {
     const int left = count - t * tile_tokens;
-    a.tiles[scan_tiles[e] - tiles + t] =
-        MoeTile{e, at + t * tile_tokens, left < tile_tokens ? left : tile_tokens, 0};
+    a.tiles[tiles_before + tiles_to - tiles + t] =
+        MoeTile{e, first + t * tile_tokens, left < tile_tokens ? left : tile_tokens, 0};
   }
-  if (count > 0)
-    for (int s = 0; s < n_slots; ++s)
-      if (ids[s] == e) a.slots[at++] = s;
-  if (e == kRouteThreads - 1) *a.n_tiles = scan_tiles[e];
+  if (e == kRouteThreads - 1) *a.n_tiles = tiles_before + tiles_to;
+  __syncthreads();
+  for (int s = threadIdx.x; s < a.M * a.topk; s += kRouteThreads) {
+    const int m = s / a.topk, id = a.ids[s];  // written by this workgroup, before a barrier
+    a.slots[start[id] + __popcll(tokens[id] & ((1ull << m) - 1))] = s;
+  }
 }
 
 // ------------------------------------------------------------ gate and up
 //
-// A workgroup owns 32 channels of h for one tile of tokens of one expert: 32
-// gate rows and 32 up rows, K split over the waves.  The 32 channels hold
-// whole transform blocks, so T_mid is applied to h right here.
-constexpr int kWaves = 8;
-
-template <int FMT, int NT, int TERMS>
-__global__ __launch_bounds__(64 * kWaves) void gate_up_kernel(MoeArgs a) {
-  __shared__ float red[kWaves][4][NT][16][16];
+// A workgroup owns 32 WN channels of h for one tile of tokens of one expert:
+// wave wn has 32 gate rows and the 32 up rows of the same channels.  32 channels
+// hold whole transform blocks, so T_mid is applied to h right here.
+template <int FMT, int NT, int TERMS, bool SPREAD, int WN, int WK>
+__global__ __launch_bounds__(64 * WN * WK, 2) void gate_up_kernel(MoeArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  __shared__ int slot[16 * NT];
+  constexpr int kThreads = 64 * WN * WK, kChannels = 32 * WN, kRows = SPREAD ? 4 : 16 * NT;
   if ((int)blockIdx.y >= *a.n_tiles) return;
   const MoeTile tile = a.tiles[blockIdx.y];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-  const int64_t H = a.H, I = a.I, i0 = (int64_t)blockIdx.x * 32;
-
-  const uint8_t* cp[4];
-  const uint8_t* sp[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t i = i0 + 16 * (r & 1) + n;
-    const int64_t row = (int64_t)tile.expert * (2 * I) + (r < 2 ? 0 : I) + (i < I ? i : I - 1);
-    cp[r] = a.gu_codes + row * row_code_bytes<FMT>(H);
-    sp[r] = a.gu_scales + row * row_scale_bytes<FMT>(H);
-  }
-  const uint16_t* xp[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int s = a.slots[tile.start + (16 * t + n < tile.count ? 16 * t + n : 0)];
-    xp[t] = a.x.X + (int64_t)(s / a.topk) * a.x.ldx;
-  }
-  f32x4 acc[4][NT];
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
-  wave_dot<FMT, 4, NT, TERMS>(acc, cp, sp, xp, a.x.plane, (int)H, wave, kWaves);
-
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[wave][r][t][4 * q + i][n] = acc[r][t][i];
+  const int n = threadIdx.x & 15, wn = (threadIdx.x >> 6) % WN;
+  const int64_t H = a.H, I = a.I, i0 = (int64_t)blockIdx.x * kChannels;
+  if ((int)threadIdx.x < tile.count) slot[threadIdx.x] = a.slots[tile.start + threadIdx.x];
+  const auto p = make_rows<FMT, 4, 1>(a.gu_codes, a.gu_scales, H, [&](int r) {
+    const int64_t i = i0 + 32 * wn + 16 * (r & 1) + n;
+    return (int64_t)tile.expert * (2 * I) + (r < 2 ? 0 : I) + (i < I ? i : I - 1);
+  });
   __syncthreads();
+  const uint16_t* X = a.T_in ? a.xt : a.X;
+  const int64_t ldx = a.T_in ? H : a.ldx;
+  group_dot<FMT, 4, 1, NT, TERMS, SPREAD, WN, WK>(
+      lds, p, [&](int row) { return X + slot[row] / a.topk * ldx; }, a.M * H, tile.count, H);
   const float gs = FMT == kNV ? a.gu_gs[tile.expert] : 1.0f;
-  const int c = threadIdx.x & 31;
-  float h[NT];
+  // Value v: token v / kChannels, channel v % kChannels.
+  constexpr int kEach = (kRows * kChannels + kThreads - 1) / kThreads;
+  const int values = tile.count * kChannels;
+  float h[kEach];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int m = threadIdx.x >> 5;
-    float g = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      g += red[w][c >> 4][t][m][c & 15];
-      u += red[w][2 + (c >> 4)][t][m][c & 15];
+  for (int k = 0; k < kEach; ++k) {
+    const int v = threadIdx.x + k * kThreads, m = v / kChannels, c = v % kChannels;
+    h[k] = 0.0f;
+    if (v < values) {
+      const int row = 64 * (c / 32) + c % 32;
+      float g = group_sum<4, WN, WK>(lds, row, m, tile.count);
+      float u = group_sum<4, WN, WK>(lds, row + 32, m, tile.count);
+      if (FMT == kNV) {
+        g *= gs;
+        u *= gs;
+      }
+      h[k] = g / (1.0f + expf(-g)) * u;
     }
-    if (FMT == kNV) {
-      g *= gs;
-      u *= gs;
-    }
-    h[t] = g / (1.0f + expf(-g)) * u;
   }
   if (a.T_mid) {
     constexpr int G = FMT == kNV ? 16 : 32;
-    __syncthreads();  // everyone has read red
-    float(*hs)[16][32] = reinterpret_cast<float(*)[16][32]>(&red[0][0][0][0][0]);
+    __syncthreads();  // everyone has read the sums
+    float* hs = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) hs[t][threadIdx.x >> 5][c] = h[t];
+    for (int k = 0; k < kEach; ++k) {
+      const int v = threadIdx.x + k * kThreads;
+      if (v < values) hs[v] = h[k];
+    }
     __syncthreads();
-    const int64_t i = i0 + c < I ? i0 + c : I - 1;
-    const uint16_t* T = a.T_mid + ((int64_t)tile.expert * I + i) * G;  // row i % G of block i / G
-    const int b = c / G * G;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) h[t] = 0.0f;
+    for (int k = 0; k < kEach; ++k) {
+      const int v = threadIdx.x + k * kThreads, c = v % kChannels;
+      if (v >= values || i0 + c >= I) continue;
+      const uint16_t* T = a.T_mid + ((int64_t)tile.expert * I + i0 + c) * G;  // row c % G of its block
+      const float* block = hs + v / G * G;
+      float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const float tj = __uint_as_float((uint32_t)T[j] << 16);
+      for (int j = 0; j < G; j += 8) {
+        const u32x4 t = *reinterpret_cast<const u32x4*>(T + j);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) h[t] = __builtin_fmaf(tj, hs[t][threadIdx.x >> 5][b + j], h[t]);
+        for (int i = 0; i < 4; ++i) {
+          s = __builtin_fmaf(__uint_as_float(t[i] << 16), block[j + 2 * i], s);
+          s = __builtin_fmaf(__uint_as_float(t[i] & 0xFFFF0000u), block[j + 2 * i + 1], s);
+        }
+      }
+      h[k] = s;
     }
   }
-  if (i0 + c >= I) return;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int m = 16 * t + (threadIdx.x >> 5);
-    if (m >= tile.count) continue;
-    const int64_t s = a.slots[tile.start + m];
-    uint16_t* o = a.h + s * I + i0 + c;
-    float v = h[t];
-    for (int p = 0; p < a.h_terms; ++p) {
-      const __bf16 bv = (__bf16)v;
-      o[p * (int64_t)a.M * a.topk * I] = __builtin_bit_cast(uint16_t, bv);
-      v -= (float)bv;
+  for (int k = 0; k < kEach; ++k) {
+    const int v = threadIdx.x + k * kThreads, m = v / kChannels, c = v % kChannels;
+    if (v >= values || i0 + c >= I) continue;
+    uint16_t* o = a.h + slot[m] * I + i0 + c;
+    float r = h[k];
+    for (int t = 0; t < a.terms; ++t) {
+      const __bf16 b = (__bf16)r;
+      o[t * ((int64_t)a.M * a.topk * I)] = __builtin_bit_cast(uint16_t, b);
+      r -= (float)b;
     }
   }
 }
 
 // ------------------------------------------------------------ down
 //
-// A workgroup owns 16 channels of y for all tokens and goes through all
-// tiles: the steps of all tiles form one sequence, of which every wave takes
-// a stretch.  Where a wave leaves a tile, it adds the tile's sums, times the
-// tokens' weights, to its own y in LDS; the waves' sums meet at the end.
-template <int FMT, int NT, int TERMS>
-__global__ __launch_bounds__(64 * kWaves) void down_kernel(MoeArgs a) {
-  __shared__ float ys[kWaves][kMoeTokens][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
-  const int64_t H = a.H, I = a.I;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t row = n0 + n < H ? n0 + n : H - 1;
-  for (int m = q; m < a.M; m += 4) ys[wave][m][n] = 0.0f;
-  // ys[wave] is this wave's alone; its lanes meet there in program order.
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  const int n_tiles = *a.n_tiles;
-  const int whole = (int)(I / kStep), steps = (int)((I + kStep - 1) / kStep);
-  const int64_t units = (int64_t)n_tiles * steps;
-  const int64_t u0 = units * wave / kWaves, u1 = units * (wave + 1) / kWaves;
-  const int64_t plane = (int64_t)a.M * a.topk * I;
-
-  Raw<FMT> w[1], nw[1];
-  auto load = [&](Raw<FMT>& to, int tile, int st) {
-    const int64_t r = (int64_t)a.tiles[tile].expert * H + row;
-    const uint8_t* cp = a.dn_codes + r * row_code_bytes<FMT>(I);
-    const uint8_t* sp = a.dn_scales + r * row_scale_bytes<FMT>(I);
-    if (st < whole) {
-      load_raw<FMT>(to, cp, sp, st, q);
-    } else {
-      load_raw_tail<FMT>(to, cp, sp, st, q, (int)I);
-    }
-  };
-  if (u0 < u1) {
-    int tile = (int)(u0 / steps), st = (int)(u0 % steps);
-    load(w[0], tile, st);
-    int64_t u = u0;
-    while (u < u1) {
-      const MoeTile info = a.tiles[tile];
-      const uint16_t* xp[NT];
-      f32x4 acc[1][NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        acc[0][t] = f32x4{0, 0, 0, 0};
-        xp[t] = a.h + (int64_t)a.slots[info.start + (16 * t + n < info.count ? 16 * t + n : 0)] * I;
-      }
-      // This tile's share of the stretch.
-      while (true) {
-        const bool last = st + 1 == steps;
-        const int tile2 = last ? tile + 1 : tile, st2 = last ? 0 : st + 1;
-        if (u + 1 < u1) load(nw[0], tile2, st2);
-        if (st < whole) {
-          step<FMT, 1, NT, TERMS, false>(acc, w, xp, plane, st, q, (int)I);
-        } else {
-          step<FMT, 1, NT, TERMS, true>(acc, w, xp, plane, st, q, (int)I);
-        }
-        w[0] = nw[0];
-        ++u;
-        tile = tile2;
-        st = st2;
-        if (last || u == u1) break;
-      }
-      const float gs = FMT == kNV ? a.dn_gs[info.expert] : 1.0f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = 16 * t + 4 * q + i;
-          if (m >= info.count) continue;
-          const int s = a.slots[info.start + m];
-          ys[wave][s / a.topk][n] += a.weights[s] * (FMT == kNV ? acc[0][t][i] * gs : acc[0][t][i]);
-        }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-  }
+// A workgroup owns 16 R WN channels of y for one tile; its results, one row per
+// slot, wait in memory for the slots' other experts.
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
+__global__ __launch_bounds__(64 * WN * WK, 2) void down_kernel(MoeArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  __shared__ int slot[16 * NT];
+  constexpr int kThreads = 64 * WN * WK, kChannels = 16 * R * WN;
+  if ((int)blockIdx.y >= *a.n_tiles) return;
+  const MoeTile tile = a.tiles[blockIdx.y];
+  const int n = threadIdx.x & 15, wn = (threadIdx.x >> 6) % WN;
+  const int64_t H = a.H, I = a.I, n0 = (int64_t)blockIdx.x * kChannels;
+  if ((int)threadIdx.x < tile.count) slot[threadIdx.x] = a.slots[tile.start + threadIdx.x];
+  const auto p = make_rows<FMT, R, D>(a.dn_codes, a.dn_scales, I, [&](int r) {
+    const int64_t i = n0 + 16 * (wn * R + r) + n;
+    return tile.expert * H + (i < H ? i : H - 1);
+  });
   __syncthreads();
-  for (int o = threadIdx.x; o < a.M * 16; o += 64 * kWaves) {
-    const int m = o >> 4, c = o & 15;
+  group_dot<FMT, R, D, NT, TERMS, SPREAD, WN, WK>(
+      lds, p, [&](int row) { return a.h + slot[row] * I; }, (int64_t)a.M * a.topk * I, tile.count, I);
+  const float gs = FMT == kNV ? a.dn_gs[tile.expert] : 1.0f;
+  for (int v = threadIdx.x; v < tile.count * kChannels; v += kThreads) {
+    const int m = v / kChannels, c = v % kChannels;
     if (n0 + c >= H) continue;
-    float v = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += ys[k][m][c];
-    const int64_t at = m * H + n0 + c;
-    if (a.bf16_out) {
-      reinterpret_cast<uint16_t*>(a.Y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
-    } else {
-      reinterpret_cast<float*>(a.Y)[at] = v;
-    }
+    float s = group_sum<R, WN, WK>(lds, c, m, tile.count);
+    if (FMT == kNV) s *= gs;
+    a.part[slot[m] * H + n0 + c] = s;
   }
 }
 
-template <int FMT, int NT, int TERMS>
-hipError_t go_gate_up(const MoeArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.I + 31) / 32), (unsigned)moe_max_tiles(a.M, a.topk, a.E));
-  hipLaunchKernelGGL((gate_up_kernel<FMT, NT, TERMS>), grid, dim3(64 * kWaves), 0, s, a);
-  return hipGetLastError();
+// ------------------------------------------------------------ weighted sum
+__global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
+  const int m = blockIdx.y;
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.H) return;
+  const float* part = a.part + (int64_t)m * a.topk * a.H + c;
+  float v = 0.0f;
+#pragma unroll 8
+  for (int j = 0; j < a.topk; ++j) v = __builtin_fmaf(a.weights[m * a.topk + j], part[j * a.H], v);
+  if (a.bf16_out) {
+    reinterpret_cast<uint16_t*>(a.Y)[m * a.H + c] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  } else {
+    reinterpret_cast<float*>(a.Y)[m * a.H + c] = v;
+  }
 }
 
-template <int FMT, int NT, int TERMS>
-hipError_t go_down(const MoeArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((down_kernel<FMT, NT, TERMS>), dim3((unsigned)((a.H + 15) / 16)), dim3(64 * kWaves), 0, s, a);
-  return hipGetLastError();
+template <int FMT, int NT, int TERMS, bool SPREAD, int WN, int WK>
+hipError_t go_gate_up(const MoeArgs& a, int max_tiles, hipStream_t s) {
+  const dim3 grid((unsigned)((a.I + 32 * WN - 1) / (32 * WN)), (unsigned)max_tiles);
+  constexpr int kRows = SPREAD ? 4 : 16 * NT;
+  const int rows = a.M < kRows ? a.M : kRows;
+  int64_t lds = lds_bytes<4, 1, NT, TERMS, WN, WK>(rows, a.H);
+  const int64_t hs = (int64_t)4 * rows * 32 * WN;
+  if (hs > lds) lds = hs;
+  return launch_lds(gate_up_kernel<FMT, NT, TERMS, SPREAD, WN, WK>, grid, 64 * WN * WK, lds, s, a);
 }
 
-template <int FMT, int NT>
-hipError_t go_experts(const MoeArgs& a, hipStream_t s) {
-  hipError_t e;
-  if (a.x.terms == 1) e = go_gate_up<FMT, NT, 1>(a, s);
-  else if (a.x.terms == 2) e = go_gate_up<FMT, NT, 2>(a, s);
-  else e = go_gate_up<FMT, NT, 3>(a, s);
-  if (e != hipSuccess) return e;
-  return a.h_terms == 2 ? go_down<FMT, NT, 2>(a, s) : go_down<FMT, NT, 3>(a, s);
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
+hipError_t go_down(const MoeArgs& a, int max_tiles, hipStream_t s) {
+  const dim3 grid((unsigned)((a.H + 16 * R * WN - 1) / (16 * R * WN)), (unsigned)max_tiles);
+  constexpr int kRows = SPREAD ? 4 : 16 * NT;
+  const int rows = a.M < kRows ? a.M : kRows;
+  return launch_lds(down_kernel<FMT, R, D, NT, TERMS, SPREAD, WN, WK>, grid, 64 * WN * WK,
+                    lds_bytes<R, D, NT, TERMS, WN, WK>(rows, a.I), s, a);
+}
+
+// Tokens per tile, by how many tokens an expert can expect: 4, 16 or 32.
+int tile_tokens(const MoeArgs& a) {
+  const float expect = (float)(a.M * a.topk) / a.E;
+  return a.M <= 4 || expect <= 2.0f ? 4 : a.M <= 16 || expect <= 12.0f ? 16 : 32;
+}
+
+template <int FMT, int TERMS>
+hipError_t go_gate_up_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
+  const int t = tile_tokens(a);
+  if (t == 4) return go_gate_up<FMT, 1, TERMS, true, 1, 8>(a, max_tiles, s);
+  if (t == 16) return go_gate_up<FMT, 1, TERMS, false, 2, 4>(a, max_tiles, s);
+  return go_gate_up<FMT, 2, TERMS, false, 4, 2>(a, max_tiles, s);
+}
+
+template <int FMT, int TERMS>
+hipError_t go_down_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
+  const int t = tile_tokens(a);
+  if (t == 4) return go_down<FMT, 2, 2, 1, TERMS, true, 1, 4>(a, max_tiles, s);
+  if (t == 16) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, max_tiles, s);
+  return go_down<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, max_tiles, s);
 }
 
 template <int FMT>
-hipError_t go_fmt(const MoeArgs& a, hipStream_t s) {
-  const int nt = moe_tile_nt(a.M, a.topk, a.E);
-  if (nt == 1) return go_experts<FMT, 1>(a, s);
-  if (nt == 2) return go_experts<FMT, 2>(a, s);
-  return go_experts<FMT, 4>(a, s);
+hipError_t go_experts(const MoeArgs& a, hipStream_t s) {
+  // No more tiles than slots, nor than experts and the tiles cut off full ones.
+  const int slots = a.M * a.topk, cut = (slots < a.E ? slots : a.E) + slots / tile_tokens(a);
+  const int max_tiles = slots < cut ? slots : cut;
+  hipError_t e = !a.T_in          ? go_gate_up_tiles<FMT, 1>(a, max_tiles, s)
+                 : a.terms == 2 ? go_gate_up_tiles<FMT, 2>(a, max_tiles, s)
+                                : go_gate_up_tiles<FMT, 3>(a, max_tiles, s);
+  if (e != hipSuccess) return e;
+  return a.terms == 2 ? go_down_tiles<FMT, 2>(a, max_tiles, s) : go_down_tiles<FMT, 3>(a, max_tiles, s);
 }
 
 }  // namespace
 
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(router_kernel, dim3((unsigned)((a.E + 15) / 16), (unsigned)((a.M + 15) / 16)),
-                     dim3(64 * kRouterWaves), 0, s, a);
+  const int router_tiles = (a.E + 15) / 16;
+  const int64_t split = a.T_in ? (a.H + 32 * kRouterWaves - 1) / (32 * kRouterWaves) : 0;
+  hipLaunchKernelGGL(router_kernel, dim3((unsigned)(router_tiles + split), (unsigned)((a.M + 15) / 16)),
+                     dim3(64 * kRouterWaves), 0, s, a, router_tiles);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int tokens = 16 * moe_tile_nt(a.M, a.topk, a.E);
+  const int tokens = tile_tokens(a);
   if (a.E <= 128) hipLaunchKernelGGL((route_kernel<2>), dim3(1), dim3(kRouteThreads), 0, s, a, tokens);
   else if (a.E <= 256) hipLaunchKernelGGL((route_kernel<4>), dim3(1), dim3(kRouteThreads), 0, s, a, tokens);
   else hipLaunchKernelGGL((route_kernel<16>), dim3(1), dim3(kRouteThreads), 0, s, a, tokens);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.fmt == kMX) return go_fmt<kMX>(a, s);
-  if (a.fmt == kNV) return go_fmt<kNV>(a, s);
-  return go_fmt<kINT>(a, s);
+  e = a.fmt == kMX ? go_experts<kMX>(a, s) : a.fmt == kNV ? go_experts<kNV>(a, s) : go_experts<kINT>(a, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((a.H + 255) / 256), (unsigned)a.M), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace wush

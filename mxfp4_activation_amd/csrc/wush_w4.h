@@ -51,8 +51,7 @@ struct MoeTile {
 
 struct MoeArgs {
   int fmt;
-  Planes x;                 // what gate and up multiply: X or the planes of T_in X
-  const uint16_t* X;        // bf16 [M], row stride ldx: what the router reads
+  const uint16_t* X;        // bf16 [M], row stride ldx
   int64_t ldx;
   const uint16_t* router;   // bf16 [E][H]
   const uint8_t* gu_codes;  // [E][2 I][H/2]: I gate rows, then I up rows
@@ -61,32 +60,24 @@ struct MoeArgs {
   const uint8_t* dn_codes;  // [E][H][I/2]
   const uint8_t* dn_scales;
   const float* dn_gs;
+  const uint16_t* T_in;     // bf16 [H/G][G][G] or null
   const uint16_t* T_mid;    // bf16 [E][I/G][G][G] or null
   int M, E, topk;           // M <= kMoeTokens
   int64_t H, I;
-  int renorm, h_terms;
+  int renorm, terms;        // terms: planes of T_in X and of h
   bool bf16_out;
   void* Y;                  // [M][H]
   int32_t* ids;             // [M][topk]
   float* weights;           // [M][topk]
   // Workspace.
+  uint16_t* xt;             // [terms][M][H], if T_in
   float* logits;            // [M][E]
-  uint16_t* h;              // [h_terms][M * topk][I]
+  uint16_t* h;              // [terms][M * topk][I]
+  float* part;              // [M * topk][H]
   int32_t* slots;           // [M * topk], grouped by expert
   int32_t* n_tiles;
-  MoeTile* tiles;           // [moe_max_tiles]
+  MoeTile* tiles;           // [M * topk]
 };
-
-// Token tiles (of 16) per MoeTile: experts that expect more than 12 tokens take
-// wider tiles, so that few are cut in two.
-inline int moe_tile_nt(int M, int topk, int E) {
-  const int expect = M * topk / E;
-  return expect > 24 ? 4 : expect > 8 ? 2 : 1;
-}
-inline int moe_max_tiles(int M, int topk, int E) {
-  const int slots = M * topk, tiles = (slots < E ? slots : E) + slots / (16 * moe_tile_nt(M, topk, E));
-  return tiles < slots ? tiles : slots;  // every tile holds a slot
-}
 
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s);
 

@@ -1,22 +1,31 @@
-// The wave-level product of a few activation rows with rows of 4-bit weights,
-// shared by the linear layer (wush_w4.hip) and the mixture of experts
-// (wush_moe.hip).  Device code only.
+// The product of a few activation rows with rows of 4-bit weights, shared by
+// the linear layer (wush_w4.hip) and the mixture of experts (wush_moe.hip).
+// Device code only.
 //
-// One wave multiplies R tiles of 16 weight rows with NT tiles of 16 tokens
-// on v_mfma_f32_16x16x32_bf16: A = activations (row m = token), B = weights
-// (column n = weight row), D[m][n] with m = 4 (lane / 16) + i, n = lane % 16.
-// A few tokens leave most of A's rows unused (row m of D depends on row m of A
-// alone, so unused rows hold copies of a valid token and are never stored);
-// the matrix cores are still far from the limit.  The limit is the weights'
-// way in, and behind it the vector instructions that turn codes into bf16.
+// v_mfma_f32_16x16x32_bf16 multiplies A = 16 tokens with B = 16 weight rows:
+// D[m][n] with m = 4 (lane / 16) + i, n = lane % 16.  A few tokens leave
+// most of A's rows unused (row m of D depends on row m of A alone, so unused rows
+// hold copies of a valid token and are never stored); the matrix cores are
+// still far from the limit.  The limit is the weights' way in, and behind it
+// the vector instructions that turn codes into bf16.
 //
-// A step is 128 elements of K: lane (q = lane / 16, n) loads the 16 code
-// bytes of row n, elements 32 q .. 32 q + 31, so the four lanes of a row read
-// 64 contiguous bytes.  A 4 x 4 transpose of dwords between the four
-// lane quarters (four lane-swap instructions) then leaves in dword g elements
-// 32 g + 8 q .. + 7: matrix instruction g covers exactly the group of 32
-// elements g of all 16 rows, and the activations are read in their natural
-// order.
+// A workgroup has WN x WK waves: wave (wn, wk) owns R tiles of 16 weight rows
+// and, of every chunk of K, its D steps of 128 elements.  R D = 4 units (16
+// rows x 128 elements, 1 KB of codes) are in registers while the next four
+// are on their way; the activations of a chunk come through LDS, where all waves
+// of the same wk read them, one chunk ahead.  (Read from global memory they
+// would share the weights' load counter, and each wait for them would drain the
+// weights in flight.)  The WK sums meet in LDS at the end.
+//
+// A unit: lane (q = lane / 16, n) loads the 16 code bytes of row n, elements
+// 32 q .. 32 q + 31, so the four lanes of a row read 64 contiguous bytes.
+// MXFP4 and NVFP4 apply their scales to the elements; matrix instruction j takes
+// elements 32 q + 8 j .. + 7 of every quarter q, and the activations from the
+// same places.  INT4 applies its scale to sums over one group: a 4 x 4 transpose
+// of dwords between the lane quarters (four lane-swap instructions) makes matrix
+// instruction j cover group j of all 16 rows, elements 32 j + 8 q .. + 7.  The
+// scales of four units come in one load, lane quarter u holding unit u's, and
+// three lane swaps hand them round.
 //
 // Exactness.  E2M1 * 2^e and E2M1 * E4M3 have at most 6 significant bits, and
 // the integers of INT4 have 4, so all of them are exact in bf16; the fp16
@@ -30,10 +39,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "wush_w4.h"
+
 namespace wush {
 namespace w4 {
 
-constexpr int kMX = 0, kNV = 1, kINT = 2, kBF = 3;  // kBF: bf16 weights (the router)
+constexpr int kMX = 0, kNV = 1, kINT = 2;
 constexpr int kStep = 128;                          // elements of K per step
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -61,67 +72,176 @@ __device__ __forceinline__ bf16x2 cvt_bf16(float a, float b) {
   return r;
 }
 
-// One lane's share of 16 rows x 128 elements as it is in memory.
-template <int FMT>
+// One lane's share of R row tiles x D steps, as it is in memory.  With four
+// units in all, lane quarter u holds the scales of unit u (row tile u / D, step
+// u % D); otherwise every lane holds every unit's.
+template <int FMT, int R, int D>
 struct Raw {
-  u32x4 c;   // 32 codes
-  u32x2 s;   // the row's scales of this step: 4 E8M0 bytes, 8 E4M3 bytes or 4 fp16
-};
-template <>
-struct Raw<kBF> {
-  u32x4 c[4];
+  static constexpr int kUnits = R * D;
+  static constexpr bool kShared = kUnits == 4;
+  u32x4 c[kUnits];
+  u32x2 s[kShared ? 1 : kUnits];  // 4 E8M0 bytes, 8 E4M3 bytes or 4 fp16
 };
 
 template <int FMT>
-__device__ __forceinline__ int64_t row_code_bytes(int64_t K) { return FMT == kBF ? 2 * K : K / 2; }
+__device__ __forceinline__ int64_t row_code_bytes(int64_t K) { return K / 2; }
 template <int FMT>
-__device__ __forceinline__ int64_t row_scale_bytes(int64_t K) {
-  return FMT == kMX ? K / 32 : FMT == kNV || FMT == kINT ? K / 16 : 0;
-}
+__device__ __forceinline__ int64_t row_scale_bytes(int64_t K) { return FMT == kMX ? K / 32 : K / 16; }
 
-// A whole step: cp and sp point at the lane's row, st counts steps.
 template <int FMT>
-__device__ __forceinline__ void load_raw(Raw<FMT>& w, const uint8_t* cp, const uint8_t* sp, int64_t st, int q) {
-  if constexpr (FMT == kBF) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) w.c[g] = load_unaligned<u32x4>(cp + 256 * st + 64 * g + 16 * q);
+__device__ __forceinline__ u32x2 load_scales(const uint8_t* sp, int64_t st) {
+  if constexpr (FMT == kMX) {
+    return u32x2{load_unaligned<uint32_t>(sp + 4 * st), 0};
   } else {
-    w.c = load_unaligned<u32x4>(cp + 64 * st + 16 * q);
-    if constexpr (FMT == kMX) {
-      w.s[0] = load_unaligned<uint32_t>(sp + 4 * st);
-      w.s[1] = 0;
-    } else {
-      w.s = load_unaligned<u32x2>(sp + 8 * st);
-    }
+    return load_unaligned<u32x2>(sp + 8 * st);
   }
 }
 
-// The last, partial step of a K that is no multiple of 128: nothing is read
-// past the row, and what is missing is zero.
-template <int FMT>
-__device__ __forceinline__ void load_raw_tail(Raw<FMT>& w, const uint8_t* cp, const uint8_t* sp, int64_t st, int q,
-                                              int K) {
-  const int left = K - (int)st * kStep;  // 16 .. 112 elements
-  if constexpr (FMT == kBF) {
+// Row pointers of a wave's R tiles.
+template <int FMT, int R, int D>
+struct Rows {
+  const uint8_t* cp[R];  // the lane's row of each tile, at its 16 bytes of step 0
+  const uint8_t* sp[Raw<FMT, R, D>::kShared ? 1 : R];
+};
+
+// row(t): index of the weight row that the lane's column of row tile t stands for.
+template <int FMT, int R, int D, typename F>
+__device__ __forceinline__ Rows<FMT, R, D> make_rows(const uint8_t* codes, const uint8_t* scales, int64_t K, F row) {
+  const int q = (threadIdx.x & 63) >> 4;
+  Rows<FMT, R, D> o;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      w.c[g] = u32x4{0, 0, 0, 0};
-      if (32 * g + 8 * q + 8 <= left) w.c[g] = load_unaligned<u32x4>(cp + 256 * st + 64 * g + 16 * q);
-    }
+  for (int r = 0; r < R; ++r) o.cp[r] = codes + row(r) * row_code_bytes<FMT>(K) + 16 * q;
+  if constexpr (Raw<FMT, R, D>::kShared) {
+    o.sp[0] = scales + row(q / D) * row_scale_bytes<FMT>(K) + (FMT == kMX ? 4 : 8) * (q % D);
   } else {
-    w.c = u32x4{0, 0, 0, 0};
-    if (32 * q + 32 <= left) {
-      w.c = load_unaligned<u32x4>(cp + 64 * st + 16 * q);
-    } else if (32 * q + 16 <= left) {
-      const u32x2 h = load_unaligned<u32x2>(cp + 64 * st + 16 * q);
-      w.c[0] = h[0];
-      w.c[1] = h[1];
-    }
-    w.s = u32x2{0, 0};
-    const int bytes = FMT == kMX ? left / 32 : left / 16;
 #pragma unroll
-    for (int b = 0; b < 7; ++b)
-      if (b < bytes) w.s[b / 4] |= (uint32_t)sp[(FMT == kMX ? 4 : 8) * st + b] << (8 * (b % 4));
+    for (int r = 0; r < R; ++r) o.sp[r] = scales + row(r) * row_scale_bytes<FMT>(K);
+  }
+  return o;
+}
+
+// D whole steps from step st.
+template <int FMT, int R, int D>
+__device__ __forceinline__ void load_raw(Raw<FMT, R, D>& w, const Rows<FMT, R, D>& p, int64_t st) {
+  using RawT = Raw<FMT, R, D>;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 0; d < D; ++d) w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d));
+  if constexpr (RawT::kShared) {
+    w.s[0] = load_scales<FMT>(p.sp[0], st);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < D; ++d) w.s[r * D + d] = load_scales<FMT>(p.sp[r], st + d);
+  }
+}
+
+// D steps of which some reach past K: nothing is read past a row, and what is
+// missing is zero.  From K = 128 on, the loads depend on no condition (their addresses
+// do), so that fix_tail can be left until the weights are needed.
+template <int FMT, int R, int D>
+__device__ __forceinline__ void load_raw_tail(Raw<FMT, R, D>& w, const Rows<FMT, R, D>& p, int64_t st, int64_t K) {
+  using RawT = Raw<FMT, R, D>;
+  constexpr int kStepBytes = FMT == kMX ? 4 : 8;
+  const int q = (threadIdx.x & 63) >> 4;
+  const int64_t row_scales = row_scale_bytes<FMT>(K);
+  if (K >= kStep) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        // The lane's 16 bytes, or the row's last 16 if they reach past it.
+        const int64_t last = K / 2 - 16 - 16 * q, at = 64 * (st + d);
+        w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + (at < last ? at : last));
+      }
+    // sp points at this step's bytes; not past the row's last kStepBytes.
+    auto back = [&](int64_t step) {
+      const int64_t over = kStepBytes * (step + 1) - row_scales;
+      return over > 0 ? over : 0;
+    };
+    if constexpr (RawT::kShared) {
+      w.s[0] = load_scales<FMT>(p.sp[0] - back(st + q % D), st);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int d = 0; d < D; ++d) w.s[r * D + d] = load_scales<FMT>(p.sp[r] - back(st + d), st + d);
+    }
+    return;
+  }
+  // One partial step is all there is.
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int64_t k = (st + d) * kStep + 32 * q;
+      u32x4 c = {0, 0, 0, 0};
+      if (k + 32 <= K) {
+        c = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d));
+      } else if (FMT == kNV && k + 16 <= K) {
+        const u32x2 h = load_unaligned<u32x2>(p.cp[r] + 64 * (st + d));
+        c[0] = h[0];
+        c[1] = h[1];
+      }
+      w.c[r * D + d] = c;
+    }
+  auto scales = [&](const uint8_t* sp, int64_t first, int64_t step) {
+    u32x2 s = {0, 0};
+    if (step == 0) {
+      for (int b = 0; b < row_scales; ++b) {
+        const uint32_t v = (uint32_t)sp[kStepBytes * first + b] << (8 * (b % 4));
+        if (b < 4) {
+          s[0] |= v;
+        } else {
+          s[1] |= v;
+        }
+      }
+    }
+    return s;
+  };
+  if constexpr (RawT::kShared) {
+    w.s[0] = scales(p.sp[0] - kStepBytes * (q % D), st, st + q % D);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < D; ++d) w.s[r * D + d] = scales(p.sp[r], st + d, st + d);
+  }
+}
+
+// What load_raw_tail took from before its place: shifted there, zero behind it.
+template <int FMT, int R, int D>
+__device__ __forceinline__ void fix_tail(Raw<FMT, R, D>& w, int64_t st, int64_t K) {
+  using RawT = Raw<FMT, R, D>;
+  constexpr int kStepBytes = FMT == kMX ? 4 : 8;
+  if (K < kStep) return;
+  const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int64_t k = (st + d) * kStep + 32 * q;
+      u32x4& c = w.c[r * D + d];
+      const bool half = FMT == kNV && k + 16 == K;
+      if (half) c = u32x4{c[2], c[3], 0, 0};
+      if (k + 32 > K && !half) c = u32x4{0, 0, 0, 0};
+    }
+  auto fix = [&](u32x2 s, int64_t step) {
+    const int64_t over = kStepBytes * (step + 1) - row_scale_bytes<FMT>(K);
+    uint64_t v = ((uint64_t)s[1] << 32) | s[0];
+    if (over >= kStepBytes) v = 0;
+    else if (over > 0) v >>= 8 * over;
+    return u32x2{(uint32_t)v, (uint32_t)(v >> 32)};
+  };
+  if constexpr (RawT::kShared) {
+    w.s[0] = fix(w.s[0], st + q % D);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < D; ++d) w.s[r * D + d] = fix(w.s[r * D + d], st + d);
   }
 }
 
@@ -134,39 +254,44 @@ __device__ __forceinline__ void transpose4(u32x4& c) {
   c = u32x4{x[0], x[1], y[0], y[1]};
 }
 
-// What group g's codes are multiplied with before (MXFP4, NVFP4) or after
-// (INT4) the matrix instruction.
+// v of lane quarter u, in all quarters, as o[u].
+__device__ __forceinline__ void hand_round(uint32_t v, uint32_t (&o)[4]) {
+  const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const auto x = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+  const auto y = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+  o[0] = x[0];
+  o[1] = x[1];
+  o[2] = y[0];
+  o[3] = y[1];
+}
+
+// What dword j of a lane's codes is multiplied with before (MXFP4, NVFP4) or
+// after (INT4) the matrix instruction; s: the scales of the lane's row.
 template <int FMT>
-__device__ __forceinline__ float group_scale(const Raw<FMT>& w, int g, int q) {
+__device__ __forceinline__ float code_scale(const u32x2& s, int j, int q) {
   if constexpr (FMT == kMX) {
-    // The E8M0 byte is an fp32 exponent; the conversion reads nothing else
-    // of its scale operand, and takes 0 for 2^-127 and 255 for NaN.
-    return __uint_as_float(((w.s[0] >> (8 * g)) & 0xFFu) << 23);
+    // The E8M0 byte of group q is an fp32 exponent; the conversion reads
+    // nothing else of its scale operand, and takes 0 for 2^-127 and 255 for NaN.
+    return __uint_as_float(((s[0] >> (8 * q)) & 0xFFu) << 23);
   } else if constexpr (FMT == kNV) {
-    // Elements 8 q .. 8 q + 7 of the 32 are in scale group 2 g + q / 2.
-    const uint32_t v = w.s[g >> 1] >> (8 * (q >> 1));
-    return g & 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 2) : __builtin_amdgcn_cvt_f32_fp8(v, 0);
-  } else if constexpr (FMT == kINT) {
-    return __half2float(__ushort_as_half((uint16_t)(w.s[g >> 1] >> (16 * (g & 1)))));
+    // Dwords 0 and 1 are scale group 2 q, 2 and 3 are 2 q + 1.
+    const uint32_t v = (q < 2 ? s[0] : s[1]) >> (16 * (q & 1));
+    return j < 2 ? __builtin_amdgcn_cvt_f32_fp8(v, 0) : __builtin_amdgcn_cvt_f32_fp8(v, 1);
   } else {
-    return 1.0f;
+    return __half2float(__ushort_as_half((uint16_t)(s[j >> 1] >> (16 * (j & 1)))));
   }
 }
 
-// Group g of the (transposed) codes as 8 bf16 weights; INT4 as code + 8.
+// Eight codes of one group as bf16 weights; INT4 as code + 8.
 template <int FMT>
-__device__ __forceinline__ bf16x8 expand(const Raw<FMT>& w, int g, float s) {
+__device__ __forceinline__ bf16x8 expand(uint32_t d, float s) {
   u32x4 r;
-  if constexpr (FMT == kBF) {
-    r = w.c[g];
-  } else if constexpr (FMT == kMX) {
-    const uint32_t d = w.c[g];
+  if constexpr (FMT == kMX) {
     r[0] = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0));
     r[1] = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1));
     r[2] = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2));
     r[3] = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3));
   } else if constexpr (FMT == kNV) {
-    const uint32_t d = w.c[g];
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 0);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 1);
     const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d, 1.0f, 2);
@@ -179,7 +304,7 @@ __device__ __forceinline__ bf16x8 expand(const Raw<FMT>& w, int g, float s) {
     // u = code + 8 in 0 .. 15 is, as an E4M3 byte, the number u * 2^-9 (up to
     // 7 as a subnormal, from 8 on with exponent 1); scaled by 2^9 the
     // conversion gives u.
-    const uint32_t u = w.c[g] ^ 0x88888888u;
+    const uint32_t u = d ^ 0x88888888u;
     const uint32_t lo = u & 0x0F0F0F0Fu, hi = (u >> 4) & 0x0F0F0F0Fu;
     const uint32_t p0 = __builtin_amdgcn_perm(hi, lo, 0x05010400u);  // elements 0 .. 3
     const uint32_t p1 = __builtin_amdgcn_perm(hi, lo, 0x07030602u);  // elements 4 .. 7
@@ -191,96 +316,364 @@ __device__ __forceinline__ bf16x8 expand(const Raw<FMT>& w, int g, float s) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
-// One step's products.  xp[t] points at the lane's token row of token tile t;
-// TAIL: groups (of 8 elements) past K read nothing and count as zero.
-template <int FMT, int R, int NT, int TERMS, bool TAIL>
-__device__ __forceinline__ void step(f32x4 (&acc)[R][NT], Raw<FMT> (&w)[R], const uint16_t* const (&xp)[NT],
-                                     int64_t plane, int64_t st, int q, int K) {
-  bf16x8 x[4][NT][TERMS];
+// The activations of a chunk in LDS: lines of bf16, one line per (term, token
+// row).  One copy instruction writes a piece of 1 KB (64 lanes x 16 bytes).  Lines
+// of 512 elements or more are whole pieces and 16 bytes more, which put the 16
+// rows that a quarter wave reads at once on 16 different 16-byte groups of
+// banks.  Two lines of 256 elements share a piece; there the second one's
+// elements sit at their index ^ 64, for the same end.
+template <int WIDTH>
+struct Lines {
+  static constexpr int kPerPiece = WIDTH >= 512 ? 1 : 2;            // lines per piece
+  static constexpr int kPieces = WIDTH >= 512 ? WIDTH / 512 : 1;    // pieces per line
+  static constexpr int kStride = WIDTH >= 512 ? WIDTH + 8 : 512 + 8;  // elements per kPerPiece lines
+  static_assert(WIDTH == 256 || WIDTH % 512 == 0, "a line is half a piece or whole pieces");
+  static __host__ __device__ __forceinline__ int at(int line) {
+    return kPerPiece == 1 ? line * kStride : line / 2 * kStride + line % 2 * WIDTH;
+  }
+  static __device__ __forceinline__ int flip(int line) { return kPerPiece == 1 ? 0 : line % 2 * 64; }
+  static __host__ __device__ __forceinline__ int groups(int lines) { return (lines + kPerPiece - 1) / kPerPiece; }
+};
+
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
+typedef const __attribute__((address_space(1))) uint16_t glb_u16;
+
+// Global-to-LDS copy of 16 bytes per lane to LDS byte address dst (uniform;
+// lane l writes at dst + 16 l), outside the compiler's view: it would wait for
+// every copy in flight before any LDS read.  The copy takes its LDS base from
+// M0, which nothing else in these kernels uses.  The statement has no outputs.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16(glb_u16* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// This wave's first copies have landed, given that at least N loads of
+// weights were requested after them, and so have the others'.
+template <int N>
+__device__ __forceinline__ void arrive() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// All of this wave's LDS reads are done, then the workgroup meets.  Loads
+// and copies in flight stay in flight.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Where a lane reads its activations: of dword (MXFP4, NVFP4) or group (INT4) j
+// of a step at x + at[j / 2] + kXJ * j.
+template <int FMT>
+constexpr int kXJ = FMT == kINT ? 32 : 8;
+struct XAt {
+  int at[2];
+};
+
+// acc += the wave's D steps.  x: the wave's first step in line 0 of the chunk; xo[t][p]:
+// where the lane reads term p of its row of token tile t.
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[R][NT], Raw<FMT, R, D>& w, const uint16_t* x,
+                                         const XAt (&xo)[NT][TERMS]) {
+  const int q = (threadIdx.x & 63) >> 4;
+  u32x2 sc[R * D];
+  if constexpr (Raw<FMT, R, D>::kShared) {
+    uint32_t lo[4], hi[4] = {0, 0, 0, 0};
+    hand_round(w.s[0][0], lo);
+    if constexpr (FMT != kMX) hand_round(w.s[0][1], hi);
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
+    for (int u = 0; u < 4; ++u) sc[u] = u32x2{lo[u], hi[u]};
+  } else {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int u = 0; u < R * D; ++u) sc[u] = w.s[u];
+  }
+  if constexpr (FMT == kINT) {
 #pragma unroll
-      for (int p = 0; p < TERMS; ++p) {
-        const int64_t k = st * kStep + 32 * g + 8 * q;
-        u32x4 v = {0, 0, 0, 0};
-        if (!TAIL || k + 8 <= K) v = *reinterpret_cast<const u32x4*>(xp[t] + p * plane + k);
-        x[g][t][p] = __builtin_bit_cast(bf16x8, v);
-      }
-  if constexpr (FMT != kBF) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) transpose4(w[r].c);
+    for (int u = 0; u < R * D; ++u) transpose4(w.c[u]);
   }
   // INT4's codes come in as code + 8: the group's sum starts at
   // -8 sum x, which one more matrix instruction with a constant -8 gives in
   // every column.
   const uint32_t m8 = 0xC100C100u;  // bf16 -8, twice
   const bf16x8 minus8 = __builtin_bit_cast(bf16x8, (u32x4{m8, m8, m8, m8}));
+  bf16x8 a[NT][TERMS], next[NT][TERMS];
+  auto load_a = [&](bf16x8 (&to)[NT][TERMS], int i) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    f32x4 init[NT];
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int p = 0; p < TERMS; ++p)
+        to[t][p] = *reinterpret_cast<const bf16x8*>(x + xo[t][p].at[i % 4 / 2] + i / 4 * kStep + kXJ<FMT> * (i % 4));
+  };
+  load_a(a, 0);
+#pragma unroll
+  for (int i = 0; i < 4 * D; ++i) {  // dword or group j of step d
+    const int d = i / 4, j = i % 4;
+    if (i + 1 < 4 * D) load_a(next, i + 1);
     if constexpr (FMT == kINT) {
+      f32x4 init[NT], sum[R][NT];
+      float sc1[R];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         init[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int p = 0; p < TERMS; ++p)
-          init[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[g][t][p], minus8, init[t], 0, 0, 0);
+          init[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][p], minus8, init[t], 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        sc1[r] = code_scale<FMT>(sc[r * D + d], j, q);
+        const bf16x8 b = expand<FMT>(w.c[r * D + d][j], 0.0f);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          sum[r][t] = init[t];
+#pragma unroll
+          for (int p = 0; p < TERMS; ++p)
+            sum[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][p], b, sum[r][t], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < (SPREAD ? 1 : 4); ++k) acc[r][t][k] = __builtin_fmaf(sc1[r], sum[r][t][k], acc[r][t][k]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bf16x8 b = expand<FMT>(w.c[r * D + d][j], code_scale<FMT>(sc[r * D + d], j, q));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int p = 0; p < TERMS; ++p)
+            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][p], b, acc[r][t], 0, 0, 0);
       }
     }
+    // Expanding more than one dword ahead costs registers, and with them waves.
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float s = group_scale<FMT>(w[r], g, q);
-      const bf16x8 b = expand<FMT>(w[r], g, s);
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f32x4 c = FMT == kINT ? init[t] : acc[r][t];
+      for (int p = 0; p < TERMS; ++p) a[t][p] = next[t][p];
+  }
+  if constexpr (FMT == kINT) {
+    // The sums are wanted here: left to itself the compiler moves the scales'
+    // multiplications behind the branches that follow, and keeps every group's sum
+    // until then.
 #pragma unroll
-        for (int p = 0; p < TERMS; ++p) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[g][t][p], b, c, 0, 0, 0);
-        if constexpr (FMT == kINT) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(s, c[i], acc[r][t][i]);
-        } else {
-          acc[r][t] = c;
+      for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(acc[r][t]));
+  }
+}
+
+constexpr int kBuffers = 3;  // activation chunks in LDS
+
+// LDS of one workgroup in bytes: the activation buffers, or the sums that meet at
+// the end, whichever is more.
+template <int R, int D, int NT, int TERMS, int WN, int WK>
+inline int64_t lds_bytes(int rows, int64_t K) {
+  constexpr int kWidth = WK * D * kStep;
+  const int64_t chunks = (K + kWidth - 1) / kWidth;
+  const int64_t x = (chunks < kBuffers ? chunks : kBuffers) * 2 * Lines<kWidth>::groups(TERMS * rows) *
+                    Lines<kWidth>::kStride;
+  const int64_t red = 4 * (int64_t)WN * WK * R * 16 * rows;
+  return x > red ? x : red;
+}
+
+// The workgroup's product of `rows` activation rows (at most 16 NT, or 4 where
+// SPREAD) with its 16 R WN weight rows over all of K; wave wk * WN + wn takes
+// its row tiles from p.  src(row): pointer to term 0 of an activation row; terms
+// are `plane` elements apart.  Afterwards group_sum gives the results.
+//
+// SPREAD: up to four tokens stand in rows 0, 4, 8 and 12 of A, so that each
+// lane holds one result in the first component of D and INT4's scales cost one
+// multiplication per instruction rather than four.
+//
+// Order of a wave's requests: activations of chunk c + 1, weights of chunk c;
+// those of one chunk are in flight while the one before is multiplied.  Loads
+// complete in order, so a wave that has chunk c's weights knows that its
+// copies of chunk c + 1 have landed, and the barrier after chunk c tells the
+// others.
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK, typename F>
+__device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& p, F src, int64_t plane, int rows,
+                                          int64_t K) {
+  constexpr int kSteps = WK * D, kWidth = kSteps * kStep, kWaves = WN * WK;
+  static_assert(!SPREAD || NT == 1, "a spread tile is one tile");
+  using Ln = Lines<kWidth>;
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wk = wave / WN;
+  const int groups = Ln::groups(TERMS * rows), buffer = groups * Ln::kStride;
+  const int chunks = (int)((K + kWidth - 1) / kWidth);
+  const uint32_t base = (uint32_t)(uintptr_t)(lds_u16*)lds;
+
+  f32x4 acc[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+  XAt xo[NT][TERMS];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) {
+      const int row = SPREAD ? n >> 2 : 16 * t + n;
+      const int line = i * rows + (row < rows ? row : 0), f = Ln::flip(line);
+      if (FMT == kINT) {  // element 32 j + 8 q, j = 0 .. 3
+        xo[t][i].at[0] = Ln::at(line) + 8 * q + f;
+        xo[t][i].at[1] = Ln::at(line) + 8 * q - f;
+      } else {  // element 32 q + 8 j
+        xo[t][i].at[0] = xo[t][i].at[1] = Ln::at(line) + ((32 * q) ^ f);
+      }
+    }
+
+  // Elements past K are copies of the row's first ones: their weights are zero.
+  auto copy_x = [&](int c) {
+    const int total = groups * Ln::kPieces;
+    for (int i = wave; i < total; i += kWaves) {
+      const int group = i / Ln::kPieces, piece = i % Ln::kPieces;
+      const int e = piece * 512 + lane * 8;  // element of the group
+      int line = group * Ln::kPerPiece, pos = e;
+      if (Ln::kPerPiece > 1) {
+        if (line + e / kWidth < TERMS * rows) line += e / kWidth;
+        pos = e % kWidth ^ Ln::flip(e / kWidth);
+      }
+      const int t = TERMS == 1 ? 0 : line / rows, row = line - t * rows;
+      int64_t k = (int64_t)c * kWidth + pos;
+      k = k + 8 <= K ? k : 0;
+      copy16((glb_u16*)(src(row) + t * plane + k),
+             __builtin_amdgcn_readfirstlane(base + 2 * (c % kBuffers * buffer + group * Ln::kStride + piece * 512)));
+    }
+  };
+
+  const int full = (int)(K / kWidth);
+  const int64_t step0 = wk * D;
+  const bool tail = full < chunks && ((int64_t)full * kSteps + step0) * kStep < K;  // this wave has a part of it
+  const uint16_t* xw = lds + step0 * kStep;
+  Raw<FMT, R, D> wt;
+  if (tail) load_raw_tail(wt, p, (int64_t)full * kSteps + step0, K);
+  copy_x(0);
+  if (full > 0) {
+    // Two sets of registers in turn, and no load on a condition inside the loop:
+    // the compiler counts what is in flight and waits for no more than it
+    // needs.
+    Raw<FMT, R, D> w0, w1;
+    auto load = [&](Raw<FMT, R, D>& to, int c) { load_raw(to, p, (int64_t)c * kSteps + step0); };
+    auto dot = [&](Raw<FMT, R, D>& w, int c) {
+      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, xw + (c % kBuffers) * buffer, xo);
+      meet();
+    };
+    if (chunks > 1) copy_x(1);
+    load(w0, 0);
+    int c = 0;
+    if (full == 1) {
+      arrive<R * D>();
+    } else {
+      if (chunks > 2) copy_x(2);
+      load(w1, 1);
+      arrive<2 * R * D>();
+      for (; c + 2 < full; c += 2) {
+        dot(w0, c);
+        if (c + 3 < chunks) copy_x(c + 3);
+        load(w0, c + 2);
+        dot(w1, c + 1);
+        if (c + 3 >= full) {
+          c += 2;
+          break;
         }
+        if (c + 4 < chunks) copy_x(c + 4);
+        load(w1, c + 3);
+      }
+      // c is full - 2 with w1 loaded, or full - 1 without.
+      if (c + 1 < full) {
+        dot(w0, c);
+        dot(w1, c + 1);
+        c = full;
+      }
+    }
+    if (c < full) dot(w0, c);
+  } else {
+    arrive<0>();
+  }
+  if (full < chunks) {
+    if (tail) {
+      fix_tail(wt, (int64_t)full * kSteps + step0, K);
+      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, wt, xw + (full % kBuffers) * buffer, xo);
+    }
+    meet();
+  }
+  float* red = reinterpret_cast<float*>(lds) + wave * (R * 16 * rows);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < (SPREAD ? 1 : 4); ++i) {
+        const int m = SPREAD ? q : 16 * t + 4 * q + i;
+        if (m < rows) red[(r * rows + m) * 16 + n] = acc[r][t][i];
+      }
+  __syncthreads();
+}
+
+// Sum over wk of the product for weight row c (of 16 R WN) and token m.
+template <int R, int WN, int WK>
+__device__ __forceinline__ float group_sum(const uint16_t* lds, int c, int m, int rows) {
+  const float* red = reinterpret_cast<const float*>(lds) + ((c >> 4) * rows + m) * 16 + (c & 15);
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < WK; ++k) v += red[k * (WN * R * 16 * rows)];
+  return v;
+}
+
+// X' = T x per block of G channels in fp32, kept as a sum of bf16 planes:
+// y = y0 + y1 (+ y2), each the rounding of what the planes before it left.
+// Two planes hold 16 bits of y, three hold all 24.  One wave: 32 channels
+// (panel) of 16 tokens from m0.
+__device__ __forceinline__ void split_panel(const SplitArgs& a, int64_t panel, int64_t m0) {
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int64_t k0 = panel * 32, K = a.K;
+  const int64_t mx = m0 + n < a.M ? m0 + n : a.M - 1;
+  const uint16_t* x = a.X + mx * a.ldx + k0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    u32x4 av = {0, 0, 0, 0}, bv = {0, 0, 0, 0};
+    if (a.G == 32) {
+      av = *reinterpret_cast<const u32x4*>(x + 8 * q);
+      bv = *reinterpret_cast<const u32x4*>(a.T + panel * 1024 + (16 * h + n) * 32 + 8 * q);
+    } else {
+      // G = 16: the block fills half of the instruction's 32 columns.
+      if (k0 + 16 * h >= K) break;
+      if (q < 2) {
+        av = *reinterpret_cast<const u32x4*>(x + 16 * h + 8 * q);
+        bv = *reinterpret_cast<const u32x4*>(a.T + (2 * panel + h) * 256 + n * 16 + 8 * q);
+      }
+    }
+    const f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av),
+                                                            __builtin_bit_cast(bf16x8, bv), f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + 4 * q + i;
+      if (m >= a.M) continue;
+      float v = y[i];
+      uint16_t* o = a.out + m * K + k0 + 16 * h + n;
+      for (int t = 0; t < a.terms; ++t) {
+        const __bf16 b = (__bf16)v;
+        o[t * a.M * K] = __builtin_bit_cast(uint16_t, b);
+        v -= (float)b;
       }
     }
   }
 }
 
-// acc += the product over steps first, first + every, ... below n_steps
-// (ceil(K / 128)).  The next step's weights are on their way while this one's
-// are multiplied.
-template <int FMT, int R, int NT, int TERMS>
-__device__ __forceinline__ void wave_dot(f32x4 (&acc)[R][NT], const uint8_t* const (&cp)[R],
-                                         const uint8_t* const (&sp)[R], const uint16_t* const (&xp)[NT],
-                                         int64_t plane, int K, int first, int every) {
-  const int q = (threadIdx.x & 63) >> 4;
-  const int whole = K / kStep;
-  Raw<FMT> w[R];
-  int st = first;
-  if (st < whole) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) load_raw<FMT>(w[r], cp[r], sp[r], st, q);
+// A launch with `lds` bytes of dynamic LDS (beyond 64 KB it has to be asked for).
+template <typename Kernel, typename Args>
+inline hipError_t launch_lds(Kernel kernel, dim3 grid, int threads, int64_t lds, hipStream_t s, const Args& a) {
+  constexpr int64_t kLds = 163840;
+  if (lds > kLds) return hipErrorInvalidConfiguration;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
   }
-  while (st < whole) {
-    Raw<FMT> nw[R];
-    const int nx = st + every;
-    // The last turn loads its own step once more, rather than branch.
-    const int ld = nx < whole ? nx : st;
-#pragma unroll
-    for (int r = 0; r < R; ++r) load_raw<FMT>(nw[r], cp[r], sp[r], ld, q);
-    step<FMT, R, NT, TERMS, false>(acc, w, xp, plane, st, q, K);
-#pragma unroll
-    for (int r = 0; r < R; ++r) w[r] = nw[r];
-    st = nx;
-  }
-  if (st == whole && whole * kStep < K) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) load_raw_tail<FMT>(w[r], cp[r], sp[r], st, q, K);
-    step<FMT, R, NT, TERMS, true>(acc, w, xp, plane, st, q, K);
-  }
+  hipLaunchKernelGGL(kernel, grid, dim3(threads), (unsigned)lds, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace w4
