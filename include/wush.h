@@ -357,8 +357,8 @@ wush_status wush_f64_to_bf16(const double* src, int64_t n, void* dst, hipStream_
  *   codes u8 [N][K/2], 8-byte aligned; scales [N][K/G] (fp16 for INT4).
  *   global_scale: device fp32, NVFP4 only (wush_nvfp4_global_scale).
  *   Y: [M][N] fp32 or bf16 (out_type as in wush_gemm_mxfp4).
- * K is a positive multiple of G; any M and N >= 0 (0 is a no-op), M up to
- * about a million.  It is meant for few tokens: from about a hundred on,
+ * K is a positive multiple of G, at most 2^27; any M and N >= 0 (0 is a
+ * no-op), M up to about a million.  It is meant for few tokens: from about a hundred on,
  * quantized activations and wush_gemm_mxfp4 are faster.
  * workspace: needed with T only. */
 wush_status wush_linear_w4(int fmt, const void* X, int64_t ldx, const void* T, const void* codes, const void* scales,

@@ -45,6 +45,7 @@ uint64_t scale_bytes(int fmt, int64_t rows, int64_t K) {
 }
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
+constexpr int64_t kMaxK = (int64_t)1 << 27;
 
 wush_status check_fmt(int fmt, int out_type) {
   if (fmt != wush::kMXFP4 && fmt != wush::kNVFP4 && fmt != wush::kINT4)
@@ -54,8 +55,8 @@ wush_status check_fmt(int fmt, int out_type) {
 }
 
 wush_status check_width(const char* name, int64_t K, int fmt) {
-  if (K <= 0 || K > kMaxDim || K % group_of(fmt) != 0)
-    return fail(WUSH_EINVAL, "%s must be a positive multiple of %d, at most 2^30 (got %lld)", name, group_of(fmt),
+  if (K <= 0 || K > kMaxK || K % group_of(fmt) != 0)
+    return fail(WUSH_EINVAL, "%s must be a positive multiple of %d, at most 2^27 (got %lld)", name, group_of(fmt),
                 (long long)K);
   return WUSH_OK;
 }
@@ -93,7 +94,7 @@ wush_status launched(hipError_t e) {
 int64_t moe_chunk(int64_t M) { return M < wush::kMoeTokens ? M : wush::kMoeTokens; }
 
 struct MoeWorkspace {
-  uint64_t planes, h, part, logits, slots, n_tiles, tiles, total;
+  uint64_t planes, h, part, logits, n_tiles, tiles, total;
 };
 
 MoeWorkspace moe_workspace(int64_t M, int64_t E, int topk, int64_t H, int64_t I, bool transform, int out_type) {
@@ -103,8 +104,7 @@ MoeWorkspace moe_workspace(int64_t M, int64_t E, int topk, int64_t H, int64_t I,
   w.h = w.planes + (transform ? round16(terms * c * H * 2) : 0);
   w.part = w.h + round16(terms * slots * I * 2);
   w.logits = w.part + round16(slots * H * 4);
-  w.slots = w.logits + round16(c * E * 4);
-  w.n_tiles = w.slots + round16(slots * 4);
+  w.n_tiles = w.logits + round16(c * E * 4);
   w.tiles = w.n_tiles + 16;
   // A tile holds at least one slot.
   w.total = w.tiles + slots * sizeof(wush::MoeTile);
@@ -126,7 +126,7 @@ wush_status check_moe_shape(int64_t M, int64_t E, int topk, int64_t H, int64_t I
 extern "C" {
 
 int64_t wush_linear_w4_workspace(int64_t M, int64_t K, int out_type) {
-  if (M <= 0 || K <= 0 || K > kMaxDim || M > INT64_MAX / 8 / K) return 0;
+  if (M <= 0 || K <= 0 || K > kMaxK || M > INT64_MAX / 8 / K) return 0;
   return (int64_t)(2u * (uint64_t)terms_of(out_type) * (uint64_t)M * (uint64_t)K);
 }
 
@@ -277,7 +277,6 @@ wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router,
   a.h = reinterpret_cast<uint16_t*>(ws + w.h);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.logits = reinterpret_cast<float*>(ws + w.logits);
-  a.slots = reinterpret_cast<int32_t*>(ws + w.slots);
   a.n_tiles = reinterpret_cast<int32_t*>(ws + w.n_tiles);
   a.tiles = reinterpret_cast<wush::MoeTile*>(ws + w.tiles);
   for (int64_t m0 = 0; m0 < M; m0 += wush::kMoeTokens) {
@@ -295,7 +294,7 @@ wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router,
 int64_t wush_token_logprobs_workspace(int64_t R, int64_t V, int logit_type, int top) {
   if (R <= 0 || V <= 0 || V > INT32_MAX || logit_type < 0 || logit_type > 2 || top < 0 || top > wush::kLogprobMaxTop)
     return 0;
-  const int64_t s = wush::logprob_splits(R, V, logit_type);
+  const int64_t s = wush::logprob_plan(R, V).splits;
   return s == 1 ? 0 : R * s * (16 + 8 * (int64_t)top);
 }
 
@@ -346,7 +345,9 @@ wush_status wush_token_logprobs(const void* logits, int logit_type, int64_t ld, 
   a.entropy = entropy;
   a.top_ids = top_ids;
   a.top_logprobs = top_logprobs;
-  a.splits = wush::logprob_splits(R, V, logit_type);
+  const wush::LogprobPlan plan = wush::logprob_plan(R, V);
+  a.splits = plan.splits;
+  a.split_batches = plan.split_batches;
   // The keys first: they need 8-byte alignment whatever their number.
   a.keys = static_cast<uint64_t*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (need ? R * a.splits * (int64_t)top * 8 : 0));

@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include "wush_w4.h"
+#include "wush_wave.h"
 
 namespace wush {
 namespace {
@@ -21,14 +22,20 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kPerThread = 32;                       // elements per thread and batch
-constexpr int kBatch = kThreads * kPerThread;        // elements per workgroup and batch
+// Elements per thread and batch: 32 where there are rows or batches enough to
+// fill the chip, otherwise 8.
+constexpr int kWide = 32, kNarrow = 8;
 constexpr int kMaxSplits = 64;
-// Candidates of one batch: at most `top` threads per wave hold any (see
-// keep_largest), with 32 elements each, besides the entries kept so far.
-constexpr int kMaxCandidates = kWaves * kLogprobMaxTop * kPerThread + kLogprobMaxTop;
+// Candidates of one batch: at most `top` threads hold any (see keep_largest),
+// besides the entries kept so far; padded for rank_candidates.
+template <int PER>
+constexpr int kMaxCandidates = kLogprobMaxTop * PER + kLogprobMaxTop + 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
+
+// Workgroups that a launch should have.
+constexpr int64_t kTargetGroups = 1024;
+inline bool narrow(int64_t R, int64_t V) { return R * ((V + kThreads * kWide - 1) / (kThreads * kWide)) < kTargetGroups / 2; }
 
 struct Triple {
   float m, s, u;
@@ -53,21 +60,9 @@ __device__ __forceinline__ Triple join(Triple a, Triple b) {
   return r;
 }
 
-__device__ __forceinline__ Triple wave_join(Triple t) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    Triple o;
-    o.m = __shfl_xor(t.m, d);
-    o.s = __shfl_xor(t.s, d);
-    o.u = __shfl_xor(t.u, d);
-    t = join(t, o);
-  }
-  return t;
-}
-
-// Key of value v at index i; 0 for what never counts (-inf, NaN).
+// Key of value v at index i, -0 like +0; 0 for what never counts (-inf, NaN).
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t i) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = __float_as_uint(v + 0.0f);
   const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
   return v > -kInf ? ((uint64_t)o << 32) | (0xFFFFFFFFu - i) : 0u;
 }
@@ -105,38 +100,60 @@ struct Elem<2> {
   }
 };
 
-// The n-th largest (n >= 1) of the keys of the lanes with `in`, of which
-// there are at least n: one bit of the key at a time.
-__device__ __forceinline__ uint64_t nth_of_wave(uint64_t key, bool in, int n) {
-  uint64_t live = __ballot(in);
-  for (int b = 63; b >= 0 && __popcll(live) > 1; --b) {
-    const uint64_t set = __ballot((key >> b) & 1u) & live;
-    const int c = __popcll(set);
-    if (c >= n) {
-      live = set;
+// A bound that exactly n (>= 1) of the wave's keys reach, of which at least n are
+// not 0 (those are distinct), by bisection between the smallest and the largest.
+// Some eight halvings where values are spread, at most 64.
+template <int K>
+__device__ __forceinline__ uint64_t bound_of(const uint64_t (&key)[K], int n) {
+  uint32_t most = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const uint32_t word = (uint32_t)(key[i] >> 32);
+    most = word > most ? word : most;
+    least = key[i] != 0 && word < least ? word : least;
+  }
+  most = fold(most, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  least = fold(least, 0xFFFFFFFFu, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+  uint64_t lo = ((uint64_t)least << 32) + 1, hi = ((uint64_t)most << 32) + 0x100000000ull;  // n reach lo, none hi
+  while (hi - lo > 1) {
+    const uint64_t mid = lo + (hi - lo) / 2;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) c += __popcll(__ballot(key[i] >= mid));
+    if (c == n) return mid;
+    if (c > n) {
+      lo = mid;
     } else {
-      live &= ~set;
-      n -= c;
+      hi = mid;
     }
   }
-  return __shfl((unsigned long long)key, __ffsll((unsigned long long)live) - 1);
+  return lo;
 }
 
+template <int PER>
 struct TopState {
   uint64_t best[kLogprobMaxTop];  // sorted, 0 where there are fewer
-  uint64_t wave_bound[kWaves];
-  uint64_t cand[kMaxCandidates];
+  uint64_t largest[kThreads];     // of every thread
+  __attribute__((aligned(16))) uint64_t cand[kMaxCandidates<PER>];
   int n;
 };
 
-// best <- the `top` largest of the n candidates, by counting for each how many are
-// larger (keys are distinct).  All threads; `n` candidates are in place.
-__device__ __forceinline__ void rank_candidates(TopState& t, int top) {
+// best <- the `top` largest of the t.n candidates, by counting for each how
+// many are larger (keys are distinct, but for zeros, which all go last).  All
+// threads; the candidates are in place.
+template <int PER>
+__device__ __forceinline__ void rank_candidates(TopState<PER>& t, int top) {
+  constexpr int kStep = 8;
   const int n = t.n;
+  if ((int)threadIdx.x < kStep) t.cand[n + threadIdx.x] = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t k = t.cand[i];
     int larger = 0;
-    for (int j = 0; j < n; ++j) larger += t.cand[j] > k;
+    for (int j = 0; j < n; j += kStep) {
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) larger += t.cand[j + u] > k;
+    }
     if (larger < top) t.best[larger] = k;
   }
   __syncthreads();
@@ -145,40 +162,64 @@ __device__ __forceinline__ void rank_candidates(TopState& t, int top) {
 // One batch of the workgroup: thread's elements x[j] at index
 // at + (j / VEC) * kThreads * VEC + j % VEC.
 //
-// Only what is larger than the worst entry kept counts.  Where a wave has at least
-// `top` threads with such a maximum, its top-th largest thread maximum bounds the
-// answer from below too: at least `top` elements reach it.  Under the largest
-// such bound of the waves, at most `top` threads of any wave hold candidates.
-template <int VEC>
-__device__ __forceinline__ void keep_largest(TopState& t, const float (&x)[kPerThread], uint32_t at, float batch_max,
+// Only what is larger than the worst entry kept counts.  Where at least `top`
+// threads have such a maximum, a bound that `top` of the threads' maxima reach bounds
+// the answer from below too, and just these threads hold candidates.
+template <int VEC, int PER>
+__device__ __forceinline__ void keep_largest(TopState<PER>& t, const float (&x)[PER], uint32_t at, float batch_max,
                                              int top) {
   const uint64_t worst = t.best[top - 1];
   const float worst_value = worst ? key_value(worst) : -kInf;
   // Later batches hold higher indices: an equal value does not enter.
   const bool in = batch_max > worst_value;
-  if (!__syncthreads_or(in)) return;
+  const int entering = __syncthreads_count(in);
+  if (entering == 0) return;
   uint64_t mine = 0;
   if (in) {
+    // The thread's first element of that value.
+    int first = 0;
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const uint64_t k = key_of(x[j], at + (uint32_t)((j / VEC) * kThreads * VEC + j % VEC));
-      mine = k > mine ? k : mine;
-    }
+    for (int j = PER - 1; j >= 0; --j) first = x[j] == batch_max ? (j / VEC) * kThreads * VEC + j % VEC : first;
+    mine = key_of(batch_max, at + (uint32_t)first);
   }
-  const uint64_t votes = __ballot(in);
+  // The entries kept so far, none before the first batch with any.
+  const int kept = t.best[0] ? top : 0;
+  if ((int)threadIdx.x < kept) t.cand[threadIdx.x] = t.best[threadIdx.x];
+  if (threadIdx.x == 0) t.n = kept;
   uint64_t bound = worst + 1;
-  if (__popcll(votes) >= top) bound = nth_of_wave(mine, in, top);
-  if ((threadIdx.x & 63) == 0) t.wave_bound[threadIdx.x >> 6] = bound;
-  if (threadIdx.x < top) t.cand[threadIdx.x] = t.best[threadIdx.x];
-  if (threadIdx.x == 0) t.n = top;
-  __syncthreads();
+  if (entering >= top) {
+    t.largest[threadIdx.x] = mine;
+    __syncthreads();
+    uint64_t all[kWaves];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) bound = t.wave_bound[w] > bound ? t.wave_bound[w] : bound;
-  if (mine >= bound) {
+    for (int w = 0; w < kWaves; ++w) all[w] = t.largest[64 * w + (threadIdx.x & 63)];
+    bound = bound_of<kWaves>(all, top);
+  } else {
+    __syncthreads();
+  }
+  // key >= bound, on the halves: the value first, then the lower index.
+  const float least = bound > 1 ? key_value(bound) : -kInf;
+  const uint32_t up_to = 0xFFFFFFFFu - (uint32_t)bound;
+  const bool hold = mine >= bound;
+  if (__ballot(hold) != 0) {
+    uint64_t at_j[PER];  // lanes whose element j is a candidate
+    int total = 0;
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const uint64_t k = key_of(x[j], at + (uint32_t)((j / VEC) * kThreads * VEC + j % VEC));
-      if (k >= bound) t.cand[atomicAdd(&t.n, 1)] = k;
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t i = at + (uint32_t)((j / VEC) * kThreads * VEC + j % VEC);
+      at_j[j] = __ballot(hold && (x[j] > least || (x[j] == least && least > -kInf && i <= up_to)));
+      total += __popcll(at_j[j]);
+    }
+    const int lane = threadIdx.x & 63;
+    int to = 0;
+    if (lane == 0) to = atomicAdd(&t.n, total);
+    to = __builtin_amdgcn_readfirstlane(to);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (at_j[j] >> lane & 1)
+        t.cand[to + __popcll(at_j[j] & ((1ull << lane) - 1))] =
+            key_of(x[j], at + (uint32_t)((j / VEC) * kThreads * VEC + j % VEC));
+      to += __popcll(at_j[j]);
     }
   }
   __syncthreads();
@@ -200,8 +241,8 @@ __device__ __forceinline__ Finish finish(Triple t) {
   return f;
 }
 
-template <int TYPE>
-__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, Triple t, const TopState* top) {
+template <int TYPE, typename Top>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, Triple t, const Top* top) {
   const Finish f = finish(t);
   if (threadIdx.x == 0) {
     const int64_t id = a.targets[row];
@@ -226,47 +267,53 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, Tri
 }
 
 __device__ __forceinline__ Triple group_join(Triple t, Triple* lds) {
-  t = wave_join(t);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = t;
+  Triple w;
+  w.m = wave_max(t.m);
+  const float d = t.m == -kInf ? 0.0f : fmaxf(t.m - w.m, kFloor), e = exp_of(d);
+  w.s = wave_sum(t.s * e);
+  w.u = wave_sum(e * __builtin_fmaf(d, t.s, t.u));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = w;
   __syncthreads();
   t = lds[0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) t = join(t, lds[w]);
+  for (int k = 1; k < kWaves; ++k) t = join(t, lds[k]);
   return t;
 }
 
-template <bool TOP>
+template <bool TOP, int PER>
 struct Shared {
   Triple part[kWaves];
 };
-template <>
-struct Shared<true> {
+template <int PER>
+struct Shared<true, PER> {
   Triple part[kWaves];
-  TopState top;
+  TopState<PER> top;
 };
 
-template <int TYPE, bool TOP>
+template <int TYPE, bool TOP, int PER>
 __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
   using El = Elem<TYPE>;
-  constexpr int VEC = El::kVec, NV = kPerThread / VEC;
-  __shared__ Shared<TOP> sh;
-  const int64_t row = blockIdx.x / a.splits;
-  const int split = blockIdx.x % a.splits;
+  constexpr int VEC = El::kVec, NV = PER / VEC;
+  __shared__ Shared<TOP, PER> sh;
+  const int64_t row = blockIdx.x;
+  const int split = blockIdx.y;
   const uint8_t* L = static_cast<const uint8_t*>(a.L) + row * a.ld * El::kBytes;
   // Vectors on 16-byte boundaries: the first and the last may be partial.
   const int shift = (int)((reinterpret_cast<uintptr_t>(L) % 16) / El::kBytes);
-  const int64_t V = a.V, n_vec = (V + shift + VEC - 1) / VEC;
-  const int64_t batches = (n_vec + kThreads * NV - 1) / (kThreads * NV);
-  const int64_t b0 = batches * split / a.splits, b1 = batches * (split + 1) / a.splits;
+  const int64_t V = a.V;
+  constexpr uint32_t kVecs = kThreads * NV;  // vectors per batch
+  const uint32_t n_vec = ((uint32_t)V + shift + VEC - 1) / VEC, batches = (n_vec + kVecs - 1) / kVecs;
+  const uint32_t b0 = split * a.split_batches;
+  const uint32_t b1 = split == a.splits - 1 ? batches : b0 + a.split_batches;
   if constexpr (TOP) {
     if ((int)threadIdx.x < kLogprobMaxTop) sh.top.best[threadIdx.x] = 0;
     __syncthreads();
   }
   Triple t = {-kInf, 0.0f, 0.0f};
-  for (int64_t b = b0; b < b1; ++b) {
-    const int64_t v0 = b * (kThreads * NV) + threadIdx.x;
+  for (uint32_t b = b0; b < b1; ++b) {
+    const int64_t v0 = (int64_t)b * kVecs + threadIdx.x;
     u32x4 raw[NV];
-    float x[kPerThread];
+    float x[PER];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t e = (v0 + j * kThreads) * VEC - shift;  // the vector's first element
@@ -286,7 +333,7 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
     }
     float bm = x[0];
 #pragma unroll
-    for (int j = 1; j < kPerThread; ++j) bm = fmaxf(bm, x[j]);
+    for (int j = 1; j < PER; ++j) bm = fmaxf(bm, x[j]);
     if (bm > t.m) {
       const float d = t.m == -kInf ? 0.0f : fmaxf(t.m - bm, kFloor), e = exp_of(d);
       t.u = e * __builtin_fmaf(d, t.s, t.u);
@@ -295,16 +342,16 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
     }
     const float m = t.m == -kInf ? 0.0f : t.m;
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
+    for (int j = 0; j < PER; ++j) {
       // Masked: e = 0, and the floor keeps e d from being NaN.  NaN stays in e.
       const float d = x[j] - m, e = exp_of(d);
       t.s += e;
       t.u = __builtin_fmaf(e, fmaxf(d, kFloor), t.u);
     }
-    if constexpr (TOP) keep_largest<VEC>(sh.top, x, (uint32_t)(v0 * VEC - shift), bm, a.top);
+    if constexpr (TOP) keep_largest<VEC, PER>(sh.top, x, (uint32_t)(v0 * VEC - shift), bm, a.top);
   }
   t = group_join(t, sh.part);
-  const TopState* top = nullptr;
+  const TopState<PER>* top = nullptr;
   if constexpr (TOP) top = &sh.top;
   if (a.splits == 1) {
     write_row<TYPE>(a, row, t, top);
@@ -321,23 +368,37 @@ __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
   }
 }
 
-// Rows that several workgroups shared.
+// Rows that several workgroups shared.  Where there are `top` splits or more, a
+// bound that `top` of their largest entries reach bounds the answer from below,
+// and at most `top` splits hold candidates.
 template <int TYPE, bool TOP>
 __global__ __launch_bounds__(kThreads) void join_kernel(LogprobArgs a) {
-  __shared__ Shared<TOP> sh;
+  __shared__ Shared<TOP, kWide> sh;
   const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 63;
   Triple t = {-kInf, 0.0f, 0.0f};
   if ((int)threadIdx.x < a.splits) {
     const float* p = a.part + 4 * (row * a.splits + threadIdx.x);
     t = Triple{p[0], p[1], p[2]};
   }
-  const TopState* top = nullptr;
+  const TopState<kWide>* top = nullptr;
   if constexpr (TOP) {
-    const int n = a.splits * a.top;  // at most kMaxSplits * kLogprobMaxTop
-    static_assert(kMaxSplits * kLogprobMaxTop <= kMaxCandidates, "the splits' entries must fit");
-    for (int i = threadIdx.x; i < n; i += kThreads) sh.top.cand[i] = a.keys[row * n + i];
+    static_assert(kMaxSplits == 64, "one wave holds a row's splits");
+    static_assert(kLogprobMaxTop * kLogprobMaxTop + 8 <= kMaxCandidates<kWide>, "the candidates must fit");
+    const uint64_t* keys = a.keys + row * a.splits * a.top;
+    const int n = a.splits * a.top;
+    uint64_t bound = 1;
+    if (a.splits >= a.top) {
+      const uint64_t first[1] = {lane < a.splits ? keys[lane * a.top] : 0};
+      if (__popcll(__ballot(first[0] != 0)) >= a.top) bound = bound_of<1>(first, a.top);
+    }
     if ((int)threadIdx.x < kLogprobMaxTop) sh.top.best[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.top.n = n;
+    if (threadIdx.x == 0) sh.top.n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const uint64_t k = keys[i];
+      if (k >= bound) sh.top.cand[atomicAdd(&sh.top.n, 1)] = k;
+    }
     __syncthreads();
     rank_candidates(sh.top, a.top);
     top = &sh.top;
@@ -348,7 +409,12 @@ __global__ __launch_bounds__(kThreads) void join_kernel(LogprobArgs a) {
 
 template <int TYPE, bool TOP>
 hipError_t go(const LogprobArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((logprob_kernel<TYPE, TOP>), dim3((unsigned)(a.R * a.splits)), dim3(kThreads), 0, s, a);
+  const dim3 grid((unsigned)a.R, (unsigned)a.splits);
+  if (narrow(a.R, a.V)) {
+    hipLaunchKernelGGL((logprob_kernel<TYPE, TOP, kNarrow>), grid, dim3(kThreads), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((logprob_kernel<TYPE, TOP, kWide>), grid, dim3(kThreads), 0, s, a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL((join_kernel<TYPE, TOP>), dim3((unsigned)a.R), dim3(kThreads), 0, s, a);
@@ -357,12 +423,17 @@ hipError_t go(const LogprobArgs& a, hipStream_t s) {
 
 }  // namespace
 
-int logprob_splits(int64_t R, int64_t V, int) {
-  const int64_t batches = (V + kBatch - 1) / kBatch;
-  int64_t s = 1024 / (R > 0 ? R : 1);
+LogprobPlan logprob_plan(int64_t R, int64_t V) {
+  const int64_t per = kThreads * (narrow(R, V) ? kNarrow : kWide);
+  const int64_t batches = (V + per - 1) / per;
+  int64_t s = kTargetGroups / (R > 0 ? R : 1);
   if (s > batches) s = batches;
   if (s > kMaxSplits) s = kMaxSplits;
-  return s < 1 ? 1 : (int)s;
+  if (s < 1) s = 1;
+  // Whole batches per split; the last split also has the batch that an
+  // unaligned row start may add.
+  const int64_t each = (batches + s - 1) / s;
+  return LogprobPlan{(int)((batches + each - 1) / each), (int)each};
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {

@@ -9,6 +9,7 @@
 
 #include "wush_w4.h"
 #include "wush_w4_core.h"
+#include "wush_wave.h"
 
 namespace wush {
 namespace {
@@ -73,128 +74,145 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a, in
 }
 
 // ------------------------------------------------------------ choice
-//
-// One workgroup.  A wave chooses a token's experts: every lane holds the
-// logits of experts lane, lane + 64, ...; topk times the largest of the wave
-// is found, and among its equals the lowest expert.  Then expert e's tokens are
-// the set bits of a 64-bit mask, in order.
-constexpr int kRouteThreads = 1024;
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// A logit as an integer of the same order, for comparisons in one instruction:
+// NaN below every number, -0 like +0.
+constexpr int kTaken = INT32_MIN;  // below all of them
+__device__ __forceinline__ int order_key(float l) {
+  const int b = (int)__float_as_uint(l + 0.0f);
+  return l != l ? kTaken + 1 : b ^ (b >> 31 & 0x7FFFFFFF);
 }
 
-// Largest v of the wave, in all lanes.
-__device__ __forceinline__ float wave_max(float v) {
-#define WUSH_MAX_DPP(ctrl, rows)                                                                                    \
-  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(v), __float_as_uint(v), ctrl, rows, 0xf, \
-                                                           false)))
-  WUSH_MAX_DPP(0x111, 0xf);  // row_shr 1, 2, 4, 8: lane 15 of every row has the row's
-  WUSH_MAX_DPP(0x112, 0xf);
-  WUSH_MAX_DPP(0x114, 0xf);
-  WUSH_MAX_DPP(0x118, 0xf);
-  WUSH_MAX_DPP(0x142, 0xa);  // row_bcast 15: into rows 1 and 3
-  WUSH_MAX_DPP(0x143, 0xc);  // row_bcast 31: into rows 2 and 3
-#undef WUSH_MAX_DPP
-  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
-}
-
-// Inclusive prefix sum over the wave.
-__device__ __forceinline__ int wave_scan(int v) {
+// One wave chooses B tokens' experts: every lane holds the logits of experts lane,
+// lane + 64, ...; topk times the largest is found, and among its equals the
+// lowest expert.  Lane p < topk ends with choice p and its weight.
+template <int J, int B>
+__device__ __forceinline__ void choose(const MoeArgs& a, int m0, int (&id)[B], float (&weight)[B]) {
   const int lane = threadIdx.x & 63;
+  float l[B][J], chosen[B];
+  int key[B][J];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
-template <int J>  // experts per lane
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a, int tile_tokens) {
-  __shared__ unsigned long long tokens[kMoeMaxExperts];  // of each expert
-  __shared__ int start[kMoeMaxExperts];
-  __shared__ int wave_slots[16], wave_tiles[16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = threadIdx.x;
-  tokens[e] = 0;
-  __syncthreads();
-  for (int m = wave; m < a.M; m += kRouteThreads / 64) {
-    const float* logits = a.logits + (int64_t)m * a.E;
-    float l[J], left[J];
-    uint32_t taken = 0;  // bit j: expert lane + 64 j is taken, or there is none
+  for (int b = 0; b < B; ++b)
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int k = lane + 64 * j;
-      l[j] = k < a.E ? logits[k] : 0.0f;
-      left[j] = l[j] == l[j] ? l[j] : -__builtin_inff();  // NaN ranks below every number
-      if (k >= a.E) taken |= 1u << j;
+      const int e = lane + 64 * j, m = m0 + b < a.M ? m0 + b : m0;
+      l[b][j] = a.logits[(int64_t)m * a.E + (e < a.E ? e : 0)];
     }
-    int my_id = 0;
-    for (int p = 0; p < a.topk; ++p) {
-      float best = -__builtin_inff();
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (!(taken >> j & 1u)) best = fmaxf(best, left[j]);
-      best = wave_max(best);
-      int id = -1;
+  for (int b = 0; b < B; ++b) {
+    id[b] = 0;
+    chosen[b] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const uint64_t at = __ballot(!(taken >> j & 1u) && left[j] == best);
-        if (id < 0 && at != 0) id = 64 * j + __ffsll((unsigned long long)at) - 1;
+    for (int j = 0; j < J; ++j) key[b][j] = lane + 64 * j < a.E ? order_key(l[b][j]) : kTaken;
+  }
+  for (int p = 0; p < a.topk; ++p) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      int best = key[b][0];
+#pragma unroll
+      for (int j = 1; j < J; ++j) best = key[b][j] > best ? key[b][j] : best;
+      best = wave_max_int(best);
+      int found = 0;
+#pragma unroll
+      for (int j = J - 1; j >= 0; --j) {
+        const uint64_t at = __ballot(key[b][j] == best);
+        if (at != 0) found = 64 * j + __ffsll((unsigned long long)at) - 1;
       }
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (id == lane + 64 * j) taken |= 1u << j;
-      if (lane == p) my_id = id;
+        if (found == lane + 64 * j) key[b][j] = kTaken;
+      if (lane == p) {
+        id[b] = found;
+        // The key's logit; a chosen NaN gives NaN below.
+        chosen[b] = best == kTaken + 1 ? __builtin_nanf("") : __uint_as_float((uint32_t)(best ^ (best >> 31 & 0x7FFFFFFF)));
+      }
     }
-    const bool mine = lane < a.topk;
-    const float my_l = mine ? logits[my_id] : 0.0f;
-    const float top = __shfl(my_l, 0);
-    const float w = mine ? expf(my_l - top) : 0.0f;
+  }
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const float t = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(chosen[b]), 0));
+    const float w = lane < a.topk ? expf(chosen[b] - t) : 0.0f;
     float part = w;
     if (!a.renorm) {
       part = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (lane + 64 * j < a.E) part += expf(l[j] - top);
+        if (lane + 64 * j < a.E) part += expf(l[b][j] - t);
     }
-    const float total = wave_sum(part);
-    if (mine) {
-      a.ids[m * a.topk + lane] = my_id;
-      a.weights[m * a.topk + lane] = w / total;
-      atomicOr(&tokens[my_id], 1ull << m);
+    weight[b] = w / wave_sum(part);
+  }
+}
+
+// One workgroup: the tokens' choices, and the experts' tiles.  An expert's
+// tokens are the set bits of a 64-bit mask, in order.
+constexpr int kRouteThreads = 1024;
+
+template <int J, int B>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a, int tile_tokens) {
+  constexpr int kWaves = kRouteThreads / 64;
+  __shared__ unsigned long long tokens[kMoeMaxExperts];  // of each expert
+  __shared__ int first[kMoeMaxExperts];                  // its first tile
+  __shared__ short chosen[kMoeTokens * kMoeMaxTopK];
+  __shared__ int wave_tiles[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = threadIdx.x;
+  tokens[e] = 0;
+  __syncthreads();
+  for (int m0 = wave * B; m0 < a.M; m0 += kWaves * B) {
+    int id[B];
+    float weight[B];
+    choose<J, B>(a, m0, id, weight);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int m = m0 + b;
+      if (lane < a.topk && m < a.M) {
+        a.ids[m * a.topk + lane] = id[b];
+        a.weights[m * a.topk + lane] = weight[b];
+        chosen[m * a.topk + lane] = (short)id[b];
+        atomicOr(&tokens[id[b]], 1ull << m);
+      }
     }
   }
   __syncthreads();
-  // Thread e: expert e's slots and tiles; their places by a prefix sum over experts.
-  const unsigned long long mask = tokens[e];
-  const int count = __popcll(mask), tiles = (count + tile_tokens - 1) / tile_tokens;
-  const int slots_to = wave_scan(count), tiles_to = wave_scan(tiles);
-  if (lane == 63) {
-    wave_slots[wave] = slots_to;
-    wave_tiles[wave] = tiles_to;
+  // Thread e: expert e's tiles (at most 16); their place by a prefix sum over the
+  // experts, bit by bit of the counts.
+  const int count = __popcll(tokens[e]), tiles = (count + tile_tokens - 1) / tile_tokens;
+  const uint64_t below = (1ull << lane) - 1;
+  int at = 0, all = 0;
+#pragma unroll
+  for (int b = 0; b < 5; ++b) {
+    const uint64_t set = __ballot(tiles >> b & 1);
+    at += __popcll(set & below) << b;
+    all += __popcll(set) << b;
   }
+  if (lane == 0) wave_tiles[wave] = all;
   __syncthreads();
-  int slots_before = 0, tiles_before = 0;
-  for (int k = 0; k < wave; ++k) {
-    slots_before += wave_slots[k];
-    tiles_before += wave_tiles[k];
-  }
-  const int first = slots_before + slots_to - count;
-  start[e] = first;
+  for (int k = 0; k < wave; ++k) at += wave_tiles[k];
+  first[e] = at;
   for (int t = 0; t < tiles; ++t) {
     const int left = count - t * tile_tokens;
-    a.tiles[tiles_before + tiles_to - tiles + t] =
-        MoeTile{e, first + t * tile_tokens, left < tile_tokens ? left : tile_tokens, 0};
+    a.tiles[at + t].expert = e;
+    a.tiles[at + t].count = left < tile_tokens ? left : tile_tokens;
   }
-  if (e == kRouteThreads - 1) *a.n_tiles = tiles_before + tiles_to;
+  if (e == kRouteThreads - 1) *a.n_tiles = at + tiles;
   __syncthreads();
   for (int s = threadIdx.x; s < a.M * a.topk; s += kRouteThreads) {
-    const int m = s / a.topk, id = a.ids[s];  // written by this workgroup, before a barrier
-    a.slots[start[id] + __popcll(tokens[id] & ((1ull << m) - 1))] = s;
+    const int id = chosen[s], rank = __popcll(tokens[id] & ((1ull << (s / a.topk)) - 1));
+    MoeTile& tile = a.tiles[first[id] + rank / tile_tokens];
+    tile.token[rank % tile_tokens] = (int16_t)(s / a.topk);
+    tile.slot[rank % tile_tokens] = (int16_t)s;
   }
+}
+
+template <int J>
+hipError_t go_route(const MoeArgs& a, int tile_tokens, hipStream_t s) {
+  if (a.M <= 16 || J > 4) {
+    hipLaunchKernelGGL((route_kernel<J, 1>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
+  } else if (a.M <= 32) {
+    hipLaunchKernelGGL((route_kernel<J, 2>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
+  } else {
+    hipLaunchKernelGGL((route_kernel<J, 4>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
+  }
+  return hipGetLastError();
 }
 
 // ------------------------------------------------------------ gate and up
@@ -203,28 +221,39 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a, int til
 // wave wn has 32 gate rows and the 32 up rows of the same channels.  32 channels
 // hold whole transform blocks, so T_mid is applied to h right here.
 template <int FMT, int NT, int TERMS, bool SPREAD, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, 2) void gate_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void gate_up_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
-  __shared__ int slot[16 * NT];
+  __shared__ int slot[16 * NT], token[16 * NT];
   constexpr int kThreads = 64 * WN * WK, kChannels = 32 * WN, kRows = SPREAD ? 4 : 16 * NT;
+  const MoeTile& tile = a.tiles[blockIdx.y];
+  const int expert = tile.expert, count = tile.count, my_slot = tile.slot[threadIdx.x & 31];
+  const int my_token = tile.token[threadIdx.x & 31];
   if ((int)blockIdx.y >= *a.n_tiles) return;
-  const MoeTile tile = a.tiles[blockIdx.y];
-  const int n = threadIdx.x & 15, wn = (threadIdx.x >> 6) % WN;
+  const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WN;
   const int64_t H = a.H, I = a.I, i0 = (int64_t)blockIdx.x * kChannels;
-  if ((int)threadIdx.x < tile.count) slot[threadIdx.x] = a.slots[tile.start + threadIdx.x];
-  const auto p = make_rows<FMT, 4, 1>(a.gu_codes, a.gu_scales, H, [&](int r) {
-    const int64_t i = i0 + 32 * wn + 16 * (r & 1) + n;
-    return (int64_t)tile.expert * (2 * I) + (r < 2 ? 0 : I) + (i < I ? i : I - 1);
-  });
-  __syncthreads();
+  const int64_t gate = (int64_t)expert * (2 * I);
+  const auto p = make_rows<FMT, 4, 1>(
+      a.gu_codes, a.gu_scales, H,
+      [&](int r) {
+        const int64_t i = i0 + 32 * wn + 16 * (r & 1);
+        return gate + (r < 2 ? 0 : I) + (i < I ? i : I - 1);
+      },
+      [&](int r) { return gate + (r < 2 ? I : 2 * I) - 1; });
+  const auto ready = [&] {
+    if ((int)threadIdx.x < count) {
+      slot[threadIdx.x] = my_slot;
+      token[threadIdx.x] = my_token;
+    }
+    meet();
+  };
   const uint16_t* X = a.T_in ? a.xt : a.X;
   const int64_t ldx = a.T_in ? H : a.ldx;
   group_dot<FMT, 4, 1, NT, TERMS, SPREAD, WN, WK>(
-      lds, p, [&](int row) { return X + slot[row] / a.topk * ldx; }, a.M * H, tile.count, H);
-  const float gs = FMT == kNV ? a.gu_gs[tile.expert] : 1.0f;
+      lds, p, ready, [&](int row) { return X + token[row] * ldx; }, a.M * H, count, H);
+  const float gs = FMT == kNV ? a.gu_gs[expert] : 1.0f;
   // Value v: token v / kChannels, channel v % kChannels.
   constexpr int kEach = (kRows * kChannels + kThreads - 1) / kThreads;
-  const int values = tile.count * kChannels;
+  const int values = count * kChannels;
   float h[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
@@ -232,8 +261,8 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void gate_up_kernel(MoeArgs a) {
     h[k] = 0.0f;
     if (v < values) {
       const int row = 64 * (c / 32) + c % 32;
-      float g = group_sum<4, WN, WK>(lds, row, m, tile.count);
-      float u = group_sum<4, WN, WK>(lds, row + 32, m, tile.count);
+      float g = group_sum<4, WN, WK>(lds, row, m, count);
+      float u = group_sum<4, WN, WK>(lds, row + 32, m, count);
       if (FMT == kNV) {
         g *= gs;
         u *= gs;
@@ -255,7 +284,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void gate_up_kernel(MoeArgs a) {
     for (int k = 0; k < kEach; ++k) {
       const int v = threadIdx.x + k * kThreads, c = v % kChannels;
       if (v >= values || i0 + c >= I) continue;
-      const uint16_t* T = a.T_mid + ((int64_t)tile.expert * I + i0 + c) * G;  // row c % G of its block
+      const uint16_t* T = a.T_mid + ((int64_t)expert * I + i0 + c) * G;  // row c % G of its block
       const float* block = hs + v / G * G;
       float s = 0.0f;
 #pragma unroll
@@ -289,27 +318,33 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void gate_up_kernel(MoeArgs a) {
 // A workgroup owns 16 R WN channels of y for one tile; its results, one row per
 // slot, wait in memory for the slots' other experts.
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, 2) void down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void down_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   __shared__ int slot[16 * NT];
   constexpr int kThreads = 64 * WN * WK, kChannels = 16 * R * WN;
+  const MoeTile& tile = a.tiles[blockIdx.y];
+  const int expert = tile.expert, count = tile.count, my_slot = tile.slot[threadIdx.x & 31];
   if ((int)blockIdx.y >= *a.n_tiles) return;
-  const MoeTile tile = a.tiles[blockIdx.y];
-  const int n = threadIdx.x & 15, wn = (threadIdx.x >> 6) % WN;
+  const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WN;
   const int64_t H = a.H, I = a.I, n0 = (int64_t)blockIdx.x * kChannels;
-  if ((int)threadIdx.x < tile.count) slot[threadIdx.x] = a.slots[tile.start + threadIdx.x];
-  const auto p = make_rows<FMT, R, D>(a.dn_codes, a.dn_scales, I, [&](int r) {
-    const int64_t i = n0 + 16 * (wn * R + r) + n;
-    return tile.expert * H + (i < H ? i : H - 1);
-  });
-  __syncthreads();
+  const auto p = make_rows<FMT, R, D>(
+      a.dn_codes, a.dn_scales, I,
+      [&](int r) {
+        const int64_t i = n0 + 16 * (wn * R + r);
+        return expert * H + (i < H ? i : H - 1);
+      },
+      [&](int) { return expert * H + H - 1; });
+  const auto ready = [&] {
+    if ((int)threadIdx.x < count) slot[threadIdx.x] = my_slot;
+    meet();
+  };
   group_dot<FMT, R, D, NT, TERMS, SPREAD, WN, WK>(
-      lds, p, [&](int row) { return a.h + slot[row] * I; }, (int64_t)a.M * a.topk * I, tile.count, I);
-  const float gs = FMT == kNV ? a.dn_gs[tile.expert] : 1.0f;
-  for (int v = threadIdx.x; v < tile.count * kChannels; v += kThreads) {
+      lds, p, ready, [&](int row) { return a.h + slot[row] * I; }, (int64_t)a.M * a.topk * I, count, I);
+  const float gs = FMT == kNV ? a.dn_gs[expert] : 1.0f;
+  for (int v = threadIdx.x; v < count * kChannels; v += kThreads) {
     const int m = v / kChannels, c = v % kChannels;
     if (n0 + c >= H) continue;
-    float s = group_sum<R, WN, WK>(lds, c, m, tile.count);
+    float s = group_sum<R, WN, WK>(lds, c, m, count);
     if (FMT == kNV) s *= gs;
     a.part[slot[m] * H + n0 + c] = s;
   }
@@ -360,8 +395,10 @@ int tile_tokens(const MoeArgs& a) {
 template <int FMT, int TERMS>
 hipError_t go_gate_up_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);
-  if (t == 4) return go_gate_up<FMT, 1, TERMS, true, 1, 8>(a, max_tiles, s);
-  if (t == 16) return go_gate_up<FMT, 1, TERMS, false, 2, 4>(a, max_tiles, s);
+  // Three waves per SIMD hold three workgroups of four waves, but one of eight.
+  constexpr int kHalf = min_waves<FMT, 1, TERMS>() == 4 ? 1 : 2;
+  if (t == 4) return go_gate_up<FMT, 1, TERMS, true, 1, 8 / kHalf>(a, max_tiles, s);
+  if (t == 16) return go_gate_up<FMT, 1, TERMS, false, 2, 4 / kHalf>(a, max_tiles, s);
   return go_gate_up<FMT, 2, TERMS, false, 4, 2>(a, max_tiles, s);
 }
 
@@ -369,7 +406,8 @@ template <int FMT, int TERMS>
 hipError_t go_down_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);
   if (t == 4) return go_down<FMT, 2, 2, 1, TERMS, true, 1, 4>(a, max_tiles, s);
-  if (t == 16) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, max_tiles, s);
+  constexpr int kHalf = min_waves<FMT, 1, TERMS>() == 4 ? 1 : 2;
+  if (t == 16) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4 / kHalf>(a, max_tiles, s);
   return go_down<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, max_tiles, s);
 }
 
@@ -395,10 +433,7 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tokens = tile_tokens(a);
-  if (a.E <= 128) hipLaunchKernelGGL((route_kernel<2>), dim3(1), dim3(kRouteThreads), 0, s, a, tokens);
-  else if (a.E <= 256) hipLaunchKernelGGL((route_kernel<4>), dim3(1), dim3(kRouteThreads), 0, s, a, tokens);
-  else hipLaunchKernelGGL((route_kernel<16>), dim3(1), dim3(kRouteThreads), 0, s, a, tokens);
-  e = hipGetLastError();
+  e = a.E <= 128 ? go_route<2>(a, tokens, s) : a.E <= 256 ? go_route<4>(a, tokens, s) : go_route<16>(a, tokens, s);
   if (e != hipSuccess) return e;
   e = a.fmt == kMX ? go_experts<kMX>(a, s) : a.fmt == kNV ? go_experts<kNV>(a, s) : go_experts<kINT>(a, s);
   if (e != hipSuccess) return e;

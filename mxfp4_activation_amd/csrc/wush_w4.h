@@ -46,7 +46,8 @@ constexpr int kMoeMaxTopK = 32;
 
 // Tokens of one expert that share a pass over its weights.
 struct MoeTile {
-  int expert, start, count, pad;  // slots[start .. start + count)
+  int expert, count;
+  int16_t token[32], slot[32];  // slot: token * topk + place among its experts
 };
 
 struct MoeArgs {
@@ -74,7 +75,6 @@ struct MoeArgs {
   float* logits;            // [M][E]
   uint16_t* h;              // [terms][M * topk][I]
   float* part;              // [M * topk][H]
-  int32_t* slots;           // [M * topk], grouped by expert
   int32_t* n_tiles;
   MoeTile* tiles;           // [M * topk]
 };
@@ -98,12 +98,16 @@ struct LogprobArgs {
   int32_t* top_ids;        // [R][top]
   float* top_logprobs;     // [R][top]
   int splits;              // workgroups per row
+  int split_batches;       // batches of each but the last
   float* part;             // [R][splits][4], if splits > 1: max, sum, weighted sum
   uint64_t* keys;          // [R][splits][top], if splits > 1
 };
 
-// Workgroups per row (1: no workspace).
-int logprob_splits(int64_t R, int64_t V, int type);
+// Workgroups per row (1: no workspace), and batches of each.
+struct LogprobPlan {
+  int splits, split_batches;
+};
+LogprobPlan logprob_plan(int64_t R, int64_t V);
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
 
 }  // namespace wush

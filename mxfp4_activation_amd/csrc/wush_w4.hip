@@ -22,20 +22,20 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 //
 // A workgroup owns 16 R WN weight rows and up to 16 NT tokens.
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, 2) void linear_kernel(LinearArgs a) {
+__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void linear_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   constexpr int kRows = 16 * R * WN;
-  const int wave = threadIdx.x >> 6, n = threadIdx.x & 15, wn = wave % WN;
+  const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WN;
   constexpr int kTokens = SPREAD ? 4 : 16 * NT;
   const int64_t n0 = (int64_t)blockIdx.x * kRows, m0 = (int64_t)blockIdx.y * kTokens;
   const int rows = (int)(a.M - m0 < kTokens ? a.M - m0 : kTokens);
-  const auto p = make_rows<FMT, R, D>(a.codes, a.scales, a.K, [&](int r) {
-    const int64_t row = n0 + 16 * (wn * R + r) + n;
-    return row < a.N ? row : a.N - 1;
-  });
+  const auto p = make_rows<FMT, R, D>(
+      a.codes, a.scales, a.K, [&](int r) { return n0 + 16 * (wn * R + r) < a.N ? n0 + 16 * (wn * R + r) : a.N - 1; },
+      [&](int) { return a.N - 1; });
   const uint16_t* X = a.x.X + m0 * a.x.ldx;
   const int64_t ldx = a.x.ldx;
-  group_dot<FMT, R, D, NT, TERMS, SPREAD, WN, WK>(lds, p, [&](int row) { return X + row * ldx; }, a.x.plane, rows, a.K);
+  group_dot<FMT, R, D, NT, TERMS, SPREAD, WN, WK>(
+      lds, p, [] {}, [&](int row) { return X + row * ldx; }, a.x.plane, rows, a.K);
   const float g = FMT == kNV ? a.gs[0] : 1.0f;
   for (int o = threadIdx.x; o < rows * kRows; o += 64 * WN * WK) {
     const int m = o / kRows, c = o % kRows;

@@ -97,25 +97,40 @@ __device__ __forceinline__ u32x2 load_scales(const uint8_t* sp, int64_t st) {
   }
 }
 
-// Row pointers of a wave's R tiles.
+// A wave's R tiles: of each, the first row (the same in all lanes) and the lane's
+// offset from there, to its 16 bytes of step 0; and the lane's scales.
 template <int FMT, int R, int D>
 struct Rows {
-  const uint8_t* cp[R];  // the lane's row of each tile, at its 16 bytes of step 0
+  const uint8_t* cp[R];
+  uint32_t off[R];
   const uint8_t* sp[Raw<FMT, R, D>::kShared ? 1 : R];
 };
 
-// row(t): index of the weight row that the lane's column of row tile t stands for.
-template <int FMT, int R, int D, typename F>
-__device__ __forceinline__ Rows<FMT, R, D> make_rows(const uint8_t* codes, const uint8_t* scales, int64_t K, F row) {
-  const int q = (threadIdx.x & 63) >> 4;
+// first(t): index of row tile t's first row; last(t): the last one it may read (rows
+// past it stand for results that nobody stores).  K at most 2^27 keeps off
+// within 32 bits.
+template <int FMT, int R, int D, typename F, typename L>
+__device__ __forceinline__ Rows<FMT, R, D> make_rows(const uint8_t* codes, const uint8_t* scales, int64_t K, F first,
+                                                     L last) {
+  const int n = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+  const auto clamped = [&](int t) {
+    const int64_t room = last(t) - first(t);
+    return (int)(n < room ? n : room);
+  };
   Rows<FMT, R, D> o;
 #pragma unroll
-  for (int r = 0; r < R; ++r) o.cp[r] = codes + row(r) * row_code_bytes<FMT>(K) + 16 * q;
+  for (int r = 0; r < R; ++r) {
+    const int64_t at = first(r) * row_code_bytes<FMT>(K);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    o.cp[r] = codes + (int64_t)(((uint64_t)hi << 32) | lo);
+    o.off[r] = (uint32_t)(clamped(r) * row_code_bytes<FMT>(K) + 16 * q);
+  }
   if constexpr (Raw<FMT, R, D>::kShared) {
-    o.sp[0] = scales + row(q / D) * row_scale_bytes<FMT>(K) + (FMT == kMX ? 4 : 8) * (q % D);
+    o.sp[0] = scales + (first(q / D) + clamped(q / D)) * row_scale_bytes<FMT>(K) + (FMT == kMX ? 4 : 8) * (q % D);
   } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r) o.sp[r] = scales + row(r) * row_scale_bytes<FMT>(K);
+    for (int r = 0; r < R; ++r) o.sp[r] = scales + (first(r) + clamped(r)) * row_scale_bytes<FMT>(K);
   }
   return o;
 }
@@ -127,7 +142,7 @@ __device__ __forceinline__ void load_raw(Raw<FMT, R, D>& w, const Rows<FMT, R, D
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int d = 0; d < D; ++d) w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d));
+    for (int d = 0; d < D; ++d) w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d) + p.off[r]);
   if constexpr (RawT::kShared) {
     w.s[0] = load_scales<FMT>(p.sp[0], st);
   } else {
@@ -154,7 +169,7 @@ __device__ __forceinline__ void load_raw_tail(Raw<FMT, R, D>& w, const Rows<FMT,
       for (int d = 0; d < D; ++d) {
         // The lane's 16 bytes, or the row's last 16 if they reach past it.
         const int64_t last = K / 2 - 16 - 16 * q, at = 64 * (st + d);
-        w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + (at < last ? at : last));
+        w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + (at < last ? at : last) + p.off[r]);
       }
     // sp points at this step's bytes; not past the row's last kStepBytes.
     auto back = [&](int64_t step) {
@@ -179,9 +194,9 @@ __device__ __forceinline__ void load_raw_tail(Raw<FMT, R, D>& w, const Rows<FMT,
       const int64_t k = (st + d) * kStep + 32 * q;
       u32x4 c = {0, 0, 0, 0};
       if (k + 32 <= K) {
-        c = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d));
+        c = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d) + p.off[r]);
       } else if (FMT == kNV && k + 16 <= K) {
-        const u32x2 h = load_unaligned<u32x2>(p.cp[r] + 64 * (st + d));
+        const u32x2 h = load_unaligned<u32x2>(p.cp[r] + 64 * (st + d) + p.off[r]);
         c[0] = h[0];
         c[1] = h[1];
       }
@@ -466,6 +481,13 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[R][NT], Raw<FMT, R, D>& w,
 
 constexpr int kBuffers = 3;  // activation chunks in LDS
 
+// Waves per SIMD that the registers are cut for: four where the code fits 128
+// without spilling, otherwise three (168) or, with several token tiles, two.
+template <int FMT, int NT, int TERMS>
+constexpr int min_waves() {
+  return NT > 1 ? 2 : FMT == kMX || (FMT == kNV && TERMS == 1) ? 4 : 3;
+}
+
 // LDS of one workgroup in bytes: the activation buffers, or the sums that meet at
 // the end, whichever is more.
 template <int R, int D, int NT, int TERMS, int WN, int WK>
@@ -480,21 +502,22 @@ inline int64_t lds_bytes(int rows, int64_t K) {
 
 // The workgroup's product of `rows` activation rows (at most 16 NT, or 4 where
 // SPREAD) with its 16 R WN weight rows over all of K; wave wk * WN + wn takes
-// its row tiles from p.  src(row): pointer to term 0 of an activation row; terms
-// are `plane` elements apart.  Afterwards group_sum gives the results.
+// its row tiles from p.  src(row): pointer to term 0 of an activation row, once
+// ready() has run; terms are `plane` elements apart.  Afterwards group_sum gives
+// the results.
 //
 // SPREAD: up to four tokens stand in rows 0, 4, 8 and 12 of A, so that each
 // lane holds one result in the first component of D and INT4's scales cost one
 // multiplication per instruction rather than four.
 //
-// Order of a wave's requests: activations of chunk c + 1, weights of chunk c;
-// those of one chunk are in flight while the one before is multiplied.  Loads
-// complete in order, so a wave that has chunk c's weights knows that its
-// copies of chunk c + 1 have landed, and the barrier after chunk c tells the
-// others.
-template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK, typename F>
-__device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& p, F src, int64_t plane, int rows,
-                                          int64_t K) {
+// Order of a wave's requests from chunk 1 on: activations of chunk c + 1,
+// weights of chunk c; those of one chunk are in flight while the one before is
+// multiplied.  Loads complete in order, so a wave that has chunk c's weights
+// knows that its copies of chunk c + 1 have landed, and the barrier after chunk
+// c tells the others; arrive() does so for the first two.
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK, typename P, typename F>
+__device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& p, P ready, F src, int64_t plane,
+                                          int rows, int64_t K) {
   constexpr int kSteps = WK * D, kWidth = kSteps * kStep, kWaves = WN * WK;
   static_assert(!SPREAD || NT == 1, "a spread tile is one tile");
   using Ln = Lines<kWidth>;
@@ -535,7 +558,7 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
         if (line + e / kWidth < TERMS * rows) line += e / kWidth;
         pos = e % kWidth ^ Ln::flip(e / kWidth);
       }
-      const int t = TERMS == 1 ? 0 : line / rows, row = line - t * rows;
+      const int t = (TERMS > 1 && line >= rows) + (TERMS > 2 && line >= 2 * rows), row = line - t * rows;
       int64_t k = (int64_t)c * kWidth + pos;
       k = k + 8 <= K ? k : 0;
       copy16((glb_u16*)(src(row) + t * plane + k),
@@ -544,60 +567,71 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
   };
 
   const int full = (int)(K / kWidth);
-  const int64_t step0 = wk * D;
+  const int step0 = wk * D;
   const bool tail = full < chunks && ((int64_t)full * kSteps + step0) * kStep < K;  // this wave has a part of it
   const uint16_t* xw = lds + step0 * kStep;
-  Raw<FMT, R, D> wt;
-  if (tail) load_raw_tail(wt, p, (int64_t)full * kSteps + step0, K);
-  copy_x(0);
-  if (full > 0) {
-    // Two sets of registers in turn, and no load on a condition inside the loop:
-    // the compiler counts what is in flight and waits for no more than it
-    // needs.
-    Raw<FMT, R, D> w0, w1;
-    auto load = [&](Raw<FMT, R, D>& to, int c) { load_raw(to, p, (int64_t)c * kSteps + step0); };
-    auto dot = [&](Raw<FMT, R, D>& w, int c) {
-      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, xw + (c % kBuffers) * buffer, xo);
-      meet();
-    };
-    if (chunks > 1) copy_x(1);
-    load(w0, 0);
-    int c = 0;
-    if (full == 1) {
-      arrive<R * D>();
-    } else {
-      if (chunks > 2) copy_x(2);
-      load(w1, 1);
-      arrive<2 * R * D>();
-      for (; c + 2 < full; c += 2) {
-        dot(w0, c);
-        if (c + 3 < chunks) copy_x(c + 3);
-        load(w0, c + 2);
-        dot(w1, c + 1);
-        if (c + 3 >= full) {
-          c += 2;
-          break;
-        }
-        if (c + 4 < chunks) copy_x(c + 4);
-        load(w1, c + 3);
-      }
-      // c is full - 2 with w1 loaded, or full - 1 without.
-      if (c + 1 < full) {
-        dot(w0, c);
-        dot(w1, c + 1);
-        c = full;
-      }
+  Raw<FMT, R, D> w0, w1;
+  auto load = [&](Raw<FMT, R, D>& to, int c) { load_raw(to, p, (int64_t)c * kSteps + step0); };
+  auto load_tail = [&](Raw<FMT, R, D>& to) {
+    if (tail) load_raw_tail(to, p, (int64_t)full * kSteps + step0, K);
+  };
+  auto dot = [&](Raw<FMT, R, D>& w, int c) {
+    multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, xw + (c % kBuffers) * buffer, xo);
+    meet();
+  };
+  auto dot_tail = [&](Raw<FMT, R, D>& w) {
+    if (full == chunks) return;
+    if (tail) {
+      fix_tail(w, (int64_t)full * kSteps + step0, K);
+      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, xw + (full % kBuffers) * buffer, xo);
     }
-    if (c < full) dot(w0, c);
+    meet();
+  };
+  // The first weights need no activations, and are asked for before anything is
+  // known of those.
+  if (full > 0) {
+    load(w0, 0);
+  } else {
+    load_tail(w0);
+  }
+  ready();
+  copy_x(0);
+  if (chunks > 1) copy_x(1);
+  // Two sets of registers in turn, and no load on a condition inside the loop:
+  // the compiler counts what is in flight and waits for no more than it needs.
+  // At its end w0 holds chunk c and, unless that is the last whole one, w1 chunk
+  // c + 1.
+  int c = 0;
+  if (full > 1) {
+    if (chunks > 2) copy_x(2);
+    load(w1, 1);
+    arrive<R * D>();
+    for (; c + 2 < full; c += 2) {
+      dot(w0, c);
+      if (c + 3 < chunks) copy_x(c + 3);
+      load(w0, c + 2);
+      dot(w1, c + 1);
+      if (c + 3 >= full) {
+        c += 2;
+        break;
+      }
+      if (c + 4 < chunks) copy_x(c + 4);
+      load(w1, c + 3);
+    }
   } else {
     arrive<0>();
   }
-  if (full < chunks) {
-    if (tail) {
-      fix_tail(wt, (int64_t)full * kSteps + step0, K);
-      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, wt, xw + (full % kBuffers) * buffer, xo);
+  if (full > 0 && c + 1 == full) {
+    load_tail(w1);
+    dot(w0, c);
+    dot_tail(w1);
+  } else {
+    if (full > 0) {
+      dot(w0, c);
+      load_tail(w0);
+      dot(w1, c + 1);
     }
-    meet();
+    dot_tail(w0);
   }
   float* red = reinterpret_cast<float*>(lds) + wave * (R * 16 * rows);
 #pragma unroll

@@ -20,15 +20,21 @@ _OUT = {torch.float32: 0, torch.bfloat16: 1}
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
+# The current stream's handle without a Stream object around it: a call on one
+# token takes a few microseconds, of which building that object would be two.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _enter(t: torch.Tensor, name: str):
     """(device, raw current stream) of a call whose first operand is t."""
     if not t.is_cuda:
         raise ValueError("%s must be a device tensor" % name)
     dev = t.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError("%s must be on the current device (it is on %s, current cuda:%d)"
-                         % (name, dev, torch.cuda.current_device()))
-    return dev, torch.cuda.current_stream(dev).cuda_stream
+    current = torch.cuda.current_device()
+    if dev.index != current:
+        raise ValueError("%s must be on the current device (it is on %s, current cuda:%d)" % (name, dev, current))
+    return dev, _raw_stream(current)
 
 
 def _fmt(fmt: str):
