@@ -205,26 +205,31 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a, int til
 
 template <int J>
 hipError_t go_route(const MoeArgs& a, int tile_tokens, hipStream_t s) {
-  if (a.M <= 16 || J > 4) {
-    hipLaunchKernelGGL((route_kernel<J, 1>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
-  } else if (a.M <= 32) {
-    hipLaunchKernelGGL((route_kernel<J, 2>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
-  } else {
-    hipLaunchKernelGGL((route_kernel<J, 4>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
+  if constexpr (J <= 4) {
+    if (a.M > 32) {
+      hipLaunchKernelGGL((route_kernel<J, 4>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
+      return hipGetLastError();
+    }
+    if (a.M > 16) {
+      hipLaunchKernelGGL((route_kernel<J, 2>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
+      return hipGetLastError();
+    }
   }
+  hipLaunchKernelGGL((route_kernel<J, 1>), dim3(1), dim3(kRouteThreads), 0, s, a, tile_tokens);
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------ gate and up
 //
-// A workgroup owns 32 WN channels of h for one tile of tokens of one expert:
-// wave wn has 32 gate rows and the 32 up rows of the same channels.  32 channels
-// hold whole transform blocks, so T_mid is applied to h right here.
-template <int FMT, int NT, int TERMS, bool SPREAD, int WN, int WK>
+// A workgroup owns 8 R WN (32 or more) channels of h for one tile of tokens of
+// one expert: wave wn has 8 R gate rows and the 8 R up rows of the same channels.  32
+// channels hold whole transform blocks, so T_mid is applied to h right here.
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
 __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void gate_up_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   __shared__ int slot[16 * NT], token[16 * NT];
-  constexpr int kThreads = 64 * WN * WK, kChannels = 32 * WN, kRows = SPREAD ? 4 : 16 * NT;
+  constexpr int kThreads = 64 * WN * WK, kWaveChannels = 8 * R, kChannels = kWaveChannels * WN, kRows = SPREAD ? 4 : 16 * NT;
+  static_assert(kChannels % 32 == 0, "whole transform blocks");
   const MoeTile& tile = a.tiles[blockIdx.y];
   const int expert = tile.expert, count = tile.count, my_slot = tile.slot[threadIdx.x & 31];
   const int my_token = tile.token[threadIdx.x & 31];
@@ -232,13 +237,13 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void g
   const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WN;
   const int64_t H = a.H, I = a.I, i0 = (int64_t)blockIdx.x * kChannels;
   const int64_t gate = (int64_t)expert * (2 * I);
-  const auto p = make_rows<FMT, 4, 1>(
+  const auto p = make_rows<FMT, R, D>(
       a.gu_codes, a.gu_scales, H,
       [&](int r) {
-        const int64_t i = i0 + 32 * wn + 16 * (r & 1);
-        return gate + (r < 2 ? 0 : I) + (i < I ? i : I - 1);
+        const int64_t i = i0 + kWaveChannels * wn + 16 * (r % (R / 2));
+        return gate + (r < R / 2 ? 0 : I) + (i < I ? i : I - 1);
       },
-      [&](int r) { return gate + (r < 2 ? I : 2 * I) - 1; });
+      [&](int r) { return gate + (r < R / 2 ? I : 2 * I) - 1; });
   const auto ready = [&] {
     if ((int)threadIdx.x < count) {
       slot[threadIdx.x] = my_slot;
@@ -248,7 +253,7 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void g
   };
   const uint16_t* X = a.T_in ? a.xt : a.X;
   const int64_t ldx = a.T_in ? H : a.ldx;
-  group_dot<FMT, 4, 1, NT, TERMS, SPREAD, WN, WK>(
+  group_dot<FMT, R, D, NT, TERMS, SPREAD, WN, WK>(
       lds, p, ready, [&](int row) { return X + token[row] * ldx; }, a.M * H, count, H);
   const float gs = FMT == kNV ? a.gu_gs[expert] : 1.0f;
   // Value v: token v / kChannels, channel v % kChannels.
@@ -260,9 +265,9 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void g
     const int v = threadIdx.x + k * kThreads, m = v / kChannels, c = v % kChannels;
     h[k] = 0.0f;
     if (v < values) {
-      const int row = 64 * (c / 32) + c % 32;
-      float g = group_sum<4, WN, WK>(lds, row, m, count);
-      float u = group_sum<4, WN, WK>(lds, row + 32, m, count);
+      const int row = 2 * kWaveChannels * (c / kWaveChannels) + c % kWaveChannels;
+      float g = group_sum<R, WN, WK>(lds, row, m, count);
+      float u = group_sum<R, WN, WK>(lds, row + kWaveChannels, m, count);
       if (FMT == kNV) {
         g *= gs;
         u *= gs;
@@ -366,15 +371,15 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a) {
   }
 }
 
-template <int FMT, int NT, int TERMS, bool SPREAD, int WN, int WK>
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
 hipError_t go_gate_up(const MoeArgs& a, int max_tiles, hipStream_t s) {
-  const dim3 grid((unsigned)((a.I + 32 * WN - 1) / (32 * WN)), (unsigned)max_tiles);
-  constexpr int kRows = SPREAD ? 4 : 16 * NT;
+  constexpr int kChannels = 8 * R * WN, kRows = SPREAD ? 4 : 16 * NT;
+  const dim3 grid((unsigned)((a.I + kChannels - 1) / kChannels), (unsigned)max_tiles);
   const int rows = a.M < kRows ? a.M : kRows;
-  int64_t lds = lds_bytes<4, 1, NT, TERMS, WN, WK>(rows, a.H);
-  const int64_t hs = (int64_t)4 * rows * 32 * WN;
+  int64_t lds = lds_bytes<R, D, NT, TERMS, WN, WK>(rows, a.H);
+  const int64_t hs = (int64_t)4 * rows * kChannels;
   if (hs > lds) lds = hs;
-  return launch_lds(gate_up_kernel<FMT, NT, TERMS, SPREAD, WN, WK>, grid, 64 * WN * WK, lds, s, a);
+  return launch_lds(gate_up_kernel<FMT, R, D, NT, TERMS, SPREAD, WN, WK>, grid, 64 * WN * WK, lds, s, a);
 }
 
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
@@ -392,22 +397,28 @@ int tile_tokens(const MoeArgs& a) {
   return a.M <= 4 || expect <= 2.0f ? 4 : a.M <= 16 || expect <= 12.0f ? 16 : 32;
 }
 
+// Four waves of two row tiles and two steps each.  Measured on 128 experts of
+// 4096 x 1280 MXFP4 with transforms, 8 tokens (the whole call): 122 us, against 133
+// with eight waves of four row tiles that split K, and 144 with four of those;
+// down 124 against 132 with K split over four waves.
 template <int FMT, int TERMS>
 hipError_t go_gate_up_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);
-  // Three waves per SIMD hold three workgroups of four waves, but one of eight.
-  constexpr int kHalf = min_waves<FMT, 1, TERMS>() == 4 ? 1 : 2;
-  if (t == 4) return go_gate_up<FMT, 1, TERMS, true, 1, 8 / kHalf>(a, max_tiles, s);
-  if (t == 16) return go_gate_up<FMT, 1, TERMS, false, 2, 4 / kHalf>(a, max_tiles, s);
-  return go_gate_up<FMT, 2, TERMS, false, 4, 2>(a, max_tiles, s);
+  if (t == 4) return go_gate_up<FMT, 2, 2, 1, TERMS, true, 2, 2>(a, max_tiles, s);
+  if (t == 16) return go_gate_up<FMT, 2, 2, 1, TERMS, false, 2, 2>(a, max_tiles, s);
+  return go_gate_up<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, max_tiles, s);
 }
 
 template <int FMT, int TERMS>
 hipError_t go_down_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);
-  if (t == 4) return go_down<FMT, 2, 2, 1, TERMS, true, 1, 4>(a, max_tiles, s);
-  constexpr int kHalf = min_waves<FMT, 1, TERMS>() == 4 ? 1 : 2;
-  if (t == 16) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4 / kHalf>(a, max_tiles, s);
+  if (t == 4) return go_down<FMT, 2, 2, 1, TERMS, true, 2, 2>(a, max_tiles, s);
+  if (t == 16) {
+    // 96 NVFP4 experts of 2560 x 1440, 64 tokens: 196 us against 226 with eight waves
+    // of four row tiles; 8 INT4 experts of 4096 x 4096, 33 tokens: 109 against 101.
+    if (FMT == kINT) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, max_tiles, s);
+    return go_down<FMT, 2, 2, 1, TERMS, false, 4, 1>(a, max_tiles, s);
+  }
   return go_down<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, max_tiles, s);
 }
 

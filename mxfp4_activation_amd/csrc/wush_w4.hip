@@ -60,24 +60,46 @@ hipError_t go(const LinearArgs& a, hipStream_t s) {
                     lds_bytes<R, D, NT, TERMS, WN, WK>(rows, a.K), s, a);
 }
 
+constexpr int64_t kLds = 163840;
+
+// Which shape of workgroup.  What counts is how many there are (256 compute
+// units want a few waves each), how many row tiles share the activations' way
+// through LDS, and that way's share of LDS.  Measured (us, best first):
+//   1 token:   4096 x 4096 MXFP4, one row tile, eight waves along K 4.2, two row
+//              tiles and four waves 6.2; 24576 x 4096 11.5 for the latter, 12.7.
+//   13 tokens: 5003 x 5136 NVFP4, two row tiles x one step 11.5, one row tile x two
+//              steps 14.3, four row tiles 26.7.
+//   16 tokens: 24576 x 4096 MXFP4, 2 x 2 waves 17.0, 1 x 8 27.4; two planes of
+//              activations, four row tiles 20.4, 2 x 2 waves 28.6.
+//   64 tokens: 4096 x 4096 MXFP4, four workgroups of 16 tokens for every 64 rows
+//              10.6, one of 64 tokens 41; 57344 x 8192 the latter 97.6, the
+//              former 254.
 template <int FMT, int TERMS>
 hipError_t go_tiles(const LinearArgs& a, hipStream_t s) {
+  const int64_t K = a.K, N = a.N;
+  const int rows = (int)(a.M < 16 ? a.M : 16);
   if (a.M <= 4) {
-    if (a.N > 8192) return go<FMT, 2, 2, 1, TERMS, true, 1, 4>(a, s);
-    if (FMT != kINT && lds_bytes<1, 4, 1, TERMS, 1, 8>((int)a.M, a.K) <= 65536)
-      return go<FMT, 1, 4, 1, TERMS, true, 1, 8>(a, s);
-    if (lds_bytes<1, 2, 1, TERMS, 1, 8>((int)a.M, a.K) <= 65536) return go<FMT, 1, 2, 1, TERMS, true, 1, 8>(a, s);
+    if (N > 12288) return go<FMT, 2, 2, 1, TERMS, true, 1, 4>(a, s);
+    if (lds_bytes<1, 2, 1, TERMS, 1, 8>(rows, K) <= kLds / 2) return go<FMT, 1, 2, 1, TERMS, true, 1, 8>(a, s);
     return go<FMT, 1, 1, 1, TERMS, true, 1, 8>(a, s);
   }
-  if (a.M <= 16) {
-    if (a.N > 16384) return go<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, s);
-    if (TERMS == 1) return go<FMT, 2, 1, 1, 1, false, 1, 8>(a, s);
-    return go<FMT, 2, 1, 1, TERMS, false, 1, 4>(a, s);
+  const int64_t all = N * ((a.M + 15) / 16);  // weight rows, once per token tile
+  if (all <= 4608 && lds_bytes<1, 2, 1, TERMS, 1, 8>(rows, K) <= kLds / 2)
+    return go<FMT, 1, 2, 1, TERMS, false, 1, 8>(a, s);
+  if (all <= 8192 && lds_bytes<2, 1, 1, TERMS, 1, 8>(rows, K) <= kLds)
+    return go<FMT, 2, 1, 1, TERMS, false, 1, 8>(a, s);
+  if (all <= 16384 && lds_bytes<2, 2, 1, TERMS, 2, 4>(rows, K) <= kLds)
+    return go<FMT, 2, 2, 1, TERMS, false, 2, 4>(a, s);
+  if (all <= 16384 || (a.M <= 16 && TERMS == 1)) return go<FMT, 2, 2, 1, TERMS, false, 2, 2>(a, s);
+  if (a.M <= 16) return go<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, s);
+  if constexpr (TERMS > 1) {
+    return go<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, s);
+  } else {
+    if (a.M <= 32) return go<FMT, 4, 1, 2, 1, false, 2, 4>(a, s);
+    if (N <= 16384 && lds_bytes<2, 1, 4, 1, 2, 4>((int)(a.M < 64 ? a.M : 64), K) <= kLds)
+      return go<FMT, 2, 1, 4, 1, false, 2, 4>(a, s);
+    return go<FMT, 2, 2, 4, 1, false, 8, 1>(a, s);
   }
-  if (a.M <= 32) return go<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, s);
-  if (TERMS == 3) return go<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, s);
-  if (a.N > 16384 && TERMS == 1) return go<FMT, 2, 2, 4, 1, false, 8, 1>(a, s);
-  return go<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, s);
 }
 
 template <int FMT>
