@@ -319,8 +319,7 @@ __device__ __forceinline__ bf16x8 expand(uint32_t d, float s) {
     // u = code + 8 in 0 .. 15 is, as an E4M3 byte, the number u * 2^-9 (up to
     // 7 as a subnormal, from 8 on with exponent 1); scaled by 2^9 the
     // conversion gives u.
-    const uint32_t u = d ^ 0x88888888u;
-    const uint32_t lo = u & 0x0F0F0F0Fu, hi = (u >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = (d & 0x0F0F0F0Fu) ^ 0x08080808u, hi = ((d >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
     const uint32_t p0 = __builtin_amdgcn_perm(hi, lo, 0x05010400u);  // elements 0 .. 3
     const uint32_t p1 = __builtin_amdgcn_perm(hi, lo, 0x07030602u);  // elements 4 .. 7
     r[0] = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(p0, 512.0f, false));
@@ -385,10 +384,13 @@ struct XAt {
 
 // acc += the wave's D steps.  x: the wave's first step in line 0 of the chunk; xo[t][p]:
 // where the lane reads term p of its row of token tile t.
-template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[R][NT], Raw<FMT, R, D>& w, const uint16_t* x,
+template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, typename A>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[R][NT], Raw<FMT, R, D>& w, A arrived, const uint16_t* x,
                                          const XAt (&xo)[NT][TERMS]) {
   const int q = (threadIdx.x & 63) >> 4;
+  // The last weights asked for, wanted here.
+  asm volatile("" : "+v"(w.s[Raw<FMT, R, D>::kShared ? 0 : R * D - 1][0]));
+  arrived();
   u32x2 sc[R * D];
   if constexpr (Raw<FMT, R, D>::kShared) {
     uint32_t lo[4], hi[4] = {0, 0, 0, 0};
@@ -510,11 +512,14 @@ inline int64_t lds_bytes(int rows, int64_t K) {
 // lane holds one result in the first component of D and INT4's scales cost one
 // multiplication per instruction rather than four.
 //
-// Order of a wave's requests from chunk 1 on: activations of chunk c + 1,
-// weights of chunk c; those of one chunk are in flight while the one before is
-// multiplied.  Loads complete in order, so a wave that has chunk c's weights
-// knows that its copies of chunk c + 1 have landed, and the barrier after chunk
-// c tells the others; arrive() does so for the first two.
+// A wave multiplies chunk c while the weights of chunk c + 1 are in flight.  Once
+// chunk c's are there it asks for the activations of chunk c + 2 (from the cache,
+// and into the buffer that chunk c - 1 left), after the chunk for the weights of
+// chunk c + 2.  Loads complete in order, and the compiler, which does not see the
+// copies, waits for chunk c + 1's weights until only those of chunk c + 2 are in
+// flight: by then the copies before these have landed, and the barrier after chunk
+// c + 1 tells the other waves.  (Asked for before the weights of chunk c + 1 were
+// there, the copies would be waited for with them, at full latency.)
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK, typename P, typename F>
 __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& p, P ready, F src, int64_t plane,
                                           int rows, int64_t K) {
@@ -576,14 +581,17 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
     if (tail) load_raw_tail(to, p, (int64_t)full * kSteps + step0, K);
   };
   auto dot = [&](Raw<FMT, R, D>& w, int c) {
-    multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, xw + (c % kBuffers) * buffer, xo);
+    const auto arrived = [&] {
+      if (c + 2 < chunks) copy_x(c + 2);
+    };
+    multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, arrived, xw + (c % kBuffers) * buffer, xo);
     meet();
   };
   auto dot_tail = [&](Raw<FMT, R, D>& w) {
     if (full == chunks) return;
     if (tail) {
       fix_tail(w, (int64_t)full * kSteps + step0, K);
-      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, xw + (full % kBuffers) * buffer, xo);
+      multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, [] {}, xw + (full % kBuffers) * buffer, xo);
     }
     meet();
   };
@@ -603,19 +611,16 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
   // c + 1.
   int c = 0;
   if (full > 1) {
-    if (chunks > 2) copy_x(2);
     load(w1, 1);
     arrive<R * D>();
     for (; c + 2 < full; c += 2) {
       dot(w0, c);
-      if (c + 3 < chunks) copy_x(c + 3);
       load(w0, c + 2);
       dot(w1, c + 1);
       if (c + 3 >= full) {
         c += 2;
         break;
       }
-      if (c + 4 < chunks) copy_x(c + 4);
       load(w1, c + 3);
     }
   } else {
