@@ -73,7 +73,9 @@ constexpr int64_t kLds = 163840;
 //              activations, four row tiles 20.4, 2 x 2 waves 28.6.
 //   64 tokens: 4096 x 4096 MXFP4, four workgroups of 16 tokens for every 64 rows
 //              10.6, one of 64 tokens 41; 57344 x 8192 the latter 97.6, the
-//              former 254.
+//              former 254.  24576 x 4096 workgroups of 32 tokens and four row
+//              pairs 32.1, of 64 tokens and eight 44.5; 57344 x 8192 134 for the
+//              former.
 template <int FMT, int TERMS>
 hipError_t go_tiles(const LinearArgs& a, hipStream_t s) {
   const int64_t K = a.K, N = a.N;
@@ -98,6 +100,7 @@ hipError_t go_tiles(const LinearArgs& a, hipStream_t s) {
     if (a.M <= 32) return go<FMT, 4, 1, 2, 1, false, 2, 4>(a, s);
     if (N <= 16384 && lds_bytes<2, 1, 4, 1, 2, 4>((int)(a.M < 64 ? a.M : 64), K) <= kLds)
       return go<FMT, 2, 1, 4, 1, false, 2, 4>(a, s);
+    if (N <= 32768) return go<FMT, 2, 2, 2, 1, false, 4, 1>(a, s);
     return go<FMT, 2, 2, 4, 1, false, 8, 1>(a, s);
   }
 }

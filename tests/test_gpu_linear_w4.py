@@ -67,6 +67,19 @@ def test_exact(fmt, M, N, K, transform):
     assert torch.equal(got16, got.to(torch.bfloat16))
 
 
+# Many weight rows for the same token counts: the shapes of workgroups that serve
+# those, each with a last workgroup that is not full.
+_WIDE = [(3, 12400, 64), (6, 4700, 288), (13, 8200, 160), (12, 16500, 64), (16, 8200, 2080), (24, 8300, 96),
+         (50, 4200, 160), (50, 16500, 64), (40, 33000, 32)]
+
+
+@pytest.mark.parametrize("transform", [False, True])
+@pytest.mark.parametrize("M,N,K", _WIDE)
+@pytest.mark.parametrize("fmt", dc.FMTS)
+def test_exact_wide(fmt, M, N, K, transform):
+    test_exact(fmt, M, N, K, transform)
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("transform", [False, True])
 @pytest.mark.parametrize("M,N,K", [(1, 257, 2048), (4, 100, 5120), (20, 130, 1504), (64, 96, 1024)])
