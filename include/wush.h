@@ -351,7 +351,9 @@ wush_status wush_f64_to_bf16(const double* src, int64_t n, void* dst, hipStream_
  * without T, or the block transform T_c x_c of the format's group size G (as
  * in wush_transform_f32) for weights quantized with the matching weight-side
  * transform.  Products are exact, sums fp32; x' is kept to 16 significant bits for a
- * bf16 Y and to fp32 accuracy for an fp32 Y.
+ * bf16 Y and to fp32 accuracy for an fp32 Y.  A row of X with an infinity or a NaN
+ * has no finite result (NaN also where the sum would be an infinity) and leaves
+ * the other rows alone; T x has to lie within bf16's range.
  *   X: bf16 [M][K], row m at X + m * ldx elements (ldx >= K, a multiple of 8;
  *      16-byte aligned).  T: bf16 [K/G][G][G], 16-byte aligned, or NULL.
  *   codes u8 [N][K/2], 8-byte aligned; scales [N][K/G] (fp16 for INT4).
@@ -385,7 +387,7 @@ int64_t wush_linear_w4_workspace(int64_t M, int64_t K, int out_type);
  * H and I are positive multiples of G, at most 2^24; 1 <= E <= 1024;
  * 1 <= topk <= min(E, 32).  M >= 0; tokens are taken 64 at a time.  A NaN
  * logit ranks below every number; results are then NaN but all accesses stay in
- * range.
+ * range.  A token that is not finite leaves the others alone.
  * Results repeat bit for bit.  transform: whether T_in is given. */
 wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router, const void* gate_up_codes,
                         const void* gate_up_scales, const float* gate_up_global, const void* T_in,

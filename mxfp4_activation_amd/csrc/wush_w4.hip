@@ -13,6 +13,11 @@ namespace {
 using namespace w4;
 
 // ------------------------------------------------------------ transform
+//
+// x' = T x once per call, as bf16 planes (split_panel), rather than by every
+// workgroup that reads x': at 24576 weight rows there are 768 of them.  Each wave
+// takes 32 channels of 16 tokens, so that one token still has K / 32 waves.  Bound
+// by its latency: 4.1 us for 4 tokens of 4096, which read 0.3 MB.
 __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
   const int64_t panel = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (panel * 32 < a.K) split_panel(a, panel, (int64_t)blockIdx.y * 16);
@@ -20,7 +25,16 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 
 // ------------------------------------------------------------ linear
 //
-// A workgroup owns 16 R WN weight rows and up to 16 NT tokens.
+// A workgroup owns 16 R WN weight rows and up to 16 NT tokens; group_dot
+// (wush_w4_core.h) says how it multiplies.  Bound by the weights' way in where tokens are
+// few, and behind that by unpacking them, which every workgroup does once per 16 NT
+// tokens: NT grows with the tokens.  Measured without T:
+//   1 token:   4096 x 4096 MXFP4 4.2 us (2.1 TB/s: a launch and two round trips to
+//              memory), 24576 x 4096 11.5 us (4.7 TB/s), 8192 x 28672 26.2 us (4.8 TB/s),
+//              INT4 39 us with T (3.4 TB/s; sums per group cost instructions)
+//   13 tokens: 5003 x 5136 NVFP4 11.1 us (1.3 TB/s: 157 workgroups for 256 compute units)
+//   64 tokens: 57344 x 8192 MXFP4 97 us (615 TFLOP/s, 2.6 TB/s: vector and matrix
+//              instructions take turns)
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
 __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void linear_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];

@@ -215,3 +215,25 @@ def test_side_stream_and_graph_replay():
         graph.replay()
         assert torch.equal(y, eager[turn])
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("transform", [False, True])
+@pytest.mark.parametrize("M,K", [(3, 32), (4, 160), (7, 1056), (20, 160), (40, 2080)])
+@pytest.mark.parametrize("fmt", dc.FMTS)
+def test_not_finite_rows_stay_their_own(fmt, M, K, transform):
+    """Rows with an infinity or a NaN anywhere, also where a step ends past K, have
+    no finite result; every other row is exact."""
+    rng = np.random.default_rng(M + K)
+    G, N = decode.GROUP[fmt], 50
+    codes, scales = dc.weights(rng, fmt, (N,), K, exact=True)
+    x, xb = dc.bf16(rng.integers(-3, 4, size=(M, K)))
+    T = np.tile(np.eye(G), (K // G, 1, 1))
+    bad = {0: (0, 0x7F80), M // 2: (K - 1, 0xFF80), M - 1: (K // 2, 0x7FC0)}
+    for row, (k, bits) in bad.items():
+        xb[row, k] = bits
+    gs = 1.0 if fmt == "nvfp4" else None
+    want, _ = decode.linear(x, codes, scales, fmt, None, gs)
+    got = dc.values(_call(fmt, xb, codes, scales, dc.bf16(T)[1] if transform else None, gs))
+    keep = [m for m in range(M) if m not in bad]
+    assert not np.isfinite(got[sorted(bad)]).any()
+    assert np.array_equal(got[keep], want[keep])
