@@ -104,7 +104,7 @@ MoeWorkspace moe_workspace(int64_t M, int64_t E, int topk, int64_t H, int64_t I,
   w.h = w.planes + (transform ? round16(terms * c * H * 2) : 0);
   w.part = w.h + round16(terms * slots * I * 2);
   w.logits = w.part + round16(slots * H * 4);
-  w.n_tiles = w.logits + round16(c * E * 4);
+  w.n_tiles = w.logits + round16(wush::kRouterParts * c * E * 4);
   w.tiles = w.n_tiles + 16;
   // A tile holds at least one slot.
   w.total = w.tiles + slots * sizeof(wush::MoeTile);

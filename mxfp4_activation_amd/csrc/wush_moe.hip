@@ -18,44 +18,47 @@ using namespace w4;
 
 // ------------------------------------------------------------ router
 //
-// Logits of 16 experts for 16 tokens per workgroup, K split over the waves.  The
-// workgroups behind those transform: each wave 32 channels of 16 tokens (one launch
-// for two things that need x alone).  Bound by latency: one token, 64 experts of
-// 2048: 3.9 us; 64 tokens, 96 experts of 2560: 5.2 us, for half a megabyte.  Sixteen
-// waves per workgroup, since all of a wave's loads are one round trip to memory.
-constexpr int kRouterWaves = 16;
+// Logits of 16 experts for 16 tokens: K is split over the waves of kRouterParts
+// workgroups, whose sums the choice adds up in order.  The workgroups behind those
+// transform: each wave 32 channels of 16 tokens (one launch for two things that
+// need x alone).  Bound by the latency of reading the router, one round trip to memory
+// where a compute unit has few lines to fetch: 8 tokens, 128 experts of 4096 5.0 us
+// with four workgroups of eight waves per 16 experts, the same with eight of four, 8.5
+// with one of sixteen (8 workgroups for 1 MB); the whole call 107 us against 110.
+constexpr int kRouterWaves = 8, kRouterSlices = kRouterWaves * kRouterParts;
 
-__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a, int router_tiles) {
+__global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a, int router_groups) {
   __shared__ float red[kRouterWaves][16][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, q = lane >> 4;
   const int m0 = blockIdx.y * 16;
-  if ((int)blockIdx.x >= router_tiles) {
-    const int64_t panel = (int64_t)(blockIdx.x - router_tiles) * kRouterWaves + wave;
+  if ((int)blockIdx.x >= router_groups) {
+    const int64_t panel = (int64_t)(blockIdx.x - router_groups) * kRouterWaves + wave;
     if (panel * 32 < a.H)
       split_panel(SplitArgs{a.X, a.ldx, a.T_in, a.xt, a.M, a.H, a.fmt == kNV ? 16 : 32, a.terms}, panel, m0);
     return;
   }
-  const int e0 = blockIdx.x * 16;
+  const int e0 = blockIdx.x / kRouterParts * 16, part = blockIdx.x % kRouterParts;
+  const int slice = part * kRouterWaves + wave;
   const int rows = a.M - m0 < 16 ? a.M - m0 : 16;
   const int e = e0 + n < a.E ? e0 + n : a.E - 1;
   const uint16_t* w = a.router + (int64_t)e * a.H + 8 * q;
   const uint16_t* x = a.X + (int64_t)(m0 + (n < rows ? n : 0)) * a.ldx + 8 * q;
   f32x4 acc = {0, 0, 0, 0};
   const int vecs = (int)(a.H / 32);  // instructions of 32 elements; H may end in half of one
-  constexpr int kBatch = 8;          // their loads are on their way together
-  for (int i0 = wave; i0 < vecs; i0 += kBatch * kRouterWaves) {
+  constexpr int kBatch = 4;          // their loads are on their way together
+  for (int i0 = slice; i0 < vecs; i0 += kBatch * kRouterSlices) {
     bf16x8 xv[kBatch], wv[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * kRouterWaves, at = 32 * (i < vecs ? i : wave);
+      const int i = i0 + b * kRouterSlices, at = 32 * (i < vecs ? i : slice);
       xv[b] = *reinterpret_cast<const bf16x8*>(x + at);
       wv[b] = *reinterpret_cast<const bf16x8*>(w + at);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
-      if (i0 + b * kRouterWaves < vecs) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[b], wv[b], acc, 0, 0, 0);
+      if (i0 + b * kRouterSlices < vecs) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[b], wv[b], acc, 0, 0, 0);
   }
-  if (a.H % 32 != 0 && wave == vecs % kRouterWaves) {
+  if (a.H % 32 != 0 && slice == vecs % kRouterSlices) {
     u32x4 xv = {0, 0, 0, 0}, wv = {0, 0, 0, 0};
     if (q < 2) {
       xv = *reinterpret_cast<const u32x4*>(x + 32 * vecs);
@@ -72,7 +75,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(MoeArgs a, in
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < kRouterWaves; ++k) v += red[k][m][c];
-    if (m < rows && e0 + c < a.E) a.logits[(int64_t)(m0 + m) * a.E + e0 + c] = v;
+    if (m < rows && e0 + c < a.E) a.logits[((int64_t)part * a.M + m0 + m) * a.E + e0 + c] = v;
   }
 }
 
@@ -99,7 +102,10 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int m0, int (&id)[B], f
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int e = lane + 64 * j, m = m0 + b < a.M ? m0 + b : m0;
-      l[b][j] = a.logits[(int64_t)m * a.E + (e < a.E ? e : 0)];
+      const float* at = a.logits + (int64_t)m * a.E + (e < a.E ? e : 0);
+      l[b][j] = at[0];
+#pragma unroll
+      for (int k = 1; k < kRouterParts; ++k) l[b][j] += at[(int64_t)k * a.M * a.E];
     }
 #pragma unroll
   for (int b = 0; b < B; ++b) {
@@ -453,10 +459,10 @@ hipError_t go_experts(const MoeArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_moe(const MoeArgs& a, hipStream_t s) {
-  const int router_tiles = (a.E + 15) / 16;
+  const int router_groups = (a.E + 15) / 16 * kRouterParts;
   const int64_t split = a.T_in ? (a.H + 32 * kRouterWaves - 1) / (32 * kRouterWaves) : 0;
-  hipLaunchKernelGGL(router_kernel, dim3((unsigned)(router_tiles + split), (unsigned)((a.M + 15) / 16)),
-                     dim3(64 * kRouterWaves), 0, s, a, router_tiles);
+  hipLaunchKernelGGL(router_kernel, dim3((unsigned)(router_groups + split), (unsigned)((a.M + 15) / 16)),
+                     dim3(64 * kRouterWaves), 0, s, a, router_groups);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tokens = tile_tokens(a);

@@ -43,6 +43,7 @@ struct LinearArgs {
 constexpr int kMoeTokens = 64;
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
+constexpr int kRouterParts = 4;  // workgroups that share a row of the router
 
 // Tokens of one expert that share a pass over its weights.
 struct MoeTile {
@@ -72,7 +73,7 @@ struct MoeArgs {
   float* weights;           // [M][topk]
   // Workspace.
   uint16_t* xt;             // [terms][M][H], if T_in
-  float* logits;            // [M][E]
+  float* logits;            // [kRouterParts][M][E], to be summed
   uint16_t* h;              // [terms][M * topk][I]
   float* part;              // [M * topk][H]
   int32_t* n_tiles;
