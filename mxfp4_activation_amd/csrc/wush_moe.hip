@@ -422,7 +422,9 @@ int tile_tokens(const MoeArgs& a) {
 // Four waves of two row tiles and two steps each.  Measured on 128 experts of
 // 4096 x 1280 MXFP4 with transforms, 8 tokens (the whole call): 122 us, against 133
 // with eight waves of four row tiles that split K, and 144 with four of those;
-// down 124 against 132 with K split over four waves.
+// down 124 against 132 with K split over four waves.  (Both sides of these and of the
+// next were timed in turn in one state of the rest; the calls now take 107, 170 and
+// 87 us.)
 template <int FMT, int TERMS>
 hipError_t go_gate_up_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);
