@@ -79,6 +79,9 @@ template <int FMT, int R, int D>
 struct Raw {
   static constexpr int kUnits = R * D;
   static constexpr bool kShared = kUnits == 4;
+  // Loads that it takes at least (two steps' scales of a row are neighbours, and may
+  // come as one).
+  static constexpr int kLoads = kUnits + (kShared ? 1 : R);
   u32x4 c[kUnits];
   u32x2 s[kShared ? 1 : kUnits];  // 4 E8M0 bytes, 8 E4M3 bytes or 4 fp16
 };
@@ -153,60 +156,66 @@ __device__ __forceinline__ void load_raw(Raw<FMT, R, D>& w, const Rows<FMT, R, D
   }
 }
 
-// D steps of which some reach past K: nothing is read past a row, and what is
-// missing is zero.  From K = 128 on, the loads depend on no condition (their addresses
-// do), so that fix_tail can be left until the weights are needed.
+// D steps of which some reach past K, which is 128 or more: nothing is read past a
+// row, and what is missing is zero once fix_tail has run.  The loads depend on no
+// condition (their addresses do), so that fix_tail can be left until the weights are
+// needed.
 template <int FMT, int R, int D>
 __device__ __forceinline__ void load_raw_tail(Raw<FMT, R, D>& w, const Rows<FMT, R, D>& p, int64_t st, int64_t K) {
   using RawT = Raw<FMT, R, D>;
   constexpr int kStepBytes = FMT == kMX ? 4 : 8;
   const int q = (threadIdx.x & 63) >> 4;
   const int64_t row_scales = row_scale_bytes<FMT>(K);
-  if (K >= kStep) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        // The lane's 16 bytes, or the row's last 16 if they reach past it.
-        const int64_t last = K / 2 - 16 - 16 * q, at = 64 * (st + d);
-        w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + (at < last ? at : last) + p.off[r]);
-      }
-    // sp points at this step's bytes; not past the row's last kStepBytes.
-    auto back = [&](int64_t step) {
-      const int64_t over = kStepBytes * (step + 1) - row_scales;
-      return over > 0 ? over : 0;
-    };
-    if constexpr (RawT::kShared) {
-      w.s[0] = load_scales<FMT>(p.sp[0] - back(st + q % D), st);
-    } else {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int d = 0; d < D; ++d) w.s[r * D + d] = load_scales<FMT>(p.sp[r] - back(st + d), st + d);
-    }
-    return;
-  }
-  // One partial step is all there is.
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int64_t k = (st + d) * kStep + 32 * q;
+      // The lane's 16 bytes, or the row's last 16 if they reach past it.
+      const int64_t last = K / 2 - 16 - 16 * q, at = 64 * (st + d);
+      w.c[r * D + d] = load_unaligned<u32x4>(p.cp[r] + (at < last ? at : last) + p.off[r]);
+    }
+  // sp points at this step's bytes; not past the row's last kStepBytes.
+  auto back = [&](int64_t step) {
+    const int64_t over = kStepBytes * (step + 1) - row_scales;
+    return over > 0 ? over : 0;
+  };
+  if constexpr (RawT::kShared) {
+    w.s[0] = load_scales<FMT>(p.sp[0] - back(st + q % D), st);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int d = 0; d < D; ++d) w.s[r * D + d] = load_scales<FMT>(p.sp[r] - back(st + d), st + d);
+  }
+}
+
+// The only step, the wave's first, where K is less than 128.
+template <int FMT, int R, int D>
+__device__ __forceinline__ void load_raw_short(Raw<FMT, R, D>& w, const Rows<FMT, R, D>& p, int64_t K) {
+  using RawT = Raw<FMT, R, D>;
+  constexpr int kStepBytes = FMT == kMX ? 4 : 8;
+  const int q = (threadIdx.x & 63) >> 4;
+  const int64_t row_scales = row_scale_bytes<FMT>(K);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int64_t k = d * kStep + 32 * q;
       u32x4 c = {0, 0, 0, 0};
       if (k + 32 <= K) {
-        c = load_unaligned<u32x4>(p.cp[r] + 64 * (st + d) + p.off[r]);
+        c = load_unaligned<u32x4>(p.cp[r] + p.off[r]);
       } else if (FMT == kNV && k + 16 <= K) {
-        const u32x2 h = load_unaligned<u32x2>(p.cp[r] + 64 * (st + d) + p.off[r]);
+        const u32x2 h = load_unaligned<u32x2>(p.cp[r] + p.off[r]);
         c[0] = h[0];
         c[1] = h[1];
       }
       w.c[r * D + d] = c;
     }
-  auto scales = [&](const uint8_t* sp, int64_t first, int64_t step) {
+  auto scales = [&](const uint8_t* sp, int d) {
     u32x2 s = {0, 0};
-    if (step == 0) {
+    if (d == 0) {
       for (int b = 0; b < row_scales; ++b) {
-        const uint32_t v = (uint32_t)sp[kStepBytes * first + b] << (8 * (b % 4));
+        const uint32_t v = (uint32_t)sp[b] << (8 * (b % 4));
         if (b < 4) {
           s[0] |= v;
         } else {
@@ -217,12 +226,12 @@ __device__ __forceinline__ void load_raw_tail(Raw<FMT, R, D>& w, const Rows<FMT,
     return s;
   };
   if constexpr (RawT::kShared) {
-    w.s[0] = scales(p.sp[0] - kStepBytes * (q % D), st, st + q % D);
+    w.s[0] = scales(p.sp[0], q % D);
   } else {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int d = 0; d < D; ++d) w.s[r * D + d] = scales(p.sp[r], st + d, st + d);
+      for (int d = 0; d < D; ++d) w.s[r * D + d] = scales(p.sp[r], d);
   }
 }
 
@@ -370,6 +379,13 @@ __device__ __forceinline__ void arrive() {
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// This wave's copies have landed, given that at least N loads of weights were
+// requested after them.
+template <int N>
+__device__ __forceinline__ void landed() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // All of this wave's LDS reads are done, then the workgroup meets.  Loads
 // and copies in flight stay in flight.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -515,11 +531,14 @@ inline int64_t lds_bytes(int rows, int64_t K) {
 // A wave multiplies chunk c while the weights of chunk c + 1 are in flight.  Once
 // chunk c's are there it asks for the activations of chunk c + 2 (from the cache,
 // and into the buffer that chunk c - 1 left), after the chunk for the weights of
-// chunk c + 2.  Loads complete in order, and the compiler, which does not see the
-// copies, waits for chunk c + 1's weights until only those of chunk c + 2 are in
-// flight: by then the copies before these have landed, and the barrier after chunk
-// c + 1 tells the other waves.  (Asked for before the weights of chunk c + 1 were
-// there, the copies would be waited for with them, at full latency.)
+// chunk c + 2.  Loads complete in order: when in chunk c + 1 only these weights are
+// still in flight (landed), the copies before them have arrived, and the barrier after
+// chunk c + 1 tells the other waves.  That wait is written out, for the compiler does
+// not see the copies: where its own waits leave nothing of chunk c + 1 to wait for, it
+// has none there.  After the last whole chunk every wave waits for all that it asked
+// for: a wave without a part in what remains loads no weights behind its copies of
+// that.  (Asked for before the weights of chunk c + 1 were there, the copies would be
+// waited for with them, at full latency.)
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK, typename P, typename F>
 __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& p, P ready, F src, int64_t plane,
                                           int rows, int64_t K) {
@@ -582,9 +601,15 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
   };
   auto dot = [&](Raw<FMT, R, D>& w, int c) {
     const auto arrived = [&] {
+      landed<Raw<FMT, R, D>::kLoads>();  // chunk c + 1's copies
       if (c + 2 < chunks) copy_x(c + 2);
     };
     multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, arrived, xw + (c % kBuffers) * buffer, xo);
+    meet();
+  };
+  auto dot_last = [&](Raw<FMT, R, D>& w) {  // of the whole chunks
+    multiply<FMT, R, D, NT, TERMS, SPREAD>(acc, w, [] {}, xw + ((full - 1) % kBuffers) * buffer, xo);
+    landed<0>();  // the copies of what remains; weights of it are wanted next
     meet();
   };
   auto dot_tail = [&](Raw<FMT, R, D>& w) {
@@ -599,8 +624,10 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
   // known of those.
   if (full > 0) {
     load(w0, 0);
-  } else {
+  } else if (K >= kStep) {
     load_tail(w0);
+  } else if (tail) {
+    load_raw_short(w0, p, K);
   }
   ready();
   copy_x(0);
@@ -628,16 +655,17 @@ __device__ __forceinline__ void group_dot(uint16_t* lds, const Rows<FMT, R, D>& 
   }
   if (full > 0 && c + 1 == full) {
     load_tail(w1);
-    dot(w0, c);
+    dot_last(w0);
     dot_tail(w1);
   } else {
     if (full > 0) {
       dot(w0, c);
       load_tail(w0);
-      dot(w1, c + 1);
+      dot_last(w1);
     }
     dot_tail(w0);
   }
+  landed<0>();  // nothing is left on its way into what the sums take
   float* red = reinterpret_cast<float*>(lds) + wave * (R * 16 * rows);
 #pragma unroll
   for (int r = 0; r < R; ++r)
