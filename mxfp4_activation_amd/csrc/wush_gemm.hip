@@ -122,7 +122,9 @@ typedef const __attribute__((address_space(1))) uint8_t glb_u8;
 
 // Global-to-LDS copies of 16 and 4 bytes per lane to LDS address `dst`
 // (wave-uniform; lane l writes at dst + l * size).  The copy takes its LDS
-// base from M0.  M0 is declared clobbered; the compiler reserves M0 and
+// base from M0; the hardware wants one wait state between a scalar write of M0
+// and a load to LDS, which the compiler does not put inside a statement.  M0 is
+// declared clobbered; the compiler reserves M0 and
 // warns that it does not preserve it across the statement, which is safe
 // here because nothing else in these kernels uses M0 (the only M0 writes in
 // their code are these).  The statements have no outputs, so no register
@@ -130,10 +132,10 @@ typedef const __attribute__((address_space(1))) uint8_t glb_u8;
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(glb_u8* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(glb_u8* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 

@@ -364,11 +364,13 @@ typedef const __attribute__((address_space(1))) uint16_t glb_u16;
 // Global-to-LDS copy of 16 bytes per lane to LDS byte address dst (uniform;
 // lane l writes at dst + 16 l), outside the compiler's view: it would wait for
 // every copy in flight before any LDS read.  The copy takes its LDS base from
-// M0, which nothing else in these kernels uses.  The statement has no outputs.
+// M0, which nothing else in these kernels uses; between a scalar write of M0 and a
+// load to LDS the hardware wants one wait state, which the compiler does not put
+// inside a statement.  The statement has no outputs.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16(glb_u16* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
