@@ -80,12 +80,16 @@ def _scale_dtype(fmt: str):
     return torch.float16 if fmt == "int4" else torch.uint8
 
 
-def _check_global(fmt: str, g, name: str, n: int, dev) -> Optional[int]:
+def _check_global(fmt: str, g, name: str, n: int, dev):
+    """(address of the tensor scales, their flat tensor, which the caller holds until
+    the call is enqueued: it is a copy where g cannot be viewed flat)."""
     if fmt != "nvfp4":
-        return None
+        return None, None
     if g is None:
         raise ValueError("nvfp4 needs %s, a float32 tensor of %d element%s" % (name, n, "" if n == 1 else "s"))
-    return _check(g if g.dim() == 1 else g.reshape(-1), name, torch.float32, (n,), dev)
+    if g.dim() != 1:
+        g = g.reshape(-1)
+    return _check(g, name, torch.float32, (n,), dev), g
 
 
 def _workspace(n: int, dev):
@@ -109,7 +113,7 @@ def linear_w4(fmt: str, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     N = codes.shape[0]
     pc = _check(codes, "codes", torch.uint8, (N, K // 2), dev)
     ps = _check(scales, "scales", _scale_dtype(fmt), (N, K // G), dev)
-    pg = _check_global(fmt, global_scale, "global_scale", 1, dev)
+    pg, global_scale = _check_global(fmt, global_scale, "global_scale", 1, dev)
     pt = None if T is None else _check(T, "T", torch.bfloat16, (K // G, G, G), dev)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
@@ -163,10 +167,10 @@ def moe_w4(fmt: str, x: torch.Tensor, router: torch.Tensor, gate_up: W4Experts, 
     pr = _check(router, "router", torch.bfloat16, (E, H), dev)
     pgc = _check(gate_up.codes, "gate_up.codes", torch.uint8, (E, 2 * I, H // 2), dev)
     pgs = _check(gate_up.scales, "gate_up.scales", sdt, (E, 2 * I, H // G), dev)
-    pgg = _check_global(fmt, gate_up.global_scale, "gate_up.global_scale", E, dev)
+    pgg, gate_up_global = _check_global(fmt, gate_up.global_scale, "gate_up.global_scale", E, dev)
     pdc = _check(down.codes, "down.codes", torch.uint8, (E, H, I // 2), dev)
     pds = _check(down.scales, "down.scales", sdt, (E, H, I // G), dev)
-    pdg = _check_global(fmt, down.global_scale, "down.global_scale", E, dev)
+    pdg, down_global = _check_global(fmt, down.global_scale, "down.global_scale", E, dev)
     pti = None if gate_up.T is None else _check(gate_up.T, "gate_up.T", torch.bfloat16, (H // G, G, G), dev)
     ptm = None if down.T is None else _check(down.T, "down.T", torch.bfloat16, (E, I // G, G, G), dev)
     if out is None:
