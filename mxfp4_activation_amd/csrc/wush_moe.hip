@@ -242,7 +242,7 @@ hipError_t go_route(const MoeArgs& a, int tile_tokens, hipStream_t s) {
 // experts of 4096 x 4096, 33 tokens: 44 us (3.4 TB/s); 96 NVFP4 experts of 2560 x
 // 1440, 64 tokens: 98 us (4.0 TB/s).
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void gate_up_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) void gate_up_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   __shared__ int slot[16 * NT], token[16 * NT];
   constexpr int kThreads = 64 * WN * WK, kWaveChannels = 8 * R, kChannels = kWaveChannels * WN, kRows = SPREAD ? 4 : 16 * NT;
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void g
 // order would change results).  Bound as gate and up: 36, 32 and 63 us on the same
 // three (3.9, 2.4 and 3.1 TB/s: rows are short or the weights INT4).
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) void down_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   __shared__ int slot[16 * NT];
   constexpr int kThreads = 64 * WN * WK, kChannels = 16 * R * WN;

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 //              for each other's chunks; matrix cores 25% busy; 87 us of it remain at
 //              17 tokens)
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, NT, TERMS>())) void linear_kernel(LinearArgs a) {
+__global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) void linear_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
   constexpr int kRows = 16 * R * WN;
   const int wn = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WN;

@@ -502,10 +502,12 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[R][NT], Raw<FMT, R, D>& w,
 constexpr int kBuffers = 3;  // activation chunks in LDS
 
 // Waves per SIMD that the registers are cut for: four where the code fits 128
-// without spilling, otherwise three (168) or, with several token tiles, two.
-template <int FMT, int NT, int TERMS>
+// without spilling, otherwise three (168), or two with several token tiles and for four
+// row tiles of INT4 on three planes, which take 172.  (Those workgroups are eight
+// waves: three waves per SIMD would be one workgroup per compute unit as well.)
+template <int FMT, int R, int NT, int TERMS>
 constexpr int min_waves() {
-  return NT > 1 ? 2 : FMT == kMX || (FMT == kNV && TERMS == 1) ? 4 : 3;
+  return NT > 1 || (FMT == kINT && R == 4 && TERMS == 3) ? 2 : FMT == kMX || (FMT == kNV && TERMS == 1) ? 4 : 3;
 }
 
 // LDS of one workgroup in bytes: the activation buffers, or the sums that meet at

@@ -80,3 +80,14 @@ def functions(tmp_path) -> Dict[str, List[Instruction]]:
                 target = address + 4 + 4 * (words - 65536 if words >= 32768 else words)
             body.append(Instruction(address, op, args, target))
     return out
+
+
+def metadata() -> Dict[str, Dict[str, int]]:
+    """What the compiler notes of every kernel (registers, spills, scratch) by its (mangled) name."""
+    tool, out = os.path.join(os.path.dirname(objdump()), "llvm-readelf"), {}
+    for code in code_objects():
+        text = subprocess.run([tool, "--notes", "-"], input=code, capture_output=True, check=True).stdout.decode()
+        for part in text.split("  - .agpr_count:")[1:]:
+            name = re.search(r"^    \.name:\s+(\S+)", part, re.M).group(1)
+            out[name] = {k: int(v) for k, v in re.findall(r"^    \.(\w+):\s+(\d+)$", part, re.M)}
+    return out
