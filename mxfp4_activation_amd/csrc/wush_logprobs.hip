@@ -21,21 +21,14 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-// Elements per thread and batch: 32 where there are rows or batches enough to
-// fill the chip, otherwise 8.
-constexpr int kWide = 32, kNarrow = 8;
-constexpr int kMaxSplits = 64;
+constexpr int kThreads = kLogprobThreads, kWaves = kThreads / 64;
+constexpr int kWide = kLogprobWide, kNarrow = kLogprobNarrow;
 // Candidates of one batch: at most `top` threads hold any (see keep_largest),
 // besides the entries kept so far; padded for rank_candidates.
 template <int PER>
 constexpr int kMaxCandidates = kLogprobMaxTop * PER + kLogprobMaxTop + 8;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
-
-// Workgroups that a launch should have.
-constexpr int64_t kTargetGroups = 1024;
-inline bool narrow(int64_t R, int64_t V) { return R * ((V + kThreads * kWide - 1) / (kThreads * kWide)) < kTargetGroups / 2; }
 
 struct Triple {
   float m, s, u;
@@ -388,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(LogprobArgs a) {
   }
   const TopState<kWide>* top = nullptr;
   if constexpr (TOP) {
-    static_assert(kMaxSplits == 64, "one wave holds a row's splits");
+    static_assert(kLogprobMaxSplits == 64, "one wave holds a row's splits");
     static_assert(kLogprobMaxTop * kLogprobMaxTop + 8 <= kMaxCandidates<kWide>, "the candidates must fit");
     const uint64_t* keys = a.keys + row * a.splits * a.top;
     const int n = a.splits * a.top;
@@ -415,7 +408,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(LogprobArgs a) {
 template <int TYPE, bool TOP>
 hipError_t go(const LogprobArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.R, (unsigned)a.splits);
-  if (narrow(a.R, a.V)) {
+  if (logprob_narrow(a.R, a.V)) {
     hipLaunchKernelGGL((logprob_kernel<TYPE, TOP, kNarrow>), grid, dim3(kThreads), 0, s, a);
   } else {
     hipLaunchKernelGGL((logprob_kernel<TYPE, TOP, kWide>), grid, dim3(kThreads), 0, s, a);
@@ -427,19 +420,6 @@ hipError_t go(const LogprobArgs& a, hipStream_t s) {
 }
 
 }  // namespace
-
-LogprobPlan logprob_plan(int64_t R, int64_t V) {
-  const int64_t per = kThreads * (narrow(R, V) ? kNarrow : kWide);
-  const int64_t batches = (V + per - 1) / per;
-  int64_t s = kTargetGroups / (R > 0 ? R : 1);
-  if (s > batches) s = batches;
-  if (s > kMaxSplits) s = kMaxSplits;
-  if (s < 1) s = 1;
-  // Whole batches per split; the last split also has the batch that an
-  // unaligned row start may add.
-  const int64_t each = (batches + s - 1) / s;
-  return LogprobPlan{(int)((batches + each - 1) / each), (int)each};
-}
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {
   if (a.type == 0) return a.top ? go<0, true>(a, s) : go<0, false>(a, s);

@@ -104,11 +104,32 @@ struct LogprobArgs {
   uint64_t* keys;          // [R][splits][top], if splits > 1
 };
 
+// Elements per thread and batch: 32 where there are rows or batches enough to
+// fill the chip, otherwise 8.
+constexpr int kLogprobThreads = 256, kLogprobWide = 32, kLogprobNarrow = 8;
+constexpr int kLogprobMaxSplits = 64;
+// Workgroups that a launch should have.
+constexpr int64_t kLogprobGroups = 1024;
+inline bool logprob_narrow(int64_t R, int64_t V) {
+  return R * ((V + kLogprobThreads * kLogprobWide - 1) / (kLogprobThreads * kLogprobWide)) < kLogprobGroups / 2;
+}
+
 // Workgroups per row (1: no workspace), and batches of each.
 struct LogprobPlan {
   int splits, split_batches;
 };
-LogprobPlan logprob_plan(int64_t R, int64_t V);
+inline LogprobPlan logprob_plan(int64_t R, int64_t V) {
+  const int64_t per = kLogprobThreads * (logprob_narrow(R, V) ? kLogprobNarrow : kLogprobWide);
+  const int64_t batches = (V + per - 1) / per;
+  int64_t s = kLogprobGroups / (R > 0 ? R : 1);
+  if (s > batches) s = batches;
+  if (s > kLogprobMaxSplits) s = kLogprobMaxSplits;
+  if (s < 1) s = 1;
+  // Whole batches per split; the last split also has the batch that an
+  // unaligned row start may add.
+  const int64_t each = (batches + s - 1) / s;
+  return LogprobPlan{(int)((batches + each - 1) / each), (int)each};
+}
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
 
 }  // namespace wush
