@@ -46,6 +46,7 @@ uint64_t scale_bytes(int fmt, int64_t rows, int64_t K) {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxK = (int64_t)1 << 27;
+constexpr int64_t kMaxLogprobRows = (int64_t)1 << 24;
 
 wush_status check_fmt(int fmt, int out_type) {
   if (fmt != wush::kMXFP4 && fmt != wush::kNVFP4 && fmt != wush::kINT4)
@@ -292,8 +293,8 @@ wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router,
 }
 
 int64_t wush_token_logprobs_workspace(int64_t R, int64_t V, int logit_type, int top) {
-  if (R <= 0 || V <= 0 || V > INT32_MAX || logit_type < 0 || logit_type > 2 || top < 0 || top > wush::kLogprobMaxTop)
-    return 0;
+  if (R <= 0 || R > kMaxLogprobRows || V <= 0 || V > INT32_MAX) return 0;
+  if (logit_type < 0 || logit_type > 2 || top < 0 || top > wush::kLogprobMaxTop) return 0;
   const int64_t s = wush::logprob_plan(R, V).splits;
   return s == 1 ? 0 : R * s * (16 + 8 * (int64_t)top);
 }
@@ -309,7 +310,7 @@ wush_status wush_token_logprobs(const void* logits, int logit_type, int64_t ld, 
   if (top < 0 || top > wush::kLogprobMaxTop)
     return fail(WUSH_EINVAL, "top must be 0 .. %d (got %d)", wush::kLogprobMaxTop, top);
   if (R == 0) return WUSH_OK;
-  if (R > (int64_t)1 << 24) return fail(WUSH_EINVAL, "R too large for one launch");
+  if (R > kMaxLogprobRows) return fail(WUSH_EINVAL, "R too large for one launch");
   if (R > 1 && (ld < V || ld > ((int64_t)1 << 36))) return fail(WUSH_EINVAL, "ld must be V or more (got %lld)", (long long)ld);
   if (!logits || !targets || !logprob || !entropy) return fail(WUSH_EINVAL, "null pointer");
   if (top > 0 && (!top_ids || !top_logprobs)) return fail(WUSH_EINVAL, "null top_ids or top_logprobs");

@@ -270,6 +270,11 @@ static void logprobs() {
         const uintptr_t end = (uintptr_t)a.keys + 8 * R * a.splits * top;
         EXPECT((uintptr_t)a.keys == 7 * A && (uintptr_t)a.part == end && end + 16 * R * a.splits == 7 * A + n, "scratch");
       }
+  // More rows than a call takes.
+  for (int64_t R : {((int64_t)1 << 24) + 1, (int64_t)1 << 50, INT64_MAX}) {
+    EXPECT(wush_token_logprobs_workspace(R, INT32_MAX, 0, 32) == 0, "too many rows");
+    REJECT(call([&](Call& k) { k.R = R; }), WUSH_EINVAL);
+  }
   EXPECT(wush_token_logprobs_workspace(0, 9, 0, 0) == 0 && wush_token_logprobs_workspace(4, 0, 0, 0) == 0, "none");
 }
 
