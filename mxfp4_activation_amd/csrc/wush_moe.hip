@@ -438,9 +438,14 @@ hipError_t go_down_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);
   if (t == 4) return go_down<FMT, 2, 2, 1, TERMS, true, 2, 2>(a, max_tiles, s);
   if (t == 16) {
-    // 96 NVFP4 experts of 2560 x 1440, 64 tokens: 196 us against 226 with eight waves
-    // of four row tiles; 8 INT4 experts of 4096 x 4096, 33 tokens: 109 against 101.
-    if (FMT == kINT) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, max_tiles, s);
+    // Up to one workgroup per compute unit: eight waves each that split K four ways.
+    // Whole calls, those against the other shape, MXFP4, NVFP4 and INT4: 128 workgroups
+    // (24 tokens, 2 of 8 experts of 2048 x 1024) 27.1 : 28.8, 30.1 : 30.7, 30.7 : 31.9;
+    // 256 (16 tokens, 2 of 8 of 4096 x 4096) 71.6 : 74.6, 78.3 : 80.8, 80.3 : 84.0; 320
+    // (64 tokens, 2 of 16 of 2560 x 1440) 51.0 : 48.3, 60.3 : 55.2, 60.8 : 56.0; 1024
+    // (40 tokens, 8 of 32 of 4096 x 1568) 124 : 116, 143 : 130, 144 : 130.
+    const int slots = a.M * a.topk, experts = slots < a.E ? slots : a.E;
+    if ((a.H + 127) / 128 * experts <= 256) return go_down<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, max_tiles, s);
     return go_down<FMT, 2, 2, 1, TERMS, false, 4, 1>(a, max_tiles, s);
   }
   return go_down<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, max_tiles, s);

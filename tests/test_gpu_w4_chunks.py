@@ -88,10 +88,7 @@ _TILES = [(3, 4, 2), (16, 3, 2), (40, 3, 2)]
 _WIDTHS = [(1536, 1024, ""), (1696, 2080, "both"), (2048, 1568, "in"), (2592, 1312, "mid")]
 
 
-@pytest.mark.parametrize("H,I,transforms", _WIDTHS)
-@pytest.mark.parametrize("M,E,k", _TILES)
-@pytest.mark.parametrize("fmt", dc.FMTS)
-def test_moe(fmt, M, E, k, H, I, transforms):
+def _parity_and_repeats(fmt, M, E, k, H, I, transforms):
     rng = np.random.default_rng(M + H)
     G = decode.GROUP[fmt]
     if fmt == "nvfp4":
@@ -114,3 +111,17 @@ def test_moe(fmt, M, E, k, H, I, transforms):
         _check(fmt, got, *args, k, renorm, dt)
         for _ in range(3):
             assert all(torch.equal(a, b) for a, b in zip(got, _run(fmt, *args, k, renorm, dt)))
+
+
+@pytest.mark.parametrize("H,I,transforms", _WIDTHS)
+@pytest.mark.parametrize("M,E,k", _TILES)
+@pytest.mark.parametrize("fmt", dc.FMTS)
+def test_moe(fmt, M, E, k, H, I, transforms):
+    _parity_and_repeats(fmt, M, E, k, H, I, transforms)
+
+
+# Tiles of 16 tokens on more experts than compute units take at a time.
+@pytest.mark.parametrize("H,I,transforms", [(1024, 800, ""), (1056, 1312, "both")])
+@pytest.mark.parametrize("fmt", dc.FMTS)
+def test_moe_of_many_experts(fmt, H, I, transforms):
+    _parity_and_repeats(fmt, 16, 40, 8, H, I, transforms)
