@@ -79,18 +79,25 @@ constexpr int64_t kLds = 163840;
 
 // Which shape of workgroup.  What counts is how many there are (256 compute
 // units want a few waves each), how many row tiles share the activations' way
-// through LDS, and that way's share of LDS.  Measured (us, best first):
-//   1 token:   4096 x 4096 MXFP4, one row tile, eight waves along K 4.2, two row
-//              tiles and four waves 6.2; 24576 x 4096 11.5 for the latter, 12.7.
-//   13 tokens: 5003 x 5136 NVFP4, two row tiles x one step 11.5, one row tile x two
-//              steps 14.3, four row tiles 26.7.
-//   16 tokens: 24576 x 4096 MXFP4, 2 x 2 waves 17.0, 1 x 8 27.4; two planes of
-//              activations, four row tiles 20.4, 2 x 2 waves 28.6.
-//   64 tokens: 4096 x 4096 MXFP4, four workgroups of 16 tokens for every 64 rows
-//              10.6, one of 64 tokens 41; 57344 x 8192 the latter 97.6, the
-//              former 254.  24576 x 4096 workgroups of 32 tokens and four row
-//              pairs 32.1, of 64 tokens and eight 44.5; 57344 x 8192 134 for the
-//              former.
+// through LDS, and that way's share of LDS.  Measured on both sides of each bound (us;
+// MXFP4, K = 4096, without and with T; a call of a few us is the host's), R x D units
+// and WN x WK waves:
+//   up to 4 tokens, N 12288: 12288 x 1 token 1x2, 1x8 9.6, 2x2, 1x4 9.6; 4 tokens 9.0, 9.9
+//     (NVFP4 10.2, 12.6; INT4 11.2, 12.0); 16384 x 4 10.8, 10.5 (14.1, 13.2; 13.3, 12.5);
+//     24576 x 4 15.1, 14.3, with T 24.1, 19.9.
+//   13 tokens, all 4608: 4096 rows 1x2, 1x8 9.0, 2x1, 1x8 9.1; 6144 9.6, 9.3 (NVFP4 11.0, 9.9;
+//     INT4 11.3, 9.9).  8192: 8192 rows 2x1, 1x8 9.2, 2x2, 2x4 10.4; 12288 15.4, 12.2.
+//     16384: 16384 rows 2x2, 2x4 12.7, 2x2, 2x2 13.6; 24576 19.8, 19.1, with T 31.2, 27.6.
+//   17 tokens and more, all 32768 (rows x token tiles), 2x2 units and waves against the best of
+//     the wider tiles: 16384 x 32 17.8 against 24.0, with T 35.6 against 55.6; 8192 x 64
+//     15.7 against 23.4, 32.8 against 48.0 (NVFP4 20.3, 28.3; INT4 20.2, 31.9); 12288 x 64
+//     24.5 against 26.3, 47.0 against 54.3; 16384 x 64 30.4 against 26.8, 60.6 against 55.2;
+//     4096 x 128 15.7 against 23.3, 32.7 against 48.7.
+//   6 and 16 tokens with T, 24576 rows, 4x1, 2x4 against 2x2, 2x2: 26.0 and 28.5 against 23.1
+//     and 36.1; 40960 rows 40.2 and 49.9 against 31.4 and 50.6.
+//   33 to 64 tokens, N 16384: 16384 x 48 four token tiles 21.8, two 25.7; 20480 x 48 39.4, 27.1.
+//     N 32768: 32768 x 64 two token tiles 37.3, four 50.8; 40960 x 64 52.7, 51.7 (INT4
+//     66.1, 71.0); 57344 x 8192 x 64 four 97.6, two 134.
 template <int FMT, int TERMS>
 hipError_t go_tiles(const LinearArgs& a, hipStream_t s) {
   const int64_t K = a.K, N = a.N;
@@ -107,7 +114,7 @@ hipError_t go_tiles(const LinearArgs& a, hipStream_t s) {
     return go<FMT, 2, 1, 1, TERMS, false, 1, 8>(a, s);
   if (all <= 16384 && lds_bytes<2, 2, 1, TERMS, 2, 4>(rows, K) <= kLds)
     return go<FMT, 2, 2, 1, TERMS, false, 2, 4>(a, s);
-  if (all <= 16384 || (a.M <= 16 && TERMS == 1)) return go<FMT, 2, 2, 1, TERMS, false, 2, 2>(a, s);
+  if (all <= (a.M <= 16 ? 16384 : 32768) || (a.M <= 16 && TERMS == 1)) return go<FMT, 2, 2, 1, TERMS, false, 2, 2>(a, s);
   if (a.M <= 16) return go<FMT, 4, 1, 1, TERMS, false, 2, 4>(a, s);
   if constexpr (TERMS > 1) {
     return go<FMT, 4, 1, 2, TERMS, false, 4, 2>(a, s);

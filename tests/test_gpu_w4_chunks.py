@@ -42,6 +42,7 @@ _SHAPES = [
     (16, 8200, 512),
     (20, 8300, 512), (20, 8300, 256),
     (40, 5500, 512), (64, 5500, 256),
+    (24, 16500, 512), (24, 16500, 256), (40, 11000, 512),
     (50, 16500, 256), (64, 33000, 256),
 ]
 
