@@ -360,8 +360,11 @@ wush_status wush_f64_to_bf16(const double* src, int64_t n, void* dst, hipStream_
  *   global_scale: device fp32, NVFP4 only (wush_nvfp4_global_scale).
  *   Y: [M][N] fp32 or bf16 (out_type as in wush_gemm_mxfp4).
  * K is a positive multiple of G, at most 2^27; any M and N >= 0 (0 is a
- * no-op), M up to about a million.  It is meant for few tokens: from about a hundred on,
- * quantized activations and wush_gemm_mxfp4 are faster.
+ * no-op), M up to about a million.  It is meant for few tokens: weights are unpacked
+ * anew for every 64 tokens or fewer.  From about a hundred on, quantized activations
+ * and wush_gemm_mxfp4 are faster for MXFP4 weights; the other two formats have no
+ * such product here.  INT4 sums (code + 8) x - 8 x: 15 times the sum of |x| over a group
+ * has to be finite.
  * workspace: needed with T only. */
 wush_status wush_linear_w4(int fmt, const void* X, int64_t ldx, const void* T, const void* codes, const void* scales,
                            const float* global_scale, int64_t M, int64_t N, int64_t K, void* Y, int out_type,
@@ -385,9 +388,12 @@ int64_t wush_linear_w4_workspace(int64_t M, int64_t K, int out_type);
  *   T_in: bf16 [H/G][G][G].  T_mid: bf16 [E][I/G][G][G].
  *   Y: [M][H] fp32 or bf16; ids: int32 [M][topk]; weights: fp32 [M][topk].
  * H and I are positive multiples of G, at most 2^24; 1 <= E <= 1024;
- * 1 <= topk <= min(E, 32).  M >= 0; tokens are taken 64 at a time.  A NaN
- * logit ranks below every number; results are then NaN but all accesses stay in
- * range.  A token that is not finite leaves the others alone.
+ * 1 <= topk <= min(E, 32).  M >= 0; tokens are taken 64 at a time, each 64 with a
+ * pass over the experts that they choose.  A NaN logit ranks below every number: the
+ * token's results are NaN, unless renormalize is set and only numbers are chosen; all
+ * accesses stay in range.  A token that is not finite leaves the others alone.
+ * x' and h_e are kept to 16 significant bits for a bf16 Y and to fp32 accuracy for
+ * an fp32 Y.
  * Results repeat bit for bit.  transform: whether T_in is given. */
 wush_status wush_moe_w4(int fmt, const void* X, int64_t ldx, const void* router, const void* gate_up_codes,
                         const void* gate_up_scales, const float* gate_up_global, const void* T_in,

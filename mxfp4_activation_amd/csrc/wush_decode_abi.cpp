@@ -36,6 +36,7 @@ bool any_overlap(const Range* outs, int n_outs, const Range* ins, int n_ins) {
 int group_of(int fmt) { return fmt == wush::kNVFP4 ? 16 : 32; }
 int scale_bytes_of(int fmt) { return fmt == wush::kINT4 ? 2 : 1; }
 int out_bytes_of(int out_type) { return out_type == WUSH_OUT_F32 ? 4 : 2; }
+// Planes of T x and of the experts' h (split_panel says why two do for bf16).
 int terms_of(int out_type) { return out_type == WUSH_OUT_F32 ? 3 : 2; }
 
 uint64_t round16(uint64_t n) { return (n + 15) / 16 * 16; }
@@ -91,7 +92,7 @@ wush_status launched(hipError_t e) {
   return e == hipSuccess ? WUSH_OK : fail(WUSH_EHIP, "launch: %s", hipGetErrorString(e));
 }
 
-// Tokens of a mixture that share the four launches.
+// Tokens of a mixture that share its five launches.
 int64_t moe_chunk(int64_t M) { return M < wush::kMoeTokens ? M : wush::kMoeTokens; }
 
 struct MoeWorkspace {

@@ -34,6 +34,8 @@ struct Triple {
   float m, s, u;
 };
 
+// The product rounds once, so a probability is off by up to |d| roundings: 80 of them
+// where it is 1e-35.
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
 // Differences of maxima stop here: their exponential is 0 long before, and
@@ -288,6 +290,8 @@ struct Shared<true, PER> {
 // without alternatives.  Few rows are bound by the way through one workgroup: 10.5 us
 // for one row of 131072 on 64 workgroups with 20 alternatives, of which some 3.4 us are the
 // choice (bisection 0.9, candidates 1.1, their order 0.5), then 4.5 us for the join.
+// Many rows with alternatives are bound by the choice per batch of each row: 2048 x
+// 65536 takes 59 us without, 96 with one and 152 with 20.
 template <int TYPE, bool TOP, int PER>
 __global__ __launch_bounds__(kThreads) void logprob_kernel(LogprobArgs a) {
   using El = Elem<TYPE>;

@@ -239,8 +239,9 @@ hipError_t go_route(const MoeArgs& a, int tile_tokens, hipStream_t s) {
 // channels hold whole transform blocks, so T_mid is applied to h right here, and
 // neither gate nor up is ever written.  Bound by the experts' weights: 128 experts of
 // 4096 x 1280 MXFP4, 8 tokens, T: 67 us (51 experts of 5.6 MB: 4.2 TB/s); 8 INT4
-// experts of 4096 x 4096, 33 tokens: 44 us (3.4 TB/s); 96 NVFP4 experts of 2560 x
-// 1440, 64 tokens: 98 us (4.0 TB/s).
+// experts of 4096 x 4096, 33 tokens: 45 us (3.3 TB/s); 96 NVFP4 experts of 2560 x
+// 1440, 64 tokens: 98 us (4.0 TB/s).  Waves wait for 47 to 49% of their cycles; vector
+// instructions take 25, 34 and 51% of the time.
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
 __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) void gate_up_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
@@ -339,8 +340,8 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) voi
 //
 // A workgroup owns 16 R WN channels of y for one tile; its results, one row per
 // slot, wait in memory for the slots' other experts (added there by atomics, their
-// order would change results).  Bound as gate and up: 36, 32 and 63 us on the same
-// three (3.9, 2.4 and 3.1 TB/s: rows are short or the weights INT4).
+// order would change results).  Bound as gate and up: 35, 32 and 64 us on the same
+// three (4.0, 2.4 and 3.1 TB/s: rows are short, or few workgroups).
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
 __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) void down_kernel(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
@@ -422,9 +423,8 @@ int tile_tokens(const MoeArgs& a) {
 // Four waves of two row tiles and two steps each.  Measured on 128 experts of
 // 4096 x 1280 MXFP4 with transforms, 8 tokens (the whole call): 122 us, against 133
 // with eight waves of four row tiles that split K, and 144 with four of those;
-// down 124 against 132 with K split over four waves.  (Both sides of these and of the
-// next were timed in turn in one state of the rest; the calls now take 107, 170 and
-// 87 us.)
+// down 124 against 132 with K split over four waves.  (Both sides were timed in turn
+// in one state of the rest; the call now takes 104 to 109 us.)
 template <int FMT, int TERMS>
 hipError_t go_gate_up_tiles(const MoeArgs& a, int max_tiles, hipStream_t s) {
   const int t = tile_tokens(a);

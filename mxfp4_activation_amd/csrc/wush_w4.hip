@@ -31,11 +31,12 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 // tokens: NT grows with the tokens.  Measured without T:
 //   1 token:   4096 x 4096 MXFP4 4.2 us (2.1 TB/s: a launch and two round trips to
 //              memory), 24576 x 4096 11.5 us (4.7 TB/s), 8192 x 28672 26.2 us (4.8 TB/s),
-//              INT4 39 us with T (3.4 TB/s; sums per group cost instructions)
+//              INT4 39 us with T (3.4 TB/s; waves wait for 53% of their cycles,
+//              vector instructions take 31% of the time, the matrix cores 27%)
 //   13 tokens: 5003 x 5136 NVFP4 11.1 us (1.3 TB/s: 157 workgroups for 256 compute units)
 //   64 tokens: 57344 x 8192 MXFP4 99 us (605 TFLOP/s, 2.5 TB/s: two waves per SIMD wait
-//              for each other's chunks; matrix cores 25% busy; 87 us of it remain at
-//              17 tokens)
+//              for each other's chunks and for weights not asked for ahead; matrix cores
+//              23% busy; 87 us of it remain at 17 tokens), NVFP4 115, INT4 140
 template <int FMT, int R, int D, int NT, int TERMS, bool SPREAD, int WN, int WK>
 __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) void linear_kernel(LinearArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint16_t lds[];

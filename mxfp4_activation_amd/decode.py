@@ -103,7 +103,9 @@ def linear_w4(fmt: str, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     row stride that is a multiple of 8) times the 4-bit weights codes [N, K/2],
     scales [N, K/G] (``quant`` or ``gptq_wush``), with x' = x, or the block
     transform of x by the activation bank T [K/G, G, G].  NVFP4 weights take
-    their tensor scale as global_scale.  Returns [M, N] in out_dtype."""
+    their tensor scale as global_scale.  Returns [M, N] in out_dtype.  Sums are fp32;
+    T x enters them with 16 significant bits where out_dtype is bfloat16 and with all
+    24 where it is float32."""
     f, G = _fmt(fmt)
     ot = _out_type(out_dtype)
     M, K, ldx = _rows(x, "x")
@@ -154,7 +156,9 @@ def moe_w4(fmt: str, x: torch.Tensor, router: torch.Tensor, gate_up: W4Experts, 
     (renormalized to sum 1, or not), SwiGLU experts and their weighted sum.
     gate_up holds 2 I rows per expert, I of the gate, then I of the up
     projection; its T is one bank [H/G, G, G] for all experts.  down holds H
-    rows of width I; its T is [E, I/G, G, G]."""
+    rows of width I; its T is [E, I/G, G, G].  Sums are fp32; the transformed x and the
+    experts' inner activations enter them with 16 significant bits where out_dtype is
+    bfloat16 and with all 24 where it is float32."""
     f, G = _fmt(fmt)
     ot = _out_type(out_dtype)
     M, H, ldx = _rows(x, "x")
@@ -200,8 +204,8 @@ class TokenLogprobs(NamedTuple):
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0) -> TokenLogprobs:
     """Log probabilities of the tokens targets [R] (int64; negative: not
-    scored, 0) under logits [R, V] (float32, bfloat16 or float16, any row
-    stride), the rows' entropies and their `top` most likely tokens (ties to the
+    scored, 0) under logits [R, V] (float32, bfloat16 or float16, rows V or more
+    elements apart), the rows' entropies and their `top` most likely tokens (ties to the
     lower id).  Masked tokens (-inf) have probability 0 and are not listed."""
     if logits.dim() != 2:
         raise ValueError("logits must be [R, V]")

@@ -103,3 +103,24 @@ def test_wide_masks_and_ties(R):
     l[8] = -np.arange(V) / 256.0
     l, d = _typed(l, "f32")
     check_logprobs(l, d, rng.integers(0, V, size=R), 32)
+
+
+@pytest.mark.parametrize("M", [1, 5, 20])
+def test_nan_logit_ranks_last(M):
+    """An expert whose router row has a NaN: chosen only where nothing else is left, and
+    without a part in the others' shares where those alone are renormalized."""
+    x, router, gu, dn = _inputs("mxfp4", M, 7, 64, 32, False, 12)
+    bad = router[1].copy()
+    bad[3, 9] = 0x7FC0
+    without = np.delete(np.arange(7), 3)
+    others = tuple(a[without] for a in router)
+    cut = [(p[0][without], p[1][without], None, None) for p in (gu, dn)]
+    for k in (2, 6):
+        got = _run("mxfp4", x, (router[0], bad), gu, dn, k, True, torch.float32)
+        want = _run("mxfp4", x, others, *cut, k, True, torch.float32)
+        assert np.array_equal(got.ids.cpu().numpy(), without[want.ids.cpu().numpy()])
+        assert torch.equal(got.weights, want.weights)
+        assert torch.allclose(got.out, want.out, rtol=0, atol=2.0**-16 * float(want.out.abs().max()))
+        assert torch.isnan(_run("mxfp4", x, (router[0], bad), gu, dn, k, False, torch.float32).out).all()
+    got = _run("mxfp4", x, (router[0], bad), gu, dn, 7, True, torch.float32)
+    assert torch.all(got.ids[:, 6] == 3) and torch.isnan(got.out).all()
