@@ -48,7 +48,7 @@ _SHAPES = [
 
 # Whole chunks, and what remains: nothing, less than a wave's part, most waves' parts, all
 # but the last group.
-_PARTS = [(2, 0.6), (3, 0.0), (4, 0.05), (4, 0.0), (5, 0.3), (6, 0.99), (3, 0.3)]
+_PARTS = [(2, 0.6), (3, 0.3), (4, 0.05), (4, 0.0), (5, 0.0), (5, 0.3), (6, 0.99)]
 
 
 @pytest.mark.parametrize("transform", [False, True])
