@@ -426,6 +426,62 @@ wush_status wush_token_logprobs(const void* logits, int logit_type, int64_t ld, 
                                 float* top_logprobs, void* workspace, int64_t workspace_bytes, hipStream_t stream);
 int64_t wush_token_logprobs_workspace(int64_t R, int64_t V, int logit_type, int top);
 
+/* ---- A cache of keys and values in 4 bits ----------------------------------
+ *
+ * Per layer, four caller-owned buffers of `pages` pages of `page` tokens:
+ *   k_codes, v_codes    u8 [pages][heads][page][D/2]
+ *   k_scales, v_scales  [pages][heads][page][D/G] (fp16 for INT4), G the format's group
+ * all 16-byte aligned, in the formats above with groups along D, and for NVFP4
+ * the tensor scales k_global, v_global (device fp32, one each).  Token slot s is place
+ * s % page of page s / page.  page: a power of two, 16 .. 65536.  D: 64, 128 or 256.
+ * 1 <= heads <= 4096.  What no call wrote may hold anything. */
+
+/* Writes n tokens' keys and values to their slots: y = T x per block of G channels
+ * (y = x without T), rounded to fp32 from sums in float64, then the scale and codes of
+ * wush_quant's definition for y.
+ *   K, V: bf16 [n][heads][D], row i at i * ldk (ldv) elements (heads * D or more, a
+ *         multiple of 8; 16-byte aligned).
+ *   T_k, T_v: bf16 [heads][D/G][G][G], 16-byte aligned, or NULL.
+ *   slots: int64 [n].  A slot outside the cache (a negative one, say: padding) is not
+ *          written.  The slots inside it must differ from each other.
+ * n >= 0 (0 is a no-op). */
+wush_status wush_kv4_append(int fmt, const void* K, int64_t ldk, const void* V, int64_t ldv, const void* T_k,
+                            const void* T_v, const int64_t* slots, int64_t n, int64_t heads, int64_t D, int64_t page,
+                            int64_t pages, void* k_codes, void* k_scales, const float* k_global, void* v_codes,
+                            void* v_scales, const float* v_global, hipStream_t stream);
+
+/* Attention over the cache: for query i of the count that sequence b has, at place
+ * pos = lengths[b] - count + i,
+ *     out = sum_t softmax_t(scale (T q) . k_t) v_t,   max(0, pos - window + 1) <= t <= pos
+ * (all t <= pos for window 0), k and v the cache's values as in wush_dequant.  lengths
+ * counts the queries' own tokens, written before.  A query that sees no token (pos < 0) has the
+ * result 0.  For keys that were transformed with T_k, T_q is the bank with
+ * T_q^T T_k = I per block (wush_build_transforms' T_xvsh for its T_wush; the same
+ * Hadamard bank for both); values transformed with T_v give the result in that basis, which a
+ * projection quantized with the matching weight-side transform takes as it is.
+ *   Q: bf16 [n][q_heads][D], row i at i * ldq elements (as K above); q_heads a multiple of
+ *      heads: query head h reads key head h / (q_heads / heads).
+ *   T_q: bf16 [heads][D/G][G][G] or NULL.
+ *   block_table: int32 [B][width], row stride ldt >= width: token t of sequence b is in
+ *      page block_table[b][t / page].  Only entries of tokens that a query sees are read.
+ *   lengths: int32 [B].
+ *   q_start: int32 [B + 1], ascending from 0: the queries of sequence b are rows
+ *      q_start[b] .. q_start[b + 1] - 1.  NULL: one each (B == n).
+ *   out: bf16 [n][q_heads][D], 16-byte aligned.  Rows from q_start[B] on are not written.
+ * A sequence whose length passes width * page, or with a page outside the cache among those
+ * read, has NaN results; no access leaves the buffers.  Scores and sums are fp32, T q is kept
+ * to 16 significant bits, probabilities enter the sum over v with bf16's 8 (as do INT4's
+ * values).  scale is positive and finite.  Results repeat bit for bit.
+ * workspace: wush_kv4_attention_workspace bytes (0 where width * page is small). */
+wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* T_q, const void* k_codes,
+                               const void* k_scales, const float* k_global, const void* v_codes, const void* v_scales,
+                               const float* v_global, const int32_t* block_table, int64_t ldt, int64_t width,
+                               const int32_t* lengths, const int32_t* q_start, int64_t B, int64_t n, int64_t q_heads,
+                               int64_t heads, int64_t D, int64_t page, int64_t pages, float scale, int64_t window,
+                               void* out, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t wush_kv4_attention_workspace(int64_t B, int64_t n, int64_t q_heads, int64_t heads, int64_t D, int64_t page,
+                                     int64_t width);
+
 /* Status text, and the detail of the last failure on this thread.  Library
  * interfaces; nothing on the pages corresponds. */
 const char* wush_status_string(wush_status status);

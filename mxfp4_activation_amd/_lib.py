@@ -45,6 +45,12 @@ SIGNATURES = {
     "wush_moe_w4_workspace": (_i64, [_i64, _i64, _c_int, _i64, _i64, _c_int, _c_int]),
     "wush_token_logprobs": (_c_int, [_vp, _c_int, _i64, _i64, _i64, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "wush_token_logprobs_workspace": (_i64, [_i64, _i64, _c_int, _c_int]),
+    "wush_kv4_append": (_c_int, [_c_int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp,
+                                 _vp, _vp, _vp, _vp, _vp]),
+    "wush_kv4_attention": (_c_int, [_c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
+                                    _i64, _i64, _i64, _i64, _i64, _i64, _i64, ctypes.c_float, _i64, _vp, _vp, _i64,
+                                    _vp]),
+    "wush_kv4_attention_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64, _i64, _i64]),
     "wush_status_string": (ctypes.c_char_p, [_c_int]),
     "wush_last_error": (ctypes.c_char_p, []),
     "wush_abi_version": (_c_int, []),

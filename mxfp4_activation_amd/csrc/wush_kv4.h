@@ -1,0 +1,95 @@
+// Internal interface of the 4-bit key/value cache (wush_kv4.hip) and of the
+// attention over it (wush_kv4_attention.h) for their C-ABI layer
+// (wush_kv4_abi.cpp).  Not part of the public ABI.
+#ifndef WUSH_KV4_H_
+#define WUSH_KV4_H_
+
+#include <stdint.h>
+
+#include <hip/hip_runtime_api.h>
+
+namespace wush {
+
+struct KvAppendSide {
+  const uint16_t* X;  // bf16 [n][heads][D], row stride ld
+  int64_t ld;         // elements, a multiple of 8
+  const uint16_t* T;  // bf16 [heads][D/G][G][G] or null
+  uint8_t* codes;     // [pages][heads][page][D/2]
+  uint8_t* scales;    // [pages][heads][page][D/G]
+  const float* gs;    // NVFP4 only
+};
+
+struct KvAppendArgs {
+  int fmt;
+  KvAppendSide side[2];  // keys, values
+  const int64_t* slots;  // [n]: page * page size + place; outside the cache: not written
+  int64_t n, pages;
+  int heads, D, page_log2;
+};
+
+hipError_t launch_kv4_append(const KvAppendArgs& a, hipStream_t s);
+
+// Attention.  A work item is one key head's queries of one sequence, as many
+// columns (query, head of the group) as a workgroup holds; a unit is
+// kKvUnit tokens of an item.
+constexpr int kKvUnit = 128;
+
+struct KvAttnArgs {
+  int fmt;
+  const uint16_t* q;  // bf16 [n][kv * group][D], row stride ldq
+  int64_t ldq;
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const float *k_gs, *v_gs;  // NVFP4 only
+  const int32_t* table;      // [B][width], row stride ldt
+  int64_t ldt;
+  const int32_t* lengths;    // [B]
+  const int32_t* q_start;    // [B + 1], or null: query b is sequence b's
+  const uint16_t* T;         // bf16 [kv][D/G][G][G] or null
+  uint16_t* out;             // bf16 [n][kv * group][D]
+  float* part;               // pieces of items, if any item may be cut
+  int B, n, kv, group, D, page_log2, width, pages;
+  int window;                // 0: none
+  float scale;               // of the scores, times log2 e
+  int workgroups;
+  int whole;                 // every workgroup takes one whole item
+};
+
+// How a call is cut: columns per workgroup, workgroups, and whether items are
+// taken whole (then nothing is left to join, and there is no workspace).
+enum { kKvNarrow, kKvWide, kKvPrompt };  // four waves share columns, the same with twice as many, waves have their own
+// Tiles of 16 columns per wave: one where the results of two would not fit the registers.
+constexpr int kv_tiles(int shape, int D) { return shape == kKvNarrow || D > 128 ? 1 : 2; }
+constexpr int kv_columns(int shape, int D) { return 16 * kv_tiles(shape, D) * (shape == kKvPrompt ? 4 : 1); }
+
+struct KvPlan {
+  int shape, workgroups, whole;
+  int64_t items;  // at most
+};
+
+constexpr int kKvGroups = 512;        // workgroups that share a call's units
+constexpr int64_t kKvWholeTokens = 512;  // up to here an item is not worth cutting
+
+inline KvPlan kv_plan(int64_t B, int64_t n, int64_t kv, int64_t group, int D, int64_t tokens) {
+  KvPlan p;
+  const int64_t columns = B > 0 ? n * group / B : 0;  // of a sequence, on average
+  p.shape = columns <= 16 ? kKvNarrow : columns <= (D > 128 ? 32 : 64) ? (D > 128 ? kKvNarrow : kKvWide) : kKvPrompt;
+  const int64_t nc = kv_columns(p.shape, D);
+  // Each sequence ends in a part of an item; sequences without queries have none.
+  const int64_t seqs = B < n ? B : n;
+  p.items = (n * group / nc + seqs) * kv;
+  p.whole = tokens <= kKvWholeTokens;
+  const int64_t units = p.items * ((tokens + kKvUnit - 1) / kKvUnit + 1);
+  p.workgroups = (int)(p.whole ? p.items : units < kKvGroups ? units : kKvGroups);
+  return p;
+}
+
+// Floats of one piece of an item: maxima, sums, results.
+inline int64_t kv_piece(int shape, int D) { return (int64_t)kv_columns(shape, D) * (D + 2); }
+
+hipError_t launch_kv4_attention_mx(const KvAttnArgs& a, int shape, hipStream_t s);
+hipError_t launch_kv4_attention_nv(const KvAttnArgs& a, int shape, hipStream_t s);
+hipError_t launch_kv4_attention_int(const KvAttnArgs& a, int shape, hipStream_t s);
+
+}  // namespace wush
+
+#endif  // WUSH_KV4_H_
