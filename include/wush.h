@@ -482,6 +482,45 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
 int64_t wush_kv4_attention_workspace(int64_t B, int64_t n, int64_t q_heads, int64_t heads, int64_t D, int64_t page,
                                      int64_t width);
 
+/* ---- Around the products of a decode step ---------------------------------- */
+
+/* wush_linear_w4 with low-rank adapters, one per token:
+ *     Y[m] = x'[m] W^T + adapter_scale[e] (x[m] A[e]^T) B[e]^T,   e = ids[m],
+ * x the untransformed activations, also with T.  A negative id has no adapter (the result is
+ * wush_linear_w4's); an id of `adapters` or more gives NaN in its row.
+ *   A: bf16 [adapters][rank][K], B: bf16 [adapters][N][rank], 16-byte aligned.
+ *   adapter_scale: device fp32 [adapters] or NULL (1).  ids: int32 [M].
+ * rank: a multiple of 8, at most 512 (pad A and B with zeros).  The adapters' products and sums
+ * are fp32 and enter Y before its one rounding.  Everything else as in wush_linear_w4; Y is
+ * exactly repeatable.
+ * workspace: always needed. */
+wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void* T, const void* codes,
+                                const void* scales, const float* global_scale, const void* A, const void* B,
+                                const float* adapter_scale, const int32_t* ids, int64_t adapters, int64_t rank,
+                                int64_t M, int64_t N, int64_t K, void* Y, int out_type, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream);
+int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t K, int64_t rank, int transform, int out_type);
+
+/* Penalties, biases and masks on rows of logits, before wush_token_logprobs or a sampler.  For
+ * token v of row r, with c = how often v is in output[r], in fp32 and in this order:
+ *   v in prompt[r] or output[r]:  l = l > 0 ? l / repetition[r] : l * repetition[r]
+ *   c > 0:                        l = l - frequency[r] c - presence[r]
+ *   l = l + bias of each entry of bias_ids[r] that is v (their sum, in the list's order)
+ *   bit v % 32 of allowed[r][v / 32] not set:  l = -inf, whatever it was
+ * and one rounding to the logits' type.
+ *   logits, out: [R][V] of one type, row strides ld, ld_out >= V elements; out may be logits
+ *      itself (same pointer and stride).
+ *   prompt: int32 [R][n_prompt], output: int32 [R][n_output], bias_ids: int32 [R][n_bias]; entries
+ *      outside 0 .. V - 1 (padding: -1) count for nothing.  A length of 0: no list.
+ *   repetition, frequency, presence: fp32 [R] or NULL (1, 0, 0).  bias: fp32 [R][n_bias].
+ *   allowed: int32 [R][(V + 31) / 32] or NULL (all).
+ * 1 <= V < 2^31, 0 <= R <= 65535 (0 is a no-op).  Results repeat bit for bit. */
+wush_status wush_adjust_logits(const void* logits, int logit_type, int64_t ld, int64_t R, int64_t V,
+                               const int32_t* prompt, int64_t n_prompt, const int32_t* output, int64_t n_output,
+                               const float* repetition, const float* frequency, const float* presence,
+                               const int32_t* bias_ids, const float* bias, int64_t n_bias, const int32_t* allowed,
+                               void* out, int64_t ld_out, hipStream_t stream);
+
 /* Status text, and the detail of the last failure on this thread.  Library
  * interfaces; nothing on the pages corresponds. */
 const char* wush_status_string(wush_status status);

@@ -14,10 +14,12 @@ __all__ = [
     "load", "WushError", "quant", "quant_mxfp4", "quant_nvfp4", "quant_int4", "transform_f32",
     "absmax_transformed", "nvfp4_global_scale", "e2m1_encode", "build_transforms", "fixed_transforms",
     "f64_to_bf16", "dequant", "gemm_mxfp4", "linear_w4", "moe_w4", "token_logprobs", "W4Experts", "MoeResult",
-    "TokenLogprobs", "KV4Cache", "kv4_cache", "kv4_append", "kv4_attention",
+    "TokenLogprobs", "KV4Cache", "kv4_cache", "kv4_append", "kv4_attention", "linear_w4_lora",
+    "LoraAdapters", "adjust_logits",
 ]
 
-_DECODE = {"linear_w4", "moe_w4", "token_logprobs", "W4Experts", "MoeResult", "TokenLogprobs"}
+_DECODE = {"linear_w4", "linear_w4_lora", "moe_w4", "adjust_logits", "token_logprobs", "LoraAdapters", "W4Experts",
+           "MoeResult", "TokenLogprobs"}
 _KV4 = {"KV4Cache", "kv4_cache", "kv4_append", "kv4_attention"}
 
 

@@ -1,5 +1,6 @@
 // C-ABI layer of the decode entries around the 4-bit products: the cache of
-// keys and values, attention over it.  Contract: include/wush.h.
+// keys and values, attention over it, linear layers with low-rank adapters, and
+// adjustments of logits.  Contract: include/wush.h.
 
 #include <math.h>
 #include <stdint.h>
@@ -7,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/wush.h"
+#include "wush_adjust.h"
 #include "wush_decode_checks.h"
 #include "wush_kernels.h"
 #include "wush_kv4.h"
@@ -22,6 +24,9 @@ using namespace wush::decode;
 
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxLoraRows = 65535 * 16;
+constexpr int64_t kMaxRank = 512;
+constexpr int64_t kMaxAdjustRows = 65535;
 
 int log2_of(int64_t v) {
   int n = 0;
@@ -198,6 +203,163 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   if (fmt == wush::kMXFP4) return launched(wush::launch_kv4_attention_mx(a, plan.shape, stream));
   if (fmt == wush::kNVFP4) return launched(wush::launch_kv4_attention_nv(a, plan.shape, stream));
   return launched(wush::launch_kv4_attention_int(a, plan.shape, stream));
+}
+
+int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t K, int64_t rank, int transform, int out_type) {
+  if (M <= 0 || K <= 0 || K > kMaxK || M > kMaxLoraRows || rank <= 0 || rank > kMaxRank) return 0;
+  if (out_type != WUSH_OUT_F32 && out_type != WUSH_OUT_BF16) return 0;
+  return (int64_t)round16((uint64_t)M * rank * 4) + (transform ? wush_linear_w4_workspace(M, K, out_type) : 0);
+}
+
+wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void* T, const void* codes,
+                                const void* scales, const float* global_scale, const void* A, const void* B,
+                                const float* adapter_scale, const int32_t* ids, int64_t adapters, int64_t rank,
+                                int64_t M, int64_t N, int64_t K, void* Y, int out_type, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream) {
+  g_last_error[0] = 0;
+  wush_status st = check_fmt(fmt, out_type);
+  if (st != WUSH_OK) return st;
+  if (M < 0 || N < 0) return fail(WUSH_EINVAL, "M and N must be >= 0");
+  st = check_width("K", K, fmt);
+  if (st != WUSH_OK) return st;
+  if (rank < 8 || rank > kMaxRank || rank % 8 != 0)
+    return fail(WUSH_EINVAL, "rank must be a multiple of 8, 8 .. %lld (got %lld)", (long long)kMaxRank, (long long)rank);
+  if (adapters < 0 || adapters > INT32_MAX) return fail(WUSH_EINVAL, "adapters out of range (got %lld)", (long long)adapters);
+  if (M == 0 || N == 0) return WUSH_OK;
+  if (N > kMaxDim) return fail(WUSH_EINVAL, "N too large");
+  if (M > kMaxLoraRows) return fail(WUSH_EINVAL, "M too large for one launch");
+  if (adapters > 0 && (adapters > INT64_MAX / 4 / rank / K || adapters > INT64_MAX / 4 / rank / N))
+    return fail(WUSH_EINVAL, "adapters too large");
+  st = check_rows(X, ldx, M, K);
+  if (st != WUSH_OK) return st;
+  st = check_weights("weight", fmt, codes, scales, global_scale);
+  if (st != WUSH_OK) return st;
+  if (T && !aligned(T, 16)) return fail(WUSH_EALIGN, "T must be 16-byte aligned");
+  if (!Y || !ids || (adapters > 0 && (!A || !B))) return fail(WUSH_EINVAL, "null Y, ids, A or B");
+  if (!aligned(Y, (uintptr_t)out_bytes_of(out_type))) return fail(WUSH_EALIGN, "Y must be aligned to its elements");
+  if (!aligned(A, 16) || !aligned(B, 16)) return fail(WUSH_EALIGN, "A and B must be 16-byte aligned");
+  if (!aligned(ids, 4) || !aligned(adapter_scale, 4)) return fail(WUSH_EALIGN, "ids and adapter_scale must be 4-byte aligned");
+  const int64_t need = wush_linear_w4_lora_workspace(M, K, rank, T != nullptr, out_type);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != WUSH_OK) return st;
+  const Range ins[] = {{X, ((uint64_t)(M - 1) * (M > 1 ? ldx : 0) + K) * 2},
+                       {T, (uint64_t)K * group_of(fmt) * 2},
+                       {codes, code_bytes(N, K)},
+                       {scales, scale_bytes(fmt, N, K)},
+                       {fmt == wush::kNVFP4 ? global_scale : nullptr, 4},
+                       {A, (uint64_t)adapters * rank * K * 2},
+                       {B, (uint64_t)adapters * rank * N * 2},
+                       {adapter_scale, (uint64_t)adapters * 4},
+                       {ids, (uint64_t)M * 4}};
+  const Range outs[] = {{Y, (uint64_t)M * N * out_bytes_of(out_type)}, {workspace, (uint64_t)need}};
+  if (any_overlap(outs, 2, ins, 9)) return fail(WUSH_EINVAL, "Y and the workspace must not overlap each other or an input");
+  st = check_device();
+  if (st != WUSH_OK) return st;
+
+  wush::LinearArgs a{};
+  a.fmt = fmt;
+  a.x.X = static_cast<const uint16_t*>(X);
+  a.x.ldx = M > 1 ? ldx : 0;
+  a.x.terms = 1;
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.scales = static_cast<const uint8_t*>(scales);
+  a.gs = global_scale;
+  a.Y = Y;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16_out = out_type == WUSH_OUT_BF16;
+  a.lora.X = a.x.X;
+  a.lora.ldx = a.x.ldx;
+  a.lora.A = static_cast<const uint16_t*>(A);
+  a.lora.B = static_cast<const uint16_t*>(B);
+  a.lora.scale = adapter_scale;
+  a.lora.ids = ids;
+  a.lora.h = static_cast<float*>(workspace);
+  a.lora.M = M;
+  a.lora.K = K;
+  a.lora.E = adapters;
+  a.lora.rank = (int)rank;
+  wush::SplitArgs t{};
+  if (T) {
+    t.X = a.x.X;
+    t.ldx = a.x.ldx;
+    t.T = static_cast<const uint16_t*>(T);
+    t.out = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + round16((uint64_t)M * rank * 4));
+    t.M = M;
+    t.K = K;
+    t.G = group_of(fmt);
+    t.terms = terms_of(out_type);
+    a.x.X = t.out;
+    a.x.ldx = K;
+    a.x.plane = M * K;
+    a.x.terms = t.terms;
+  }
+  st = launched(wush::launch_lora(a.lora, T ? &t : nullptr, stream));
+  if (st != WUSH_OK) return st;
+  return launched(wush::launch_linear_w4(a, stream));
+}
+
+wush_status wush_adjust_logits(const void* logits, int logit_type, int64_t ld, int64_t R, int64_t V,
+                               const int32_t* prompt, int64_t n_prompt, const int32_t* output, int64_t n_output,
+                               const float* repetition, const float* frequency, const float* presence,
+                               const int32_t* bias_ids, const float* bias, int64_t n_bias, const int32_t* allowed,
+                               void* out, int64_t ld_out, hipStream_t stream) {
+  g_last_error[0] = 0;
+  if (logit_type < WUSH_LOGITS_F32 || logit_type > WUSH_LOGITS_F16)
+    return fail(WUSH_EINVAL, "unknown logit_type %d", logit_type);
+  if (R < 0) return fail(WUSH_EINVAL, "R must be >= 0 (got %lld)", (long long)R);
+  if (V < 1 || V > INT32_MAX) return fail(WUSH_EINVAL, "V must be 1 .. 2^31 - 1 (got %lld)", (long long)V);
+  if (n_prompt < 0 || n_output < 0 || n_bias < 0 || n_prompt > INT32_MAX || n_output > INT32_MAX || n_bias > INT32_MAX)
+    return fail(WUSH_EINVAL, "the lists' lengths must be 0 .. 2^31 - 1");
+  if (R == 0) return WUSH_OK;
+  if (R > kMaxAdjustRows) return fail(WUSH_EINVAL, "R too large for one launch");
+  if (R > 1 && (ld < V || ld > ((int64_t)1 << 36) || ld_out < V || ld_out > ((int64_t)1 << 36)))
+    return fail(WUSH_EINVAL, "ld and ld_out must be V or more (got %lld, %lld)", (long long)ld, (long long)ld_out);
+  if (!logits || !out) return fail(WUSH_EINVAL, "null logits or out");
+  if ((n_prompt > 0 && !prompt) || (n_output > 0 && !output) || (n_bias > 0 && (!bias_ids || !bias)))
+    return fail(WUSH_EINVAL, "null list");
+  const int eb = logit_type == WUSH_LOGITS_F32 ? 4 : 2;
+  if (!aligned(logits, (uintptr_t)eb) || !aligned(out, (uintptr_t)eb))
+    return fail(WUSH_EALIGN, "logits and out must be aligned to their elements");
+  if (!aligned(prompt, 4) || !aligned(output, 4) || !aligned(repetition, 4) || !aligned(frequency, 4) ||
+      !aligned(presence, 4) || !aligned(bias_ids, 4) || !aligned(bias, 4) || !aligned(allowed, 4))
+    return fail(WUSH_EALIGN, "lists, penalties and masks must be 4-byte aligned");
+  const bool in_place = out == logits && (R == 1 || ld_out == ld);
+  const Range ins[] = {{in_place ? nullptr : logits, ((uint64_t)(R - 1) * (R > 1 ? ld : 0) + V) * eb},
+                       {prompt, (uint64_t)R * n_prompt * 4},
+                       {output, (uint64_t)R * n_output * 4},
+                       {repetition, (uint64_t)R * 4},
+                       {frequency, (uint64_t)R * 4},
+                       {presence, (uint64_t)R * 4},
+                       {bias_ids, (uint64_t)R * n_bias * 4},
+                       {bias, (uint64_t)R * n_bias * 4},
+                       {allowed, (uint64_t)R * ((V + 31) / 32) * 4}};
+  const Range outs[] = {{out, ((uint64_t)(R - 1) * (R > 1 ? ld_out : 0) + V) * eb}};
+  if (any_overlap(outs, 1, ins, 9)) return fail(WUSH_EINVAL, "out must be logits itself or not overlap an input");
+  wush_status st = check_device();
+  if (st != WUSH_OK) return st;
+
+  wush::AdjustArgs a{};
+  a.in = logits;
+  a.out = out;
+  a.type = logit_type;
+  a.ld_in = R > 1 ? ld : 0;
+  a.ld_out = R > 1 ? ld_out : 0;
+  a.R = R;
+  a.V = V;
+  a.prompt = prompt;
+  a.output = output;
+  a.n_prompt = n_prompt;
+  a.n_output = n_output;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias_ids = bias_ids;
+  a.bias = bias;
+  a.n_bias = n_bias;
+  a.allowed = allowed;
+  return launched(wush::launch_adjust(a, stream));
 }
 
 }  // extern "C"

@@ -28,6 +28,19 @@ struct SplitArgs {
   int G, terms;
 };
 
+// Low-rank adapters of a batch: Y[m] += h[m] B[ids[m]]^T, h from launch_lora.
+struct LoraArgs {
+  const uint16_t* X;   // bf16 [M], row stride ldx
+  int64_t ldx;
+  const uint16_t* A;   // bf16 [E][rank][K]
+  const uint16_t* B;   // bf16 [E][N][rank]
+  const float* scale;  // [E] or null
+  const int32_t* ids;  // [M]: negative, none; E or more, NaN
+  float* h;            // [M][rank]: scale[ids[m]] A[ids[m]] x[m]
+  int64_t M, K, E;
+  int rank;            // a multiple of 8
+};
+
 struct LinearArgs {
   int fmt;
   Planes x;
@@ -37,6 +50,7 @@ struct LinearArgs {
   void* Y;                // [M][N] fp32 or bf16
   int64_t M, N, K;
   bool bf16_out;
+  LoraArgs lora;  // none if ids is null
 };
 
 // Mixture of experts over at most kMoeTokens tokens at a time.
@@ -84,6 +98,8 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s);
 
 hipError_t launch_split(const SplitArgs& a, hipStream_t s);
 hipError_t launch_linear_w4(const LinearArgs& a, hipStream_t s);
+// h of the adapters and, where t is not null, also what launch_split does.
+hipError_t launch_lora(const LoraArgs& a, const SplitArgs* t, hipStream_t s);
 
 // Log probabilities, entropy and largest entries of rows of logits.
 constexpr int kLogprobMaxTop = 32;

@@ -6,6 +6,7 @@
 
 #include "wush_w4.h"
 #include "wush_w4_core.h"
+#include "wush_wave.h"
 
 namespace wush {
 namespace {
@@ -21,6 +22,82 @@ using namespace w4;
 __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
   const int64_t panel = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (panel * 32 < a.K) split_panel(a, panel, (int64_t)blockIdx.y * 16);
+}
+
+// ------------------------------------------------------------ adapters
+//
+// h[m] = scale A x[m] of the token's adapter.  A workgroup takes kLoraRows rows of A for
+// one token; its waves share the row.  Tokens of one adapter read the same rows, from the
+// cache after the first.
+constexpr int kLoraRows = 4;
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void lora_rows(const LoraArgs& a, int64_t m, int r0, float (*sums)[4]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t id = a.ids[m];
+  if (id < 0 || id >= a.E) return;
+  const uint16_t* x = a.X + m * a.ldx;
+  const uint16_t* A = a.A + (id * a.rank + r0) * a.K;
+  float s[kLoraRows] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t k = wave * 512 + lane * 8; k < a.K; k += 2048) {
+    const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k);
+    u32x4 w[kLoraRows];
+#pragma unroll
+    for (int r = 0; r < kLoraRows; ++r) w[r] = *reinterpret_cast<const u32x4*>(A + r * a.K + k);
+#pragma unroll
+    for (int r = 0; r < kLoraRows; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[r] = __builtin_fmaf(bf16_lo(w[r][i]), bf16_lo(xv[i]), s[r]);
+        s[r] = __builtin_fmaf(bf16_hi(w[r][i]), bf16_hi(xv[i]), s[r]);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < kLoraRows; ++r) {
+    s[r] = wave_sum(s[r]);
+    if (lane == 0) sums[r][wave] = s[r];
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < kLoraRows) {
+    const float v = (sums[t][0] + sums[t][1]) + (sums[t][2] + sums[t][3]);
+    a.h[m * a.rank + r0 + t] = v * (a.scale ? a.scale[id] : 1.0f);
+  }
+}
+
+// The transform's workgroups, if any, then the adapters': one launch.
+__global__ __launch_bounds__(256) void lora_kernel(LoraArgs a, SplitArgs t, int panels, int split) {
+  __shared__ float sums[kLoraRows][4];
+  const int b = blockIdx.x;
+  if (b < split) {
+    const int64_t panel = (int64_t)(b % panels) * 4 + (threadIdx.x >> 6);
+    if (panel * 32 < t.K) split_panel(t, panel, (int64_t)(b / panels) * 16);
+    return;
+  }
+  const int per = a.rank / kLoraRows;
+  lora_rows(a, (b - split) / per, (b - split) % per * kLoraRows, sums);
+}
+
+// What token m's adapter adds to result n: NaN for an adapter that is not there.
+__device__ __forceinline__ float lora_term(const LoraArgs& a, int64_t N, int64_t m, int64_t n) {
+  const int64_t id = a.ids[m];
+  if (id < 0) return 0.0f;
+  if (id >= a.E) return __builtin_nanf("");
+  const uint16_t* b = a.B + (id * N + n) * a.rank;
+  const float* h = a.h + m * a.rank;
+  float v = 0.0f;
+  for (int r = 0; r < a.rank; r += 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(b + r);
+    const f32x4 h0 = *reinterpret_cast<const f32x4*>(h + r), h1 = *reinterpret_cast<const f32x4*>(h + r + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v = __builtin_fmaf(bf16_lo(w[i]), i < 2 ? h0[2 * i] : h1[2 * i - 4], v);
+      v = __builtin_fmaf(bf16_hi(w[i]), i < 2 ? h0[2 * i + 1] : h1[2 * i - 3], v);
+    }
+  }
+  return v;
 }
 
 // ------------------------------------------------------------ linear
@@ -58,6 +135,7 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) voi
     if (n0 + c >= a.N) continue;
     float v = group_sum<R, WN, WK>(lds, c, m, rows);
     if (FMT == kNV) v *= g;
+    if (a.lora.ids) v += lora_term(a.lora, a.N, m0 + m, n0 + c);
     const int64_t at = (m0 + m) * a.N + n0 + c;
     if (a.bf16_out) {
       reinterpret_cast<uint16_t*>(a.Y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
@@ -140,6 +218,14 @@ hipError_t go_terms(const LinearArgs& a, hipStream_t s) {
 hipError_t launch_split(const SplitArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.K + 127) / 128), (unsigned)((a.M + 15) / 16));
   hipLaunchKernelGGL(split_kernel, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora(const LoraArgs& a, const SplitArgs* t, hipStream_t s) {
+  const int64_t panels = t ? (t->K + 127) / 128 : 1, split = t ? panels * ((t->M + 15) / 16) : 0;
+  const int64_t groups = split + a.M * (a.rank / kLoraRows);
+  if (groups > INT32_MAX) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(lora_kernel, dim3((unsigned)groups), dim3(256), 0, s, a, t ? *t : SplitArgs{}, (int)panels, (int)split);
   return hipGetLastError();
 }
 

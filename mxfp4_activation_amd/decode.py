@@ -1,5 +1,6 @@
-"""Decoding with 4-bit weights: linear layers and mixtures of experts for a
-few tokens, and the log probabilities of tokens.
+"""Decoding with 4-bit weights: linear layers, with low-rank adapters or without,
+and mixtures of experts for a few tokens; penalties, biases and masks on logits,
+and the log probabilities of tokens.
 
 The weights are what the library writes: codes and scales of the quantizers
 (``quant``) or of GPTQ-WUSH, unchanged.  Like ``ops``, these functions only
@@ -132,6 +133,50 @@ def linear_w4(fmt: str, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
     return out
 
 
+class LoraAdapters(NamedTuple):
+    """Low-rank adapters of one layer: A bf16 [adapters, rank, K], B bf16 [adapters, N,
+    rank] (rank a multiple of 8; pad with zeros) and their scales, float32 [adapters]."""
+    A: torch.Tensor
+    B: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+
+def linear_w4_lora(fmt: str, x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, adapters: LoraAdapters,
+                   ids: torch.Tensor, T: Optional[torch.Tensor] = None, global_scale: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``linear_w4`` plus each token's own low-rank adapter: x' W^T + scale[e] (x A[e]^T)
+    B[e]^T with e = ids[m] (int32 [M]; negative: no adapter, out of range: NaN) and x
+    untransformed.  The sums are fp32 and rounded once."""
+    f, G = _fmt(fmt)
+    ot = _out_type(out_dtype)
+    M, K, ldx = _rows(x, "x")
+    dev, stream = _enter(x, "x")
+    if codes.dim() != 2 or adapters.A.dim() != 3:
+        raise ValueError("codes must be 2-D and adapters.A [adapters, rank, K]")
+    N, (E, rank) = codes.shape[0], adapters.A.shape[:2]
+    pc = _check(codes, "codes", torch.uint8, (N, K // 2), dev)
+    ps = _check(scales, "scales", _scale_dtype(fmt), (N, K // G), dev)
+    pg, global_scale = _check_global(fmt, global_scale, "global_scale", 1, dev)
+    pt = None if T is None else _check(T, "T", torch.bfloat16, (K // G, G, G), dev)
+    pa = _check(adapters.A, "adapters.A", torch.bfloat16, (E, rank, K), dev)
+    pb = _check(adapters.B, "adapters.B", torch.bfloat16, (E, N, rank), dev)
+    pe = None if adapters.scale is None else _check(adapters.scale, "adapters.scale", torch.float32, (E,), dev)
+    pi = _check(ids, "ids", torch.int32, (M,), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _check(out, "out", out_dtype, (M, N), dev)
+    lib = _lib.load()
+    nw = lib.wush_linear_w4_lora_workspace(M, K, rank, 0 if T is None else 1, ot)
+    ws = _workspace(nw, dev)
+    st = lib.wush_linear_w4_lora(f, x.data_ptr(), ldx, pt, pc, ps, pg, pa, pb, pe, pi, E, rank, M, N, K, po, ot,
+                                 ws.data_ptr() if nw else None, nw, stream)
+    if st:
+        _lib.check(st, "wush_linear_w4_lora(%s)" % fmt)
+    return out
+
+
 class W4Experts(NamedTuple):
     """One projection of all experts in 4 bits: codes uint8 [E, rows, K/2],
     scales [E, rows, K/G], for NVFP4 the experts' tensor scales [E], and the block
@@ -195,6 +240,65 @@ def moe_w4(fmt: str, x: torch.Tensor, router: torch.Tensor, gate_up: W4Experts, 
     return MoeResult(out, ids, weights)
 
 
+def _logits(logits: torch.Tensor, name: str):
+    """(rows, vocabulary, type) of logits whose rows are contiguous."""
+    if logits.dim() != 2:
+        raise ValueError("%s must be [R, V]" % name)
+    if logits.dtype not in _LOGITS:
+        raise TypeError("%s must be float32, bfloat16 or float16 (got %s)" % (name, logits.dtype))
+    R, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return R, V, _LOGITS[logits.dtype]
+
+
+def adjust_logits(logits: torch.Tensor, prompt: Optional[torch.Tensor] = None, output: Optional[torch.Tensor] = None,
+                  repetition: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None, bias_ids: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, allowed: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Penalties, biases and grammar masks on logits [R, V] (float32, bfloat16 or
+    float16, rows V or more elements apart), in this order: tokens in prompt or output
+    (int32 [R, any], -1 pads) are divided (l > 0) or multiplied by repetition [R]; tokens
+    in output lose frequency [R] per occurrence and presence [R] once; bias [R, n] is added at
+    bias_ids [R, n] (int32, -1 pads); tokens whose bit of allowed (int32 [R, (V + 31) // 32],
+    bit v % 32 of word v // 32) is not set become -inf.  The penalties and biases are float32.
+    Returns a new tensor, or out, which may be logits itself."""
+    R, V, lt = _logits(logits, "logits")
+    dev, stream = _enter(logits, "logits")
+
+    def table(t, name, dtype):
+        if t is None:
+            return None, 0
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError("%s must be a tensor [R, n]" % name)
+        return _check(t, name, dtype, (R, t.shape[1]), dev), t.shape[1]
+
+    def row(t, name):
+        return None if t is None else _check(t, name, torch.float32, (R,), dev)
+
+    pp, n_prompt = table(prompt, "prompt", torch.int32)
+    po, n_output = table(output, "output", torch.int32)
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    pi, n_bias = table(bias_ids, "bias_ids", torch.int32)
+    pb = None if bias is None else _check(bias, "bias", torch.float32, (R, n_bias), dev)
+    pm = None if allowed is None else _check(allowed, "allowed", torch.int32, (R, (V + 31) // 32), dev)
+    if out is None:
+        out = torch.empty((R, V), dtype=logits.dtype, device=dev)
+    elif out is not logits:
+        if out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev:
+            raise ValueError("out must have the shape, type and device of logits")
+        _logits(out, "out")
+    st = _lib.load().wush_adjust_logits(logits.data_ptr(), lt, logits.stride(0), R, V, pp, n_prompt, po, n_output,
+                                        row(repetition, "repetition"), row(frequency, "frequency"),
+                                        row(presence, "presence"), pi, pb, n_bias, pm, out.data_ptr(), out.stride(0),
+                                        stream)
+    if st:
+        _lib.check(st, "wush_adjust_logits")
+    return out
+
+
 class TokenLogprobs(NamedTuple):
     logprob: torch.Tensor       # float32 [R]
     entropy: torch.Tensor       # float32 [R], in nats
@@ -207,15 +311,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0) ->
     scored, 0) under logits [R, V] (float32, bfloat16 or float16, rows V or more
     elements apart), the rows' entropies and their `top` most likely tokens (ties to the
     lower id).  Masked tokens (-inf) have probability 0 and are not listed."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be [R, V]")
-    if logits.dtype not in _LOGITS:
-        raise TypeError("logits must be float32, bfloat16 or float16 (got %s)" % logits.dtype)
-    R, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
-        raise ValueError("logits must have contiguous rows")
+    R, V, lt = _logits(logits, "logits")
     dev, stream = _enter(logits, "logits")
-    lt = _LOGITS[logits.dtype]
     pt = _check(targets, "targets", torch.int64, (R,), dev)
     values = torch.empty((2, R), dtype=torch.float32, device=dev)
     ids = torch.empty((R, max(top, 0)), dtype=torch.int32, device=dev)

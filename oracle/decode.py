@@ -140,3 +140,51 @@ def token_logprobs(logits, targets, top):
     bound = U * (n_sum * (1 + np.abs(mean)) + 8 * (1 + np.abs(mean)) + 4 * np.log(S))
     second = np.where(empty, 0.0, (z * np.where(e > 0, d, 0.0)).sum(1) / S)
     return score, entropy, ids, alt, bound + 4 * U * second
+
+
+def lora(x, A, B, scale, ids):
+    """(what the tokens' adapters add to a linear layer's result, bound) for x [M, K],
+    A [E, r, K], B [E, N, r], scale [E]."""
+    y = np.zeros((x.shape[0], B.shape[1]))
+    bound = np.zeros_like(y)
+    for m, e in enumerate(ids):
+        if e < 0:
+            continue
+        h = scale[e] * (A[e] @ x[m])
+        dh = np.abs(scale[e]) * (x.shape[1] + 4) * U * (np.abs(A[e]) @ np.abs(x[m]))
+        y[m] = B[e] @ h
+        bound[m] = np.abs(B[e]) @ dh + (B.shape[2] + 4) * U * (np.abs(B[e]) @ np.abs(h))
+    return y, bound
+
+
+def adjust_logits(logits, prompt, output, repetition, frequency, presence, bias_ids, bias, allowed):
+    """(logits, bound) after penalties, biases and masks; prompt, output, bias_ids: lists of
+    token ids per row (what is outside the vocabulary counts for nothing); allowed: truth
+    values [R, V] or None."""
+    out, bound = logits.copy(), np.zeros_like(logits)
+    R, V = logits.shape
+    for r in range(R):
+        ids = [t for t in output[r] if 0 <= t < V]
+        count = np.bincount(np.array(ids, np.int64), minlength=V).astype(np.float64)
+        seen = count > 0
+        seen[[t for t in prompt[r] if 0 <= t < V]] = True
+        l = out[r]
+        l = np.where(seen, np.where(l > 0, l / repetition[r], l * repetition[r]), l)
+        size = np.abs(l)
+        f = frequency[r] * count
+        l = np.where(count > 0, l - f - presence[r], l)
+        size = size + np.where(count > 0, 2 * np.abs(f) + 2 * np.abs(presence[r]), 0.0)
+        b, a, n = np.zeros(V), np.zeros(V), np.zeros(V)
+        for t, v in zip(bias_ids[r], bias[r]):
+            if 0 <= t < V:
+                b[t] += v
+                a[t] += abs(v)
+                n[t] += 1
+        l = l + b
+        # A rounding per operation, each relative to what has come together by then.
+        bound[r] = 4 * U * (size + a) + n * U * a
+        out[r] = l
+    if allowed is not None:
+        out = np.where(allowed, out, -np.inf)
+        bound = np.where(allowed, bound, 0.0)
+    return out, bound
