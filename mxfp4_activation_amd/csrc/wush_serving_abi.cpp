@@ -116,7 +116,7 @@ int64_t wush_kv4_attention_workspace(int64_t B, int64_t n, int64_t q_heads, int6
   if (D != 64 && D != 128 && D != 256) return 0;
   if (B > kMaxTokens || n > kMaxTokens || heads > kMaxHeads || q_heads > kMaxHeads || width > kMaxTokens / page) return 0;
   const wush::KvPlan p = wush::kv_plan(B, n, heads, q_heads / heads, (int)D, page * width);
-  return p.whole ? 0 : 4 * 2 * (int64_t)p.workgroups * wush::kv_piece(p.shape, (int)D);
+  return wush::kv_workspace(p, (int)D);
 }
 
 wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* T_q, const void* k_codes,
@@ -148,7 +148,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   if (!aligned(out, 16)) return fail(WUSH_EALIGN, "out must be 16-byte aligned");
   const wush::KvPlan plan = wush::kv_plan(B, n, heads, q_heads / heads, (int)D, page * width);
   // Items and units are counted in 32 bits.
-  if (plan.items > INT32_MAX / ((plan.whole ? 1 : page * width / wush::kKvUnit) + 2))
+  if (plan.items > INT32_MAX / (page * width / wush::kKvUnit + 2))
     return fail(WUSH_EINVAL, "too many tokens for one launch");
   const int64_t need = wush_kv4_attention_workspace(B, n, q_heads, heads, D, page, width);
   st = check_workspace(workspace, workspace_bytes, need);
@@ -187,7 +187,8 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.q_start = q_start;
   a.T = static_cast<const uint16_t*>(T_q);
   a.out = static_cast<uint16_t*>(out);
-  a.part = static_cast<float*>(workspace);
+  a.join = static_cast<wush::KvJoin*>(workspace);
+  a.part = reinterpret_cast<float*>(a.join + plan.runs);
   a.B = (int)B;
   a.n = (int)n;
   a.kv = (int)heads;
@@ -199,7 +200,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.window = (int)window;
   a.scale = (float)(scale * 1.4426950408889634);  // the kernels take powers of two
   a.workgroups = plan.workgroups;
-  a.whole = plan.whole;
+  a.runs = plan.runs;
   if (fmt == wush::kMXFP4) return launched(wush::launch_kv4_attention_mx(a, plan.shape, stream));
   if (fmt == wush::kNVFP4) return launched(wush::launch_kv4_attention_nv(a, plan.shape, stream));
   return launched(wush::launch_kv4_attention_int(a, plan.shape, stream));
