@@ -56,124 +56,165 @@ __device__ __forceinline__ void store_all(void* p, int64_t i, const float (&v)[k
   }
 }
 
-// f(token) for the tokens of a list that lie in [v0, v0 + n).
-template <typename F>
-__device__ __forceinline__ void each_token(const int32_t* list, int64_t count, int64_t v0, int n, F f) {
-  for (int64_t i = (int64_t)threadIdx.x * 4; i < count; i += kThreads * 4) {
-    int32_t t[4] = {-1, -1, -1, -1};
+// A thread's share of a row's list: the first kHeld entries were asked for when the kernel
+// began, the others are read when they are wanted.
+template <int HELD>
+struct List {
+  const int32_t* p;
+  int64_t count;
+  int32_t held[HELD][4];
+
+  __device__ __forceinline__ void read(int64_t i, int32_t (&t)[4]) const {
     if (i + 4 <= count) {
-      __builtin_memcpy(t, list + i, sizeof(t));
+      __builtin_memcpy(t, p + i, sizeof(t));
     } else {
-      for (int k = 0; k < (int)(count - i); ++k) t[k] = list[i + k];
-    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t at = t[k] - v0;
-      if (at >= 0 && at < n) f((int)at);
+      for (int k = 0; k < 4; ++k) t[k] = i + k < count ? p[i + k] : -1;
     }
   }
-}
+  __device__ __forceinline__ List(const int32_t* list, int64_t n, int64_t row) : p(list + row * n), count(n) {
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) read((int64_t)(h * kThreads + threadIdx.x) * 4, held[h]);
+  }
+  // f(token, place in the list) for the tokens in [v0, v0 + n).
+  template <typename F>
+  __device__ __forceinline__ void each(int64_t v0, int n, F f) const {
+    const auto four = [&](const int32_t (&t)[4], int64_t i) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t at = t[k] - v0;
+        if (at >= 0 && at < n) f((int)at, i + k);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) four(held[h], (int64_t)(h * kThreads + threadIdx.x) * 4);
+    for (int64_t i = (int64_t)(HELD * kThreads + threadIdx.x) * 4; i < count; i += kThreads * 4) {
+      int32_t t[4];
+      read(i, t);
+      four(t, i);
+    }
+  }
+};
 
-constexpr uint32_t kAsked = 0x80000000u;  // in the prompt; below it, how often in the output
+// A token's word in LDS: in the prompt, among the biases, and how often in the output.
+constexpr uint32_t kAsked = 0x80000000u, kBiased = 0x40000000u;
 
-// A workgroup takes CHUNK tokens of the vocabulary of one row.  It reads the row's whole
-// lists (from the cache, after the first workgroup) and keeps what falls into its chunk
-// in LDS: how often a token was said, and its bias.  Then the logits pass through once.
-// Counting with integers and adding a token's biases in the list's order makes the result
-// independent of the order of the atomics.  Bound by the logits' way in and out.
+// A workgroup takes CHUNK tokens of the vocabulary of one row.  It reads the row's lists
+// (from the cache, after the first workgroup), marks and counts the chunk's tokens in LDS,
+// and changes the logits in registers.  All that it can ask for is asked for before anything
+// else: the logits, and the lists' first entries.  Counts are integers, and a token that is
+// twice among the biases has them added up in the list's order, so nothing depends on the
+// order of the atomics.
 template <int TYPE, int CHUNK>
 __global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
-  extern __shared__ uint32_t lds[];
-  uint32_t* said = lds;
-  uint32_t* times = lds + CHUNK;                                // a token's entries among the biases
-  float* bias = reinterpret_cast<float*>(lds + 2 * CHUNK);
+  constexpr int kSteps = CHUNK / (kThreads * kEach);
+  __shared__ __attribute__((aligned(16))) uint32_t word[CHUNK];
+  __shared__ __attribute__((aligned(16))) float bias[CHUNK];
+  __shared__ int twice;
+  const int tid = threadIdx.x;
   const int64_t row = blockIdx.y, v0 = (int64_t)blockIdx.x * CHUNK;
   const int n = (int)(a.V - v0 < CHUNK ? a.V - v0 : CHUNK);
-  const bool counted = a.n_prompt > 0 || a.n_output > 0, biased = a.n_bias > 0;
-  if (counted)
-    for (int i = threadIdx.x; i < n; i += kThreads) said[i] = 0;
-  if (biased)
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      times[i] = 0;
-      bias[i] = 0.0f;
+  const List<2> prompt(a.prompt, a.n_prompt, row);
+  const List<1> output(a.output, a.n_output, row), biases(a.bias_ids, a.n_bias, row);
+  float v[kSteps][kEach];
+  uint32_t ok[kSteps];
+  const int32_t* bits = a.allowed ? a.allowed + row * ((a.V + 31) / 32) : nullptr;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int i = (s * kThreads + tid) * kEach;
+    if (i + kEach <= n) {
+      load_all<TYPE>(a.in, row * a.ld_in + v0 + i, v[s]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) v[s][k] = i + k < n ? load_one<TYPE>(a.in, row * a.ld_in + v0 + i + k) : 0.0f;
     }
-  __syncthreads();
-  each_token(a.prompt + row * a.n_prompt, a.n_prompt, v0, n, [&](int t) { atomicOr(&said[t], kAsked); });
-  each_token(a.output + row * a.n_output, a.n_output, v0, n, [&](int t) { atomicAdd(&said[t], 1u); });
-  if (biased) {
-    const int32_t* ids = a.bias_ids + row * a.n_bias;
-    const float* values = a.bias + row * a.n_bias;
-    each_token(ids, a.n_bias, v0, n, [&](int t) { atomicAdd(&times[t], 1u); });
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < a.n_bias; i += kThreads) {
-      const int64_t t = ids[i] - v0;
-      if (t < 0 || t >= n) continue;
-      float sum = values[i];
-      if (times[t] > 1) {
-        bool first = true;
-        for (int64_t j = 0; j < i && first; ++j) first = ids[j] != ids[i];
-        if (!first) continue;
-        for (int64_t j = i + 1; j < a.n_bias; ++j)
-          if (ids[j] == ids[i]) sum += values[j];
-      }
-      bias[t] = sum;
-    }
+    ok[s] = bits && i < n ? (uint32_t)bits[(v0 + i) >> 5] >> ((v0 + i) & 31) : 0xFFu;
   }
-  __syncthreads();
   const float rep = a.repetition ? a.repetition[row] : 1.0f;
   const float freq = a.frequency ? a.frequency[row] : 0.0f, pres = a.presence ? a.presence[row] : 0.0f;
-  const int32_t* bits = a.allowed ? a.allowed + row * ((a.V + 31) / 32) : nullptr;
-  const auto adjusted = [&](float l, int i, bool ok) {
-    if (counted) {
-      const uint32_t s = said[i];
-      if (s) {
-        l = l > 0.0f ? l / rep : l * rep;
-        const uint32_t c = s & ~kAsked;
-        if (c) l = l - freq * (float)c - pres;
+  const bool marked = a.n_prompt > 0 || a.n_output > 0 || a.n_bias > 0;
+  if (marked) {
+    for (int i = tid * 4; i < CHUNK; i += kThreads * 4) *reinterpret_cast<u32x4*>(&word[i]) = u32x4{0, 0, 0, 0};
+    if (tid == 0) twice = 0;
+    __syncthreads();
+    prompt.each(v0, n, [&](int t, int64_t) { atomicOr(&word[t], kAsked); });
+    output.each(v0, n, [&](int t, int64_t) { atomicAdd(&word[t], 1u); });
+    const float* values = a.bias + row * a.n_bias;
+    biases.each(v0, n, [&](int t, int64_t i) {
+      if (atomicOr(&word[t], kBiased) & kBiased) {
+        twice = 1;
+      } else {
+        bias[t] = values[i];
+      }
+    });
+    __syncthreads();
+    if (twice) {
+      for (int t = tid; t < n; t += kThreads) {
+        if (!(word[t] & kBiased)) continue;
+        float sum = 0.0f;
+        bool any = false;
+        for (int64_t j = 0; j < a.n_bias; ++j)
+          if (biases.p[j] - v0 == t) {
+            sum = any ? sum + values[j] : values[j];
+            any = true;
+          }
+        bias[t] = sum;
+      }
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int i = (s * kThreads + tid) * kEach;
+    if (i >= n) continue;
+    const int64_t at = v0 + i;
+    if (marked) {
+      uint32_t w[kEach], any = 0;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        w[k] = word[i + k];
+        any |= w[k];
+      }
+      if (any) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const uint32_t said = w[k] & ~kBiased, count = said & ~kAsked;
+          float l = v[s][k];
+          if (said) l = l > 0.0f ? l / rep : l * rep;
+          if (count) l = l - freq * (float)count - pres;
+          if (w[k] & kBiased) l += bias[i + k];
+          v[s][k] = l;
+        }
       }
     }
-    if (biased && times[i]) l += bias[i];
-    return ok ? l : -__builtin_inff();
-  };
-  for (int i = threadIdx.x * kEach; i < n; i += kThreads * kEach) {
-    const int64_t at = v0 + i;
-    const uint32_t ok = bits ? (uint32_t)bits[at >> 5] >> (at & 31) : 0xFFu;
-    if (i + kEach <= n) {
-      float v[kEach];
-      load_all<TYPE>(a.in, row * a.ld_in + at, v);
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) v[k] = adjusted(v[k], i + k, (ok >> k) & 1u);
-      store_all<TYPE>(a.out, row * a.ld_out + at, v);
+    for (int k = 0; k < kEach; ++k) v[s][k] = (ok[s] >> k) & 1u ? v[s][k] : -__builtin_inff();
+    if (i + kEach <= n) {
+      store_all<TYPE>(a.out, row * a.ld_out + at, v[s]);
     } else {
-      for (int k = 0; k < n - i; ++k)
-        store_one<TYPE>(a.out, row * a.ld_out + at + k,
-                        adjusted(load_one<TYPE>(a.in, row * a.ld_in + at + k), i + k, (ok >> k) & 1u));
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (i + k < n) store_one<TYPE>(a.out, row * a.ld_out + at + k, v[s][k]);
     }
   }
 }
 
-template <int TYPE, int CHUNK>
-hipError_t go(const AdjustArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.V + CHUNK - 1) / CHUNK), (unsigned)a.R);
-  const unsigned lds = a.n_bias > 0 ? 3 * CHUNK * 4 : CHUNK * 4;
-  hipLaunchKernelGGL((adjust_kernel<TYPE, CHUNK>), grid, dim3(kThreads), lds, s, a);
-  return hipGetLastError();
-}
-
-// Chunks as wide as leaves the chip about two workgroups per compute unit.
+// Chunks of 2048: 200 rows of 100003 fp32 logits take 44.6 us (3.6 TB/s), with 4096 54, for
+// then half as many workgroups' loads are in flight; one row of 131072 bf16 logits 5.1 and 6.9.
 template <int TYPE>
-hipError_t go_chunk(const AdjustArgs& a, hipStream_t s) {
-  if (a.R * (a.V / 4096) >= 512) return go<TYPE, 4096>(a, s);
-  if (a.R * (a.V / 2048) >= 256) return go<TYPE, 2048>(a, s);
-  return go<TYPE, 512>(a, s);
+hipError_t go(const AdjustArgs& a, hipStream_t s) {
+  constexpr int kChunk = 2048;
+  const dim3 grid((unsigned)((a.V + kChunk - 1) / kChunk), (unsigned)a.R);
+  hipLaunchKernelGGL((adjust_kernel<TYPE, kChunk>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_adjust(const AdjustArgs& a, hipStream_t s) {
-  if (a.type == 0) return go_chunk<0>(a, s);
-  if (a.type == 1) return go_chunk<1>(a, s);
-  return go_chunk<2>(a, s);
+  if (a.type == 0) return go<0>(a, s);
+  if (a.type == 1) return go<1>(a, s);
+  return go<2>(a, s);
 }
 
 }  // namespace wush
