@@ -499,7 +499,7 @@ wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void*
                                 const float* adapter_scale, const int32_t* ids, int64_t adapters, int64_t rank,
                                 int64_t M, int64_t N, int64_t K, void* Y, int out_type, void* workspace,
                                 int64_t workspace_bytes, hipStream_t stream);
-int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t K, int64_t rank, int transform, int out_type);
+int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t rank, int transform, int out_type);
 
 /* Penalties, biases and masks on rows of logits, before wush_token_logprobs or a sampler.  For
  * token v of row r, with c = how often v is in output[r], in fp32 and in this order:

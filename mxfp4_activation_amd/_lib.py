@@ -53,7 +53,7 @@ SIGNATURES = {
     "wush_kv4_attention_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64, _i64, _i64]),
     "wush_linear_w4_lora": (_c_int, [_c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                                      _i64, _vp, _c_int, _vp, _i64, _vp]),
-    "wush_linear_w4_lora_workspace": (_i64, [_i64, _i64, _i64, _c_int, _c_int]),
+    "wush_linear_w4_lora_workspace": (_i64, [_i64, _i64, _i64, _i64, _c_int, _c_int]),
     "wush_adjust_logits": (_c_int, [_vp, _c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
                                     _vp, _vp, _i64, _vp]),
     "wush_status_string": (ctypes.c_char_p, [_c_int]),

@@ -55,6 +55,20 @@ wush_status check_cache(int fmt, int64_t heads, int64_t D, int64_t page, int64_t
   return WUSH_OK;
 }
 
+struct LoraWorkspace {
+  uint64_t h, delta, planes, total;
+};
+
+LoraWorkspace lora_workspace(int64_t M, int64_t N, int64_t K, int64_t rank, bool transform, int out_type) {
+  const uint64_t c = (uint64_t)(M < wush::kLoraChunk ? M : wush::kLoraChunk);
+  LoraWorkspace w;
+  w.h = 0;
+  w.delta = round16(c * rank * 4);
+  w.planes = w.delta + (M > wush::kLoraTogether ? round16(c * N * 4) : 0);
+  w.total = w.planes + (transform ? 2 * terms_of(out_type) * c * K : 0);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -206,10 +220,10 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   return launched(wush::launch_kv4_attention_int(a, plan.shape, stream));
 }
 
-int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t K, int64_t rank, int transform, int out_type) {
-  if (M <= 0 || K <= 0 || K > kMaxK || M > kMaxLoraRows || rank <= 0 || rank > kMaxRank) return 0;
+int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t rank, int transform, int out_type) {
+  if (M <= 0 || N <= 0 || N > kMaxDim || K <= 0 || K > kMaxK || M > kMaxLoraRows || rank <= 0 || rank > kMaxRank) return 0;
   if (out_type != WUSH_OUT_F32 && out_type != WUSH_OUT_BF16) return 0;
-  return (int64_t)round16((uint64_t)M * rank * 4) + (transform ? wush_linear_w4_workspace(M, K, out_type) : 0);
+  return (int64_t)lora_workspace(M, N, K, rank, transform != 0, out_type).total;
 }
 
 wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void* T, const void* codes,
@@ -240,7 +254,8 @@ wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void*
   if (!aligned(Y, (uintptr_t)out_bytes_of(out_type))) return fail(WUSH_EALIGN, "Y must be aligned to its elements");
   if (!aligned(A, 16) || !aligned(B, 16)) return fail(WUSH_EALIGN, "A and B must be 16-byte aligned");
   if (!aligned(ids, 4) || !aligned(adapter_scale, 4)) return fail(WUSH_EALIGN, "ids and adapter_scale must be 4-byte aligned");
-  const int64_t need = wush_linear_w4_lora_workspace(M, K, rank, T != nullptr, out_type);
+  const LoraWorkspace w = lora_workspace(M, N, K, rank, T != nullptr, out_type);
+  const int64_t need = (int64_t)w.total;
   st = check_workspace(workspace, workspace_bytes, need);
   if (st != WUSH_OK) return st;
   const Range ins[] = {{X, ((uint64_t)(M - 1) * (M > 1 ? ldx : 0) + K) * 2},
@@ -257,48 +272,55 @@ wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void*
   st = check_device();
   if (st != WUSH_OK) return st;
 
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   wush::LinearArgs a{};
   a.fmt = fmt;
-  a.x.X = static_cast<const uint16_t*>(X);
-  a.x.ldx = M > 1 ? ldx : 0;
-  a.x.terms = 1;
   a.codes = static_cast<const uint8_t*>(codes);
   a.scales = static_cast<const uint8_t*>(scales);
   a.gs = global_scale;
-  a.Y = Y;
-  a.M = M;
   a.N = N;
   a.K = K;
   a.bf16_out = out_type == WUSH_OUT_BF16;
-  a.lora.X = a.x.X;
-  a.lora.ldx = a.x.ldx;
+  a.lora.ldx = M > 1 ? ldx : 0;
   a.lora.A = static_cast<const uint16_t*>(A);
   a.lora.B = static_cast<const uint16_t*>(B);
   a.lora.scale = adapter_scale;
-  a.lora.ids = ids;
-  a.lora.h = static_cast<float*>(workspace);
-  a.lora.M = M;
+  a.lora.h = reinterpret_cast<float*>(ws + w.h);
+  a.lora.delta = M > wush::kLoraTogether ? reinterpret_cast<float*>(ws + w.delta) : nullptr;
   a.lora.K = K;
   a.lora.E = adapters;
   a.lora.rank = (int)rank;
-  wush::SplitArgs t{};
-  if (T) {
-    t.X = a.x.X;
-    t.ldx = a.x.ldx;
-    t.T = static_cast<const uint16_t*>(T);
-    t.out = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + round16((uint64_t)M * rank * 4));
-    t.M = M;
-    t.K = K;
-    t.G = group_of(fmt);
-    t.terms = terms_of(out_type);
-    a.x.X = t.out;
-    a.x.ldx = K;
-    a.x.plane = M * K;
-    a.x.terms = t.terms;
+  for (int64_t m0 = 0; m0 < M; m0 += wush::kLoraChunk) {
+    const int64_t m = M - m0 < wush::kLoraChunk ? M - m0 : wush::kLoraChunk;
+    a.M = a.lora.M = m;
+    a.Y = static_cast<uint8_t*>(Y) + m0 * N * out_bytes_of(out_type);
+    a.lora.X = static_cast<const uint16_t*>(X) + m0 * a.lora.ldx;
+    a.lora.ids = ids + m0;
+    a.x.X = a.lora.X;
+    a.x.ldx = a.lora.ldx;
+    a.x.plane = 0;
+    a.x.terms = 1;
+    wush::SplitArgs t{};
+    if (T) {
+      t.X = a.lora.X;
+      t.ldx = a.lora.ldx;
+      t.T = static_cast<const uint16_t*>(T);
+      t.out = reinterpret_cast<uint16_t*>(ws + w.planes);
+      t.M = m;
+      t.K = K;
+      t.G = group_of(fmt);
+      t.terms = terms_of(out_type);
+      a.x.X = t.out;
+      a.x.ldx = K;
+      a.x.plane = m * K;
+      a.x.terms = t.terms;
+    }
+    st = launched(wush::launch_lora(a.lora, T ? &t : nullptr, stream));
+    if (st == WUSH_OK && a.lora.delta) st = launched(wush::launch_lora_expand(a.lora, N, stream));
+    if (st == WUSH_OK) st = launched(wush::launch_linear_w4(a, stream));
+    if (st != WUSH_OK) return st;
   }
-  st = launched(wush::launch_lora(a.lora, T ? &t : nullptr, stream));
-  if (st != WUSH_OK) return st;
-  return launched(wush::launch_linear_w4(a, stream));
+  return WUSH_OK;
 }
 
 wush_status wush_adjust_logits(const void* logits, int logit_type, int64_t ld, int64_t R, int64_t V,

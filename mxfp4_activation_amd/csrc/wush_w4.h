@@ -28,7 +28,11 @@ struct SplitArgs {
   int G, terms;
 };
 
-// Low-rank adapters of a batch: Y[m] += h[m] B[ids[m]]^T, h from launch_lora.
+// Low-rank adapters of a batch: Y[m] += h[m] B[ids[m]]^T, h from launch_lora.  The product
+// takes what it adds from delta, which launch_lora_expand writes, or for a few tokens
+// forms it itself, which saves a launch.
+constexpr int kLoraTogether = 8;    // tokens up to which it does
+constexpr int64_t kLoraChunk = 256;  // tokens that share a workspace
 struct LoraArgs {
   const uint16_t* X;   // bf16 [M], row stride ldx
   int64_t ldx;
@@ -37,6 +41,7 @@ struct LoraArgs {
   const float* scale;  // [E] or null
   const int32_t* ids;  // [M]: negative, none; E or more, NaN
   float* h;            // [M][rank]: scale[ids[m]] A[ids[m]] x[m]
+  float* delta;        // [M][N] or null
   int64_t M, K, E;
   int rank;            // a multiple of 8
 };
@@ -100,6 +105,7 @@ hipError_t launch_split(const SplitArgs& a, hipStream_t s);
 hipError_t launch_linear_w4(const LinearArgs& a, hipStream_t s);
 // h of the adapters and, where t is not null, also what launch_split does.
 hipError_t launch_lora(const LoraArgs& a, const SplitArgs* t, hipStream_t s);
+hipError_t launch_lora_expand(const LoraArgs& a, int64_t N, hipStream_t s);
 
 // Log probabilities, entropy and largest entries of rows of logits.
 constexpr int kLogprobMaxTop = 32;

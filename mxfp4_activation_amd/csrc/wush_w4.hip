@@ -80,7 +80,75 @@ __global__ __launch_bounds__(256) void lora_kernel(LoraArgs a, SplitArgs t, int 
   lora_rows(a, (b - split) / per, (b - split) % per * kLoraRows, sums);
 }
 
-// What token m's adapter adds to result n: NaN for an adapter that is not there.
+// v plus the values of the other lanes of its aligned group of 1 << LOG2 lanes.  (Once
+// pairs and quads agree, mirroring a half row or row serves as well as an exchange.)
+template <int LOG2>
+__device__ __forceinline__ float sum_group(float v) {
+  const auto plus = [&](uint32_t o) { v += __uint_as_float(o); };
+  if (LOG2 > 0) plus(dpp<0xB1, 0xf>(0, __float_as_uint(v)));   // quad_perm 1 0 3 2
+  if (LOG2 > 1) plus(dpp<0x4E, 0xf>(0, __float_as_uint(v)));   // quad_perm 2 3 0 1
+  if (LOG2 > 2) plus(dpp<0x141, 0xf>(0, __float_as_uint(v)));  // row_half_mirror
+  if (LOG2 > 3) plus(dpp<0x140, 0xf>(0, __float_as_uint(v)));  // row_mirror
+  if (LOG2 > 4) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if (LOG2 > 5) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float dot8(const u32x4& w, const f32x4& h0, const f32x4& h1) {
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v = __builtin_fmaf(bf16_lo(w[k]), k < 2 ? h0[2 * k] : h1[2 * k - 4], v);
+    v = __builtin_fmaf(bf16_hi(w[k]), k < 2 ? h0[2 * k + 1] : h1[2 * k - 3], v);
+  }
+  return v;
+}
+
+// delta[m][n] = B[ids[m]] h[m]; 0 without an adapter, NaN for one that is not there.  A row of B is read by 1 << LOG2
+// neighbouring lanes, 16 bytes each, so that a wave reads whole lines, kLoraBlocks times 1 KB at
+// a time; the lanes of a row add up.  Many small waves: B is most of what a batch over many
+// adapters reads, and the product's own workgroups are too few to wait for it.
+constexpr int kLoraBlocks = 4;
+template <int LOG2>
+__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int64_t N) {
+  constexpr int kPer = 64 >> LOG2;  // rows of a wave's load
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m = blockIdx.y, id = a.ids[m];
+  const bool with = id >= 0 && id < a.E;
+  const int piece = lane & ((1 << LOG2) - 1), pieces = a.rank / 8;
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * (kPer * kLoraBlocks) + (lane >> LOG2);
+  if (!with) {
+    const float none = id < 0 ? 0.0f : __builtin_nanf("");
+#pragma unroll
+    for (int u = 0; u < kLoraBlocks; ++u)
+      if (piece == 0 && n0 + u * kPer < N) a.delta[m * N + n0 + u * kPer] = none;
+    return;
+  }
+  f32x4 h0 = {0, 0, 0, 0}, h1 = {0, 0, 0, 0};
+  if (piece < pieces) {
+    h0 = *reinterpret_cast<const f32x4*>(a.h + m * a.rank + 8 * piece);
+    h1 = *reinterpret_cast<const f32x4*>(a.h + m * a.rank + 8 * piece + 4);
+  }
+  u32x4 w[kLoraBlocks];
+#pragma unroll
+  for (int u = 0; u < kLoraBlocks; ++u) {
+    const int64_t n = n0 + u * kPer < N ? n0 + u * kPer : N - 1;
+    w[u] = *reinterpret_cast<const u32x4*>(a.B + (id * N + n) * a.rank + 8 * (piece < pieces ? piece : 0));
+  }
+#pragma unroll
+  for (int u = 0; u < kLoraBlocks; ++u) {
+    const float v = sum_group<LOG2>(piece < pieces ? dot8(w[u], h0, h1) : 0.0f);
+    if (piece == 0 && n0 + u * kPer < N) a.delta[m * N + n0 + u * kPer] = v;
+  }
+}
+
+// What token m's adapter adds to result n: nothing without one, NaN for one that is not there.
 __device__ __forceinline__ float lora_term(const LoraArgs& a, int64_t N, int64_t m, int64_t n) {
   const int64_t id = a.ids[m];
   if (id < 0) return 0.0f;
@@ -88,15 +156,8 @@ __device__ __forceinline__ float lora_term(const LoraArgs& a, int64_t N, int64_t
   const uint16_t* b = a.B + (id * N + n) * a.rank;
   const float* h = a.h + m * a.rank;
   float v = 0.0f;
-  for (int r = 0; r < a.rank; r += 8) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(b + r);
-    const f32x4 h0 = *reinterpret_cast<const f32x4*>(h + r), h1 = *reinterpret_cast<const f32x4*>(h + r + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v = __builtin_fmaf(bf16_lo(w[i]), i < 2 ? h0[2 * i] : h1[2 * i - 4], v);
-      v = __builtin_fmaf(bf16_hi(w[i]), i < 2 ? h0[2 * i + 1] : h1[2 * i - 3], v);
-    }
-  }
+  for (int r = 0; r < a.rank; r += 8)
+    v += dot8(*reinterpret_cast<const u32x4*>(b + r), *reinterpret_cast<const f32x4*>(h + r), *reinterpret_cast<const f32x4*>(h + r + 4));
   return v;
 }
 
@@ -130,17 +191,39 @@ __global__ __launch_bounds__(64 * WN * WK, (min_waves<FMT, R, NT, TERMS>())) voi
   group_dot<FMT, R, D, NT, TERMS, SPREAD, WN, WK>(
       lds, p, [] {}, [&](int row) { return X + row * ldx; }, a.x.plane, rows, a.K);
   const float g = FMT == kNV ? a.gs[0] : 1.0f;
-  for (int o = threadIdx.x; o < rows * kRows; o += 64 * WN * WK) {
+  constexpr int kThreads = 64 * WN * WK;
+  const auto result = [&](int o, auto more) {
     const int m = o / kRows, c = o % kRows;
-    if (n0 + c >= a.N) continue;
+    if (n0 + c >= a.N) return;
     float v = group_sum<R, WN, WK>(lds, c, m, rows);
     if (FMT == kNV) v *= g;
-    if (a.lora.ids) v += lora_term(a.lora, a.N, m0 + m, n0 + c);
+    v = more(v, m0 + m, n0 + c);
     const int64_t at = (m0 + m) * a.N + n0 + c;
     if (a.bf16_out) {
       reinterpret_cast<uint16_t*>(a.Y)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
     } else {
       reinterpret_cast<float*>(a.Y)[at] = v;
+    }
+  };
+  if (!a.lora.ids) {
+    for (int o = threadIdx.x; o < rows * kRows; o += kThreads) result(o, [](float v, int64_t, int64_t) { return v; });
+  } else if (!a.lora.delta) {
+    for (int o = threadIdx.x; o < rows * kRows; o += kThreads)
+      result(o, [&](float v, int64_t m, int64_t n) { return v + lora_term(a.lora, a.N, m, n); });
+  } else {
+    // Four results' parts asked for at a time: one by one they cost 12 of 54 us (64 tokens,
+    // 24576 x 4096 NVFP4).
+    for (int o0 = threadIdx.x; o0 < rows * kRows; o0 += 4 * kThreads) {
+      float d[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int o = o0 + u * kThreads, m = o / kRows, c = o % kRows;
+        d[u] = o < rows * kRows && n0 + c < a.N ? a.lora.delta[(m0 + m) * a.N + n0 + c] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (o0 + u * kThreads < rows * kRows)
+          result(o0 + u * kThreads, [&](float v, int64_t, int64_t) { return v + d[u]; });
     }
   }
 }
@@ -227,6 +310,26 @@ hipError_t launch_lora(const LoraArgs& a, const SplitArgs* t, hipStream_t s) {
   if (groups > INT32_MAX) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(lora_kernel, dim3((unsigned)groups), dim3(256), 0, s, a, t ? *t : SplitArgs{}, (int)panels, (int)split);
   return hipGetLastError();
+}
+
+namespace {
+template <int LOG2>
+hipError_t expand(const LoraArgs& a, int64_t N, hipStream_t s) {
+  constexpr int kRows = 4 * kLoraBlocks * (64 >> LOG2);
+  hipLaunchKernelGGL(lora_expand_kernel<LOG2>, dim3((unsigned)((N + kRows - 1) / kRows), (unsigned)a.M), dim3(256), 0, s, a, N);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_lora_expand(const LoraArgs& a, int64_t N, hipStream_t s) {
+  const int pieces = a.rank / 8;
+  if (pieces == 1) return expand<0>(a, N, s);
+  if (pieces == 2) return expand<1>(a, N, s);
+  if (pieces <= 4) return expand<2>(a, N, s);
+  if (pieces <= 8) return expand<3>(a, N, s);
+  if (pieces <= 16) return expand<4>(a, N, s);
+  if (pieces <= 32) return expand<5>(a, N, s);
+  return expand<6>(a, N, s);
 }
 
 hipError_t launch_linear_w4(const LinearArgs& a, hipStream_t s) {

@@ -168,7 +168,7 @@ def linear_w4_lora(fmt: str, x: torch.Tensor, codes: torch.Tensor, scales: torch
     else:
         po = _check(out, "out", out_dtype, (M, N), dev)
     lib = _lib.load()
-    nw = lib.wush_linear_w4_lora_workspace(M, K, rank, 0 if T is None else 1, ot)
+    nw = lib.wush_linear_w4_lora_workspace(M, N, K, rank, 0 if T is None else 1, ot)
     ws = _workspace(nw, dev)
     st = lib.wush_linear_w4_lora(f, x.data_ptr(), ldx, pt, pc, ps, pg, pa, pb, pe, pi, E, rank, M, N, K, po, ot,
                                  ws.data_ptr() if nw else None, nw, stream)
