@@ -34,13 +34,14 @@ hipError_t launch_kv4_append(const KvAppendArgs& a, hipStream_t s);
 // kKvUnit tokens of an item.
 constexpr int kKvUnit = 128;
 
-// Workspace: what the second kernel has to join per run, then two pieces per run.
+// Workspace: the number of places for pieces that may hold one (in the first one's `pieces`),
+// then one of these per place, then the pieces.
 struct KvJoin {
-  int32_t pieces, second;  // of the item that begins in this run and goes on: their number (0: none
-                           // is), whether the first stands in the run's second place
-  int32_t cols, col0;      // columns, and the first one's place in the sequence
-  int32_t start, head;     // row of the sequence's first query, key head
-  int32_t pad[2];
+  int32_t pieces;       // of the item whose first piece is here; otherwise 0
+  int32_t next, step;   // the others' places: next, next + step, ...
+  int32_t cols, col0;   // columns, and the first one's place in the sequence
+  int32_t start, head;  // row of the sequence's first query, key head
+  int32_t pad;
 };
 
 struct KvAttnArgs {
@@ -55,16 +56,15 @@ struct KvAttnArgs {
   const int32_t* q_start;    // [B + 1], or null: query b is sequence b's
   const uint16_t* T;         // bf16 [kv][D/G][G][G] or null
   uint16_t* out;             // bf16 [n][kv * group][D]
-  KvJoin* join;              // [runs]
-  float* part;               // [runs][2] pieces
+  KvJoin* join;              // [1 + 2 runs]
+  float* part;               // [2 runs] pieces
   int B, n, kv, group, D, page_log2, width, pages;
   int window;                // 0: none
   float scale;               // of the scores, times log2 e
-  int workgroups, runs;
+  int workgroups, runs;      // as in KvPlan
 };
 
-// How a call is cut: columns per workgroup, workgroups, and the runs of units that items
-// may be cut into.
+// How a call is cut: columns per workgroup, and the pieces that the device aims at.
 enum { kKvNarrow, kKvWide, kKvPrompt };  // four waves share columns, the same with twice as many, waves have their own
 // Tiles of 16 columns per wave: one where the results of two would not fit the registers.
 constexpr int kv_tiles(int shape, int D) { return shape == kKvNarrow || D > 128 ? 1 : 2; }
@@ -73,12 +73,12 @@ constexpr int kv_columns(int shape, int D) { return 16 * kv_tiles(shape, D) * (s
 constexpr int kv_resident(int shape, int D) { return shape == kKvNarrow ? (D == 64 ? 1024 : D == 128 ? 768 : 512) : 512; }
 
 struct KvPlan {
-  int shape, workgroups, runs;  // runs 0: every item is taken whole, without a workspace
-  int64_t items;                // at most
+  int shape;
+  int runs;  // shares that the units are divided into; 0: every item is taken whole, without a workspace
+  int64_t items, workgroups;  // at most
 };
 
 constexpr int64_t kKvWholeTokens = 512;  // up to here an item is not worth cutting
-constexpr int64_t kKvMaxGroups = 1 << 20;
 
 inline KvPlan kv_plan(int64_t B, int64_t n, int64_t kv, int64_t group, int D, int64_t tokens) {
   KvPlan p;
@@ -87,20 +87,20 @@ inline KvPlan kv_plan(int64_t B, int64_t n, int64_t kv, int64_t group, int D, in
   // Each sequence ends in a part of an item; sequences without queries have none.
   const int64_t seqs = B < n ? B : n;
   p.items = (n * group / kv_columns(p.shape, D) + seqs) * kv;
-  const int64_t resident = kv_resident(p.shape, D);
   const int64_t units = p.items * ((tokens + kKvUnit - 1) / kKvUnit + 1);
-  p.runs = (int)(tokens <= kKvWholeTokens && p.items < kKvMaxGroups ? 0 : units < resident ? units : resident);
-  // Whether items are cut is for the device to say, which knows the lengths; it may
-  // take as many as there are workgroups whole.
-  const int64_t most = p.items < kKvMaxGroups ? p.items : p.runs;
-  p.workgroups = (int)(most > p.runs ? most : p.runs);
+  const int64_t resident = kv_resident(p.shape, D);
+  p.runs = (int)(tokens <= kKvWholeTokens ? 0 : units < resident ? units : resident);
+  // Pieces of ceil(all units / runs) are at most runs and one more per item.
+  p.workgroups = p.items + p.runs;
   return p;
 }
 
 // Floats of one piece of an item: maxima, sums, results.
 inline int64_t kv_piece(int shape, int D) { return (int64_t)kv_columns(shape, D) * (D + 2); }
+// Cut into pieces of a share, an item has less than 2 units / share of them, so all items together
+// less than 2 runs; cut by runs, every run has at most two pieces of items that are not whole.
 inline int64_t kv_workspace(const KvPlan& p, int D) {
-  return p.runs * ((int64_t)sizeof(KvJoin) + 2 * 4 * kv_piece(p.shape, D));
+  return p.runs ? (1 + 2 * (int64_t)p.runs) * (int64_t)sizeof(KvJoin) + 2 * (int64_t)p.runs * 4 * kv_piece(p.shape, D) : 0;
 }
 
 hipError_t launch_kv4_attention_mx(const KvAttnArgs& a, int shape, hipStream_t s);

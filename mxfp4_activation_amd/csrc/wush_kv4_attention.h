@@ -9,10 +9,9 @@
 // Work.  An item is one key head's queries of one sequence: up to 16, 32 or 128
 // columns (query, head of the group).  Its tokens come in units of 128.  Items
 // and units are counted on the device, from the lengths as they are when the kernel
-// runs; every workgroup takes an equal run of units, so that one long sequence
-// among short ones is spread over the whole chip.  An item that a run's border
-// cuts leaves its pieces (maximum, sum, unscaled result) in the workspace, and a
-// second kernel joins them.
+// runs, and items of more than a share of them are cut into pieces of about that many, one
+// per workgroup, so that one long sequence among short ones is spread over the whole chip.
+// Pieces (maximum, sum, unscaled result) meet in a second kernel by way of the workspace.
 //
 // A wave's step is 32 tokens, all of it in registers: no LDS, no barrier.
 //   S = K Q^T with v_mfma_f32_16x16x32_bf16, A = 16 tokens, B = 16 columns: lane
@@ -39,6 +38,8 @@
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "wush_kv4.h"
 #include "wush_w4_core.h"
@@ -114,147 +115,206 @@ __device__ __forceinline__ int wave_scan(int v) {
   return (int)u;
 }
 
-// A sequence's share of the work, per key head: units, items, the most units of an item.
+// What a sequence and key head's items come to in units, all together and at most, and
+// cut for a share of units: in pieces, and in pieces of items that have several.
 struct Load {
-  int units, items, most;
+  int units, items, most, pieces, cut;
 };
 template <int NC>
-__device__ __forceinline__ Load load_of(const KvAttnArgs& a, const Seq& s) {
-  Load l = {0, items_of<NC>(a, s), 0};
+__device__ __forceinline__ Load load_of(const KvAttnArgs& a, const Seq& s, int share) {
+  Load l = {0, items_of<NC>(a, s), 0, 0, 0};
   for (int t = 0; t < l.items; ++t) {
     const int u = units_of<NC>(a, s, t);
+    const int p = (u - 1) / share + 1;
     l.units += u;
     l.most = l.most > u ? l.most : u;
+    l.pieces += p;
+    l.cut += p > 1 ? p : 0;
   }
   return l;
 }
 
-struct PlanLds {
-  int units[4], items[4], most[4];
-  int b, base, per_head;
-  Seq s;
-};
-
-// The sequences c .. c + 255, one per thread: its own, its load, the units and items
-// before it, and their sums over all.
-struct Chunk {
-  Seq s;
-  Load own;
-  int units, items;                // of the chunk, before the thread's
-  int all_units, all_items, most;  // of the chunk
-};
-template <int NC>
-__device__ __forceinline__ Chunk chunk_of(const KvAttnArgs& a, PlanLds& l, int c) {
-  const int b = c + (int)threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  Chunk k;
-  k.s = Seq{0, 0, 0, false};
-  k.own = Load{0, 0, 0};
-  if (b < a.B) {
-    k.s = seq_of(a, b);
-    k.own = load_of<NC>(a, k.s);
-    k.own.units *= a.kv;
-    k.own.items *= a.kv;
-  }
-  const int units = wave_scan(k.own.units), items = wave_scan(k.own.items), most = wave_max_int(k.own.most);
-  __syncthreads();  // the chunk before is done with
-  if (lane == 63) {
-    l.units[wave] = units;
-    l.items[wave] = items;
-    l.most[wave] = most;
-  }
-  __syncthreads();
-  k.units = units - k.own.units;
-  k.items = items - k.own.items;
-  k.all_units = k.all_items = k.most = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) {
-      k.units += l.units[w];
-      k.items += l.items[w];
-    }
-    k.all_units += l.units[w];
-    k.all_items += l.items[w];
-    k.most = k.most > l.most[w] ? k.most : l.most[w];
-  }
-  return k;
-}
-
-// How the call's work is shared out: by whole items, or by units.
-struct Shares {
-  bool whole;
-  int total, share;  // items or units, in all and per workgroup
-};
-
-// Items are taken whole where nothing may be cut, and where there are enough of about the
-// same length: the longest times the rounds of them is at most 1.3 times the mean share.
-// (Two prompts of 1000 queries behind 16384 tokens, 456 items for 512 places: 105 us of
-// joining and 60 MB of pieces less, for 12% longer runs.)
-template <int NC>
-__device__ __forceinline__ Shares shares_of(const KvAttnArgs& a, PlanLds& l, Chunk& first) {
-  first = chunk_of<NC>(a, l, 0);
-  int units = first.all_units, items = first.all_items, most = first.most;
-  for (int c = kThreads; c < a.B; c += kThreads) {
-    const Chunk k = chunk_of<NC>(a, l, c);
-    units += k.all_units;
-    items += k.all_items;
-    most = most > k.most ? most : k.most;
-  }
-  units = uniform(units);
-  items = uniform(items);
-  most = uniform(most);
-  Shares s;
-  s.whole = a.runs == 0 ||
-            (items <= a.workgroups && (float)most * (float)((items + a.runs - 1) / a.runs) * (float)a.runs <= 1.3f * (float)units);
-  s.total = s.whole ? items : units;
-  s.share = s.whole ? 1 : (units + a.runs - 1) / a.runs;
-  return s;
-}
-
-// Where a unit (or whole item) is: sequence, key head, item, and the unit's place in it.
+// A piece: sequence, key head, item, units of the item, of it from `off` on `take`; its place
+// in the workspace; how many there are of the item, and which one it is.
 struct Place {
-  int b, h, t, off;
+  int b, h, t, units, off, take, slot, pieces, index;
   Seq s;
 };
 
-// The place of number u < total, for the whole workgroup.
+struct PlanLds {
+  int sums[3][4];
+  int b, pieces, cut, per_head, cut_per_head;
+  Seq s;
+  Place at;  // of a run's piece, while the waves are at it
+  int left;
+};
+
+// A sequence per lane where there are no more (every wave for itself), otherwise one per
+// thread, 256 at a time.
+__device__ __forceinline__ bool few(const KvAttnArgs& a) { return a.B <= 64; }
+__device__ __forceinline__ int place_of(const KvAttnArgs& a) { return few(a) ? threadIdx.x & 63 : threadIdx.x; }
+__device__ __forceinline__ Seq seq_or_none(const KvAttnArgs& a, int b) { return b < a.B ? seq_of(a, b) : Seq{0, 0, 0, false}; }
+
+// How the units are shared out: pieces of items, of at most `share` units, or (by_runs) an
+// equal run of units for every workgroup, which may end one item's and begin another's.
+struct Shares {
+  int share;
+  bool by_runs;
+  int total;  // units, by runs
+};
+
+// Items are taken whole where nothing may be cut, and where there are enough of about the same
+// length: the longest times the rounds of them is at most 1.3 times the mean load.  (Two
+// prompts of 1000 queries behind 16384 tokens, 456 items for 512 places: cutting them made 60 MB
+// of pieces and 12% shorter runs.)  Short shares keep to one item, since a second one costs
+// a second start: 48 sequences of up to 8192 tokens, 3 units each, 27.5 us by runs and 25.7
+// by pieces.  Long ones are better equal: 16 sequences of up to 131072, 105 units, 341 and 379.
+constexpr int kRunUnits = 12;
 template <int NC>
-__device__ __forceinline__ Place find(const KvAttnArgs& a, PlanLds& l, const Chunk& first, bool whole, int u) {
-  int base = 0;
+__device__ __forceinline__ Shares shares_of(const KvAttnArgs& a, PlanLds& l, const Seq& first) {
+  Shares r = {INT32_MAX, false, 0};
+  if (a.runs == 0) return r;
+  int units = 0, items = 0, most = 0;
   for (int c = 0; c < a.B; c += kThreads) {
-    const Chunk k = c == 0 ? first : chunk_of<NC>(a, l, c);
-    const int own = whole ? k.own.items : k.own.units, before = base + (whole ? k.items : k.units);
-    if (u >= before && u - before < own) {
-      l.b = c + (int)threadIdx.x;
-      l.base = before;
-      l.per_head = own / a.kv;
-      l.s = k.s;
+    const Load o = load_of<NC>(a, c == 0 ? first : seq_or_none(a, c + (int)threadIdx.x), INT32_MAX);
+    units += a.kv * o.units;
+    items += a.kv * o.items;
+    most = most > o.most ? most : o.most;
+  }
+  units = __builtin_amdgcn_readlane(wave_scan(units), 63);
+  items = __builtin_amdgcn_readlane(wave_scan(items), 63);
+  most = wave_max_int(most);
+  if (!few(a)) {
+    if ((threadIdx.x & 63) == 0) {
+      const int wave = threadIdx.x >> 6;
+      l.sums[0][wave] = units;
+      l.sums[1][wave] = items;
+      l.sums[2][wave] = most;
     }
-    base += whole ? k.all_items : k.all_units;
-    if (base > u) break;
+    __syncthreads();
+    units = items = most = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      units += l.sums[0][w];
+      items += l.sums[1][w];
+      most = most > l.sums[2][w] ? most : l.sums[2][w];
+    }
+    units = uniform(units);
+    items = uniform(items);
+    most = uniform(most);
+    __syncthreads();
   }
-  __syncthreads();
-  Place p;
-  p.b = uniform(l.b);
-  p.s.start = uniform(l.s.start);
-  p.s.count = uniform(l.s.count);
-  p.s.len = uniform(l.s.len);
-  p.s.bad = uniform(l.s.bad);
-  const int per_head = uniform(l.per_head), at = u - uniform(l.base);
+  if ((float)most * (float)((items + a.runs - 1) / a.runs) * (float)a.runs <= 1.3f * (float)units) return r;
+  r.share = units > a.runs ? (units - 1) / a.runs + 1 : 1;
+  r.by_runs = r.share >= kRunUnits;
+  r.total = units;
+  return r;
+}
+
+// Piece number w of all, with `share` units at most, for the whole workgroup; false if there
+// are not so many.  `total`: pieces of items that have several (for w = 0, or few sequences).
+template <int NC>
+__device__ __forceinline__ bool find(const KvAttnArgs& a, PlanLds& l, const Seq& first, int share, int w, Place& p, int& total) {
+  int pieces, cut, per_head, cut_per_head;
+  total = 0;
+  if (few(a)) {
+    const Load o = load_of<NC>(a, first, share);
+    const int own = a.kv * o.pieces, many = a.kv * o.cut, upto = wave_scan(own), many_upto = wave_scan(many);
+    total = __builtin_amdgcn_readlane(many_upto, 63);
+    if (w >= __builtin_amdgcn_readlane(upto, 63)) return false;
+    const int b = __builtin_ctzll(__ballot(w < upto));
+    p.b = b;
+    p.s.start = __builtin_amdgcn_readlane(first.start, b);
+    p.s.count = __builtin_amdgcn_readlane(first.count, b);
+    p.s.len = __builtin_amdgcn_readlane(first.len, b);
+    p.s.bad = __builtin_amdgcn_readlane(first.bad, b);
+    pieces = __builtin_amdgcn_readlane(upto - own, b);
+    cut = __builtin_amdgcn_readlane(many_upto - many, b);
+    per_head = __builtin_amdgcn_readlane(o.pieces, b);
+    cut_per_head = __builtin_amdgcn_readlane(o.cut, b);
+  } else {
+    int base = 0;
+    bool found = false;
+    for (int c = 0; c < a.B; c += kThreads) {
+      const int b = c + (int)threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      const Seq s = c == 0 ? first : seq_or_none(a, b);
+      const Load o = load_of<NC>(a, s, share);
+      const int own = a.kv * o.pieces, many = a.kv * o.cut;
+      const int upto = wave_scan(own), many_upto = wave_scan(many);
+      __syncthreads();
+      if (lane == 63) {
+        l.sums[0][wave] = upto;
+        l.sums[1][wave] = many_upto;
+      }
+      __syncthreads();
+      int before = base + upto - own, many_before = total + many_upto - many;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < wave) {
+          before += l.sums[0][i];
+          many_before += l.sums[1][i];
+        }
+        base += l.sums[0][i];
+        total += l.sums[1][i];
+      }
+      if (w >= before && w - before < own) {
+        l.b = b;
+        l.pieces = before;
+        l.cut = many_before;
+        l.per_head = o.pieces;
+        l.cut_per_head = o.cut;
+        l.s = s;
+      }
+      found = w < base;
+      // The first workgroup counts them all.
+      if (found && w != 0) break;
+    }
+    total = uniform(total);
+    if (!uniform(found)) return false;
+    __syncthreads();
+    p.b = uniform(l.b);
+    p.s.start = uniform(l.s.start);
+    p.s.count = uniform(l.s.count);
+    p.s.len = uniform(l.s.len);
+    p.s.bad = uniform(l.s.bad);
+    pieces = uniform(l.pieces);
+    cut = uniform(l.cut);
+    per_head = uniform(l.per_head);
+    cut_per_head = uniform(l.cut_per_head);
+  }
+  const int at = w - pieces;
   p.h = at / per_head;
-  p.off = at - p.h * per_head;
-  p.t = 0;
-  if (whole) {
-    p.t = p.off;
-    p.off = 0;
-    return p;
+  p.index = at - p.h * per_head;
+  p.slot = cut + p.h * cut_per_head;
+  for (p.t = 0;; ++p.t) {
+    p.units = units_of<NC>(a, p.s, p.t);
+    p.pieces = (p.units - 1) / share + 1;
+    if (p.index < p.pieces) break;
+    p.index -= p.pieces;
+    p.slot += p.pieces > 1 ? p.pieces : 0;
   }
-  for (;;) {
-    const int nu = units_of<NC>(a, p.s, p.t);
-    if (p.off < nu) break;
-    p.off -= nu;
-    ++p.t;
+  p.slot += p.index;
+  // Pieces of about the same size.
+  const int each = p.pieces > 1 ? (p.units - 1) / p.pieces + 1 : p.units;
+  p.off = p.index * each;
+  p.take = p.units - p.off < each ? p.units - p.off : each;
+  return true;
+}
+
+// The item behind p's.
+template <int NC>
+__device__ __forceinline__ void next_item(const KvAttnArgs& a, Place& p) {
+  if (++p.t == items_of<NC>(a, p.s)) {
+    p.t = 0;
+    if (++p.h == a.kv) {
+      p.h = 0;
+      do {
+        p.s = seq_of(a, ++p.b);
+      } while (p.s.count == 0);
+    }
   }
-  return p;
+  p.units = units_of<NC>(a, p.s, p.t);
+  p.off = 0;
 }
 
 // ------------------------------------------------------------ one step's data
@@ -263,9 +323,9 @@ template <int FMT, int D>
 struct Raw {
   static constexpr int kK = D / 32;                       // dwords of K per lane and half
   static constexpr int kV = D / 16 > 8 ? D / 128 : 1;     // dwords of V per lane and token
-  static constexpr int kKS = FMT == kINT ? D / 16 : 1;    // dwords of K's scales per lane and half
+  static constexpr int kKS = FMT == kINT ? D / 16 : 1;    // dwords of K's scales that a lane goes by
   uint32_t kc[2][kK];
-  uint32_t ks[2][kKS];
+  uint32_t ks[2];  // INT4: lane n has dword n % kKS, and hands it to its 16 lanes when it is wanted
   uint32_t vc[8][kV];
   uint32_t vs[8];
 };
@@ -292,7 +352,7 @@ __device__ __forceinline__ Offsets<FMT, D> offsets() {
   Offsets<FMT, D> o;
   if (FMT == kINT) {
     o.k = n * kRow + (D == 64 ? 4 : 16) * q;
-    o.ks = 4 * q * kScaleRow;
+    o.ks = 4 * q * kScaleRow + 4 * (n % Raw<FMT, D>::kKS);
   } else {
     o.k = n * kRow + q * (D / 8);
     o.ks = n * kScaleRow + (FMT == kMX ? q * D / 128 : q * (D / 64));
@@ -327,18 +387,13 @@ __device__ __forceinline__ void load_half(Raw<FMT, D>& w, int u, const uint8_t* 
     }
   }
   if constexpr (FMT == kINT) {
-#pragma unroll
-    for (int i = 0; i < Raw<FMT, D>::kKS / 4; ++i) {
-      const u32x4 v = load_unaligned<u32x4>(ks + o.ks + 16 * i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w.ks[u][4 * i + k] = v[k];
-    }
+    w.ks[u] = load_unaligned<uint32_t>(ks + o.ks);
   } else if constexpr (FMT == kMX) {
-    w.ks[u][0] = D == 256 ? load_unaligned<uint16_t>(ks + o.ks) : ks[o.ks];
+    w.ks[u] = D == 256 ? load_unaligned<uint16_t>(ks + o.ks) : ks[o.ks];
   } else {
-    w.ks[u][0] = D == 256   ? load_unaligned<uint32_t>(ks + o.ks)
-                 : D == 128 ? load_unaligned<uint16_t>(ks + o.ks)
-                            : ks[o.ks];
+    w.ks[u] = D == 256   ? load_unaligned<uint32_t>(ks + o.ks)
+              : D == 128 ? load_unaligned<uint16_t>(ks + o.ks)
+                         : ks[o.ks];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -359,13 +414,32 @@ __device__ __forceinline__ void load_half(Raw<FMT, D>& w, int u, const uint8_t* 
 
 __device__ __forceinline__ float half_value(uint32_t b) { return __half2float(__ushort_as_half((uint16_t)b)); }
 
+// f(0) .. f(N - 1) with the numbers as constants.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// INT4: scales of group J of the lane quarter's four tokens, out of its lanes' dwords.
+template <int KJ, int J>
+__device__ __forceinline__ void k_scales(uint32_t ks, float (&sc)[4]) {
+  each<4>([&](auto r) {
+    constexpr int e = r * KJ + J;
+    sc[r] = half_value(dpp<0x150 + e / 2, 0xf>(0, ks) >> (16 * (e % 2)));  // row_newbcast
+  });
+}
+
 // Scale of K's dword j of half u, applied to the elements (not INT4).
 template <int FMT, int D>
 __device__ __forceinline__ float k_scale(const Raw<FMT, D>& w, int u, int j) {
   if constexpr (FMT == kMX) {
-    return __uint_as_float(((w.ks[u][0] >> (8 * (j / 4))) & 0xFFu) << 23);
+    return __uint_as_float(((w.ks[u] >> (8 * (j / 4))) & 0xFFu) << 23);
   } else {
-    const uint32_t v = w.ks[u][0];
+    const uint32_t v = w.ks[u];
     const int i = j / 2;  // two dwords share a group of 16
     return i == 0   ? __builtin_amdgcn_cvt_f32_fp8(v, 0)
            : i == 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 1)
@@ -459,10 +533,11 @@ __device__ __forceinline__ void wave_fence() {
 template <int D>
 constexpr int kQLine = D + 8;  // of a query in LDS, elements
 
-// Whether the columns' operands stay in LDS (transformed ones in two planes, or long
-// ones) rather than in registers, and the elements that a tile of them takes there.
-template <int D, int PLANES>
-constexpr bool kStaged = PLANES == 2 || D == 256;
+// Whether the columns' operands stay in LDS (transformed ones in two planes, or long ones, or
+// two tiles beside INT4's scales) rather than in registers, and the elements that a tile of
+// them takes there.
+template <int FMT, int D, int SHAPE, int PLANES>
+constexpr bool kStaged = PLANES == 2 || D == 256 || (FMT == kINT && SHAPE != kKvNarrow);
 template <int D, int PLANES>
 constexpr int kQTile = PLANES * 16 * kQLine<D>;
 
@@ -496,14 +571,14 @@ __device__ __forceinline__ void transform_q(const uint16_t* q, const uint16_t* T
 // D = 256), and in front of them the staged columns.
 template <int D>
 constexpr int kParts = D == 256 ? 2 : 1;
-template <int D, int SHAPE, int PLANES>
+template <int FMT, int D, int SHAPE, int PLANES>
 constexpr int q_floats() {
   constexpr int tiles = kv_tiles(SHAPE, D) * (SHAPE == kKvPrompt ? 4 : 1);
-  return kStaged<D, PLANES> ? tiles * kQTile<D, PLANES> / 2 : 0;
+  return kStaged<FMT, D, SHAPE, PLANES> ? tiles * kQTile<D, PLANES> / 2 : 0;
 }
-template <int D, int SHAPE, int PLANES>
+template <int FMT, int D, int SHAPE, int PLANES>
 constexpr int lds_floats() {
-  return q_floats<D, SHAPE, PLANES>() + (SHAPE == kKvPrompt ? 0 : 4 * kCh<D> / kParts<D> * 4 * 64);
+  return q_floats<FMT, D, SHAPE, PLANES>() + (SHAPE == kKvPrompt ? 0 : 4 * kCh<D> / kParts<D> * 4 * 64);
 }
 
 struct Piece {
@@ -517,7 +592,7 @@ struct Piece {
 template <int FMT, int D, int SHAPE, int PLANES>
 __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, float* lds, float (&stat)[2][4][32]) {
   constexpr int NQ = kv_tiles(SHAPE, D), KJ = D / 32, CH = kCh<D>, NC = kv_columns(SHAPE, D);
-  constexpr bool kInLds = kStaged<D, PLANES>;
+  constexpr bool kInLds = kStaged<FMT, D, SHAPE, PLANES>;
   constexpr bool kAlone = SHAPE == kKvPrompt;  // waves have columns of their own
   using RawT = Raw<FMT, D>;
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
@@ -537,6 +612,41 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
   const int first = lo / kTile + (kAlone ? 0 : wave), step = kAlone ? 1 : 4;
   const int last = (hi + kTile - 1) / kTile;
   const int steps = hi > lo && last > first ? (last - first + step - 1) / step : 0;
+
+  const auto o = offsets<FMT, D>();
+  const int mask = (1 << a.page_log2) - 1;
+  const int top = (hi - 1) & ~15, bottom = lo & ~15;  // halves that hold tokens
+  // First token of half u of step k, or of the nearest half that holds tokens.
+  auto half_at = [&](int k, int u) {
+    const int t = (first + k * step) * kTile + 16 * u;
+    return t > top ? top : t < bottom ? bottom : t;
+  };
+  int pages = 0;  // lane l: page of half l % 2 of step 32 i + l / 2
+  bool bad = p.s.bad;
+  auto read_pages = [&](int k) {
+    const int at = half_at(k + (lane >> 1), lane & 1);
+    int v = a.table[p.b * a.ldt + (at >> a.page_log2)];
+    if (v < 0 || v >= a.pages) {
+      bad = true;
+      v = 0;
+    }
+    pages = v;
+  };
+  auto load = [&](RawT& w, int k) {
+    if ((k & 31) == 0) read_pages(k);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int page = __builtin_amdgcn_readlane(pages, 2 * (k & 31) + u);
+      const int64_t row = (((int64_t)page * a.kv + p.h) << a.page_log2) + (half_at(k, u) & mask);
+      constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
+      load_half<FMT, D>(w, u, a.k_codes + row * (D / 2), a.k_scales + row * kScaleRow, a.v_codes + row * (D / 2),
+                        a.v_scales + row * kScaleRow, o);
+    }
+  };
+
+  // The first step is asked for before the queries are looked at.
+  RawT w0, w1;
+  if (steps > 0) load(w0, 0);
 
   // Columns: query rows, their places, operands.
   int pos[NQ];
@@ -609,37 +719,6 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
     for (int j = 0; j < CH; ++j) acc[j][ct] = f32x4{0, 0, 0, 0};
   }
 
-  const auto o = offsets<FMT, D>();
-  const int mask = (1 << a.page_log2) - 1;
-  const int top = (hi - 1) & ~15, bottom = lo & ~15;  // halves that hold tokens
-  // First token of half u of step k, or of the nearest half that holds tokens.
-  auto half_at = [&](int k, int u) {
-    const int t = (first + k * step) * kTile + 16 * u;
-    return t > top ? top : t < bottom ? bottom : t;
-  };
-  int pages = 0;  // lane l: page of half l % 2 of step 32 i + l / 2
-  bool bad = p.s.bad;
-  auto read_pages = [&](int k) {
-    const int at = half_at(k + (lane >> 1), lane & 1);
-    int v = a.table[p.b * a.ldt + (at >> a.page_log2)];
-    if (v < 0 || v >= a.pages) {
-      bad = true;
-      v = 0;
-    }
-    pages = v;
-  };
-  auto load = [&](RawT& w, int k) {
-    if ((k & 31) == 0) read_pages(k);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int page = __builtin_amdgcn_readlane(pages, 2 * (k & 31) + u);
-      const int64_t row = (((int64_t)page * a.kv + p.h) << a.page_log2) + (half_at(k, u) & mask);
-      constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
-      load_half<FMT, D>(w, u, a.k_codes + row * (D / 2), a.k_scales + row * kScaleRow, a.v_codes + row * (D / 2),
-                        a.v_scales + row * kScaleRow, o);
-    }
-  };
-
   auto compute = [&](RawT& w, int k) {
     const int t0 = (first + k * step) * kTile;
     const bool clear = t0 >= clear_from && t0 + kTile <= clear_to;
@@ -658,8 +737,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
+    each<KJ>([&](auto jc) {
+      constexpr int j = jc;
       bf16x8 qf[NQ][PLANES];
 #pragma unroll
       for (int ct = 0; ct < NQ; ++ct)
@@ -670,11 +749,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
         if constexpr (FMT == kINT) {
           const bf16x8 kf = expand<FMT>(w.kc[u][j], 0.0f);
           float sc[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int e = r * KJ + j;  // of the lane's four tokens' scales
-            sc[r] = half_value(w.ks[u][e / 2] >> (16 * (e % 2)));
-          }
+          k_scales<KJ, j>(w.ks[u], sc);
 #pragma unroll
           for (int ct = 0; ct < NQ; ++ct) {
             f32x4 g = {qs[ct][j], qs[ct][j], qs[ct][j], qs[ct][j]};
@@ -694,9 +769,14 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       }
       // Expanding more than one dword ahead costs registers, and with them waves.
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
     if (!clear) {
-      asm volatile("");  // a branch, not selects on every step
+      // (The scores pass through an empty statement, so that this stays behind the
+      // branch: as selects it would be a third of every step's instructions.)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int ct = 0; ct < NQ; ++ct) asm volatile("" : "+v"(s[u][ct]));
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -776,8 +856,6 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
 
   if (steps > 0) {
     // Two register sets in turn; a load past the last step repeats a place in range.
-    RawT w0, w1;
-    load(w0, 0);
     for (int k = 0; k < steps; k += 2) {
       load(w1, k + 1);
       compute(w0, k);
@@ -847,7 +925,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       constexpr int kQuads = CH / kParts<D>;  // quads of channels per lane: CH in all
 #pragma unroll
       for (int part = 0; part < kParts<D>; ++part) {
-        f32x4* red = reinterpret_cast<f32x4*>(lds + q_floats<D, SHAPE, PLANES>());
+        f32x4* red = reinterpret_cast<f32x4*>(lds + q_floats<FMT, D, SHAPE, PLANES>());
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
           const int e = part * kQuads + i, r = e / (CH / 4), j = e % (CH / 4) * 4;
@@ -879,73 +957,95 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
 }
 
 template <int FMT, int D, int SHAPE, int PLANES>
-__global__ __launch_bounds__(kThreads, 2) void kv4_attention_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D) / 256) void kv4_attention_kernel(KvAttnArgs a) {
   constexpr int NC = kv_columns(SHAPE, D);
   extern __shared__ __attribute__((aligned(16))) float lds[];
   __shared__ float stat[2][4][32];
   __shared__ PlanLds plan;
   const int w = blockIdx.x;
-  Chunk chunk;
-  const Shares s = shares_of<NC>(a, plan, chunk);
-  const int64_t begin = (int64_t)w * s.share;
-  KvJoin join = {};
-  if (begin < s.total) {
-    const int end = (int)(begin + s.share < s.total ? begin + s.share : s.total);
-    Place at = find<NC>(a, plan, chunk, s.whole, (int)begin);
-    for (int u = (int)begin; u < end;) {
-      const int nu = units_of<NC>(a, at.s, at.t);
-      const int take = s.whole || nu - at.off < end - u ? nu - at.off : end - u;
-      Piece p;
-      p.b = at.b;
-      p.h = at.h;
-      p.t = at.t;
-      p.s = at.s;
-      p.whole = take == nu;
-      p.part = a.part + ((int64_t)w * 2 + (u == (int)begin ? 0 : 1)) * (NC * (D + 2));
-      const int i0 = at.t * NC / a.group, il = (at.t * NC + NC - 1) / a.group;
-      const Span all = span_of(a, at.s, i0, il < at.s.count ? il : at.s.count - 1);
-      const int64_t from = (int64_t)(all.lo / kKvUnit + at.off) * kKvUnit, to = from + (int64_t)take * kKvUnit;
-      p.lo = all.lo > from ? all.lo : (int)from;
-      p.hi = all.hi < to ? all.hi : (int)to;
-      attend<FMT, D, SHAPE, PLANES>(a, p, lds, stat);
-      if (at.off == 0 && take < nu) {
-        const int cols = at.s.count * a.group - at.t * NC;
-        join = KvJoin{(u + nu - 1) / s.share - w + 1, u == (int)begin ? 0 : 1, cols < NC ? cols : NC, at.t * NC, at.s.start, at.h, {0, 0}};
-      }
-      u += s.whole ? 1 : take;
-      if (u >= end) break;
-      at.off = 0;
-      if (++at.t == items_of<NC>(a, at.s)) {
-        at.t = 0;
-        if (++at.h == a.kv) {
-          at.h = 0;
-          do {
-            at.s = seq_of(a, ++at.b);
-          } while (at.s.count == 0);
-        }
-      }
-      __syncthreads();  // LDS changes its use
+  const Seq first = seq_or_none(a, place_of(a));
+  const Shares s = shares_of<NC>(a, plan, first);
+  Place at;
+  int cut, left = 0;  // units left of the run
+  if (s.by_runs) {
+    if (w >= a.runs) return;
+    const int64_t begin = (int64_t)w * s.share;
+    left = (int)(begin >= s.total ? 0 : s.total - begin < s.share ? s.total - begin : s.share);
+    if (threadIdx.x == 0) {
+      if (w == 0) a.join[0].pieces = 2 * a.runs;
+      a.join[1 + 2 * w].pieces = a.join[2 + 2 * w].pieces = 0;
     }
+    // A unit is a piece of one.
+    if (left == 0 || !find<NC>(a, plan, first, 1, (int)begin, at, cut)) return;
+    at.slot = 2 * w;
+  } else {
+    const bool any = find<NC>(a, plan, first, s.share, w, at, cut);
+    if (w == 0 && threadIdx.x == 0 && a.runs > 0) a.join[0].pieces = cut;
+    if (!any) return;
   }
-  if (w < a.runs && threadIdx.x == 0) a.join[w] = join;
+  for (;;) {
+    KvJoin join = {at.index == 0 ? at.pieces : 0, at.slot + 1, 1, 0, 0, at.s.start, at.h, 0};
+    if (s.by_runs) {
+      at.take = at.units - at.off < left ? at.units - at.off : left;
+      left -= at.take;
+      // The rest of the item is at the beginnings of the runs behind.
+      const int rest = at.units - at.off - at.take;
+      join = KvJoin{at.off == 0 && rest > 0 ? (rest - 1) / s.share + 2 : 0, 2 * w + 2, 2, 0, 0, at.s.start, at.h, 0};
+    }
+    const int i0 = at.t * NC / a.group, il = (at.t * NC + NC - 1) / a.group, cols = at.s.count * a.group - at.t * NC;
+    join.cols = cols < NC ? cols : NC;
+    join.col0 = at.t * NC;
+    const Span all = span_of(a, at.s, i0, il < at.s.count ? il : at.s.count - 1);
+    const int64_t from = (int64_t)(all.lo / kKvUnit + at.off) * kKvUnit, to = from + (int64_t)at.take * kKvUnit;
+    Piece p;
+    p.b = at.b;
+    p.h = at.h;
+    p.t = at.t;
+    p.s = at.s;
+    p.lo = all.lo > from ? all.lo : (int)from;
+    p.hi = all.hi < to ? all.hi : (int)to;
+    p.whole = at.take == at.units;
+    p.part = p.whole ? nullptr : a.part + (int64_t)at.slot * (NC * (D + 2));
+    if (!p.whole && threadIdx.x == 0) a.join[1 + at.slot] = join;
+    // (Kept here rather than in registers.)
+    if (threadIdx.x == 0) {
+      plan.at = at;
+      plan.left = left;
+    }
+    attend<FMT, D, SHAPE, PLANES>(a, p, lds, stat);
+    __syncthreads();
+    left = uniform(plan.left);
+    if (left == 0) return;
+    at.b = uniform(plan.at.b);
+    at.h = uniform(plan.at.h);
+    at.t = uniform(plan.at.t);
+    at.s.start = uniform(plan.at.s.start);
+    at.s.count = uniform(plan.at.s.count);
+    at.s.len = uniform(plan.at.s.len);
+    at.s.bad = uniform(plan.at.s.bad);
+    next_item<NC>(a, at);
+    // Only a run's last item can go on behind it.
+    at.slot = 2 * w + 1;
+    __syncthreads();  // LDS changes its use
+  }
 }
 
-// The pieces of the item that begins in run blockIdx.x and goes on behind its end, if there is
-// one.  A workgroup takes a column at a time; lanes take four channels each, so that it
-// reads 1024 / D pieces at once.
+// The pieces of the item whose first one is in place blockIdx.x, if that is one.  A workgroup
+// takes a column at a time; lanes take four channels each, so that it reads 1024 / D pieces
+// at once.
 template <int D, int SHAPE>
 __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv) {
   constexpr int NC = kv_columns(SHAPE, D), kLanes = D / 4, kAtOnce = kThreads / kLanes;
   __shared__ float wave_m[4], wave_l[kAtOnce];
   __shared__ __attribute__((aligned(16))) float sums[kAtOnce][D];
-  const KvJoin j = a.join[blockIdx.x];
+  if ((int)blockIdx.x >= a.join[0].pieces) return;
+  const KvJoin j = a.join[1 + blockIdx.x];
   if (j.pieces == 0) return;
   const int tid = threadIdx.x, mine = tid / kLanes, ch = tid % kLanes * 4;
   constexpr int64_t kPiece = NC * (D + 2);
   const float vg = nv ? a.v_gs[0] : 1.0f;
-  // Piece i: the run's second place perhaps, then every run's first.
-  const float* base = a.part + (int64_t)blockIdx.x * 2 * kPiece;
-  auto piece = [&](int i) { return base + ((int64_t)i * 2 + (i == 0 ? j.second : 0)) * kPiece; };
+  const float* base = a.part + (int64_t)blockIdx.x * kPiece;
+  auto piece = [&](int i) { return i == 0 ? base : a.part + ((int64_t)j.next + (int64_t)(i - 1) * j.step) * kPiece; };
   for (int c = blockIdx.y; c < j.cols; c += gridDim.y) {
     float M = -FLT_MAX;
     for (int i = tid; i < j.pieces; i += kThreads) M = fmaxf(M, piece(i)[c]);
@@ -985,9 +1085,9 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv
 template <int FMT, int D, int SHAPE, int PLANES>
 hipError_t go(const KvAttnArgs& a, hipStream_t s) {
   hipError_t e = launch_lds(kv4_attention_kernel<FMT, D, SHAPE, PLANES>, dim3(a.workgroups), kThreads,
-                            4 * lds_floats<D, SHAPE, PLANES>(), s, a);
+                            4 * lds_floats<FMT, D, SHAPE, PLANES>(), s, a);
   if (e != hipSuccess || a.runs == 0) return e;
-  hipLaunchKernelGGL((kv4_join_kernel<D, SHAPE>), dim3(a.runs, kv_columns(SHAPE, D) / 4), dim3(kThreads), 0, s, a,
+  hipLaunchKernelGGL((kv4_join_kernel<D, SHAPE>), dim3(2 * a.runs, kv_columns(SHAPE, D) / 4), dim3(kThreads), 0, s, a,
                      FMT == kNV ? 1 : 0);
   return hipGetLastError();
 }

@@ -162,7 +162,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   if (!aligned(out, 16)) return fail(WUSH_EALIGN, "out must be 16-byte aligned");
   const wush::KvPlan plan = wush::kv_plan(B, n, heads, q_heads / heads, (int)D, page * width);
   // Items and units are counted in 32 bits.
-  if (plan.items > INT32_MAX / (page * width / wush::kKvUnit + 2))
+  if (plan.items > INT32_MAX / 2 / (page * width / wush::kKvUnit + 2))
     return fail(WUSH_EINVAL, "too many tokens for one launch");
   const int64_t need = wush_kv4_attention_workspace(B, n, q_heads, heads, D, page, width);
   st = check_workspace(workspace, workspace_bytes, need);
@@ -202,7 +202,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.T = static_cast<const uint16_t*>(T_q);
   a.out = static_cast<uint16_t*>(out);
   a.join = static_cast<wush::KvJoin*>(workspace);
-  a.part = reinterpret_cast<float*>(a.join + plan.runs);
+  a.part = plan.runs ? reinterpret_cast<float*>(a.join + 1 + 2 * (int64_t)plan.runs) : nullptr;
   a.B = (int)B;
   a.n = (int)n;
   a.kv = (int)heads;
@@ -213,7 +213,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.pages = (int)pages;
   a.window = (int)window;
   a.scale = (float)(scale * 1.4426950408889634);  // the kernels take powers of two
-  a.workgroups = plan.workgroups;
+  a.workgroups = (int)plan.workgroups;
   a.runs = plan.runs;
   if (fmt == wush::kMXFP4) return launched(wush::launch_kv4_attention_mx(a, plan.shape, stream));
   if (fmt == wush::kNVFP4) return launched(wush::launch_kv4_attention_nv(a, plan.shape, stream));
