@@ -365,10 +365,7 @@ __device__ __forceinline__ Offsets<FMT, D> offsets() {
 
 // Half u of a step: 16 tokens, in one page, whose first one's rows these are.
 template <int FMT, int D>
-__device__ __forceinline__ void load_half(Raw<FMT, D>& w, int u, const uint8_t* kc, const uint8_t* ks, const uint8_t* vc,
-                                          const uint8_t* vs, const Offsets<FMT, D>& o) {
-  constexpr int kRow = D / 2;
-  constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
+__device__ __forceinline__ void load_k(Raw<FMT, D>& w, int u, const uint8_t* kc, const uint8_t* ks, const Offsets<FMT, D>& o) {
   if constexpr (D == 64) {
     if constexpr (FMT == kINT) {
       w.kc[u][0] = load_unaligned<uint32_t>(kc + o.k);
@@ -395,6 +392,12 @@ __device__ __forceinline__ void load_half(Raw<FMT, D>& w, int u, const uint8_t* 
               : D == 128 ? load_unaligned<uint16_t>(ks + o.ks)
                          : ks[o.ks];
   }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_v(Raw<FMT, D>& w, int u, const uint8_t* vc, const uint8_t* vs, const Offsets<FMT, D>& o) {
+  constexpr int kRow = D / 2;
+  constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint8_t* p = vc + o.v + i * kRow;
@@ -523,6 +526,108 @@ __device__ __forceinline__ float column_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// INT4: the lane's codes of half u, regrouped so that dword j is group j's.
+template <int FMT, int D>
+__device__ __forceinline__ void arrange_k(Raw<FMT, D>& w, int u) {
+  if constexpr (FMT == kINT && D > 64) {
+#pragma unroll
+    for (int i = 0; i < D / 128; ++i) {
+      u32x4 c = {w.kc[u][4 * i], w.kc[u][4 * i + 1], w.kc[u][4 * i + 2], w.kc[u][4 * i + 3]};
+      transpose4(c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w.kc[u][4 * i + j] = c[j];
+    }
+  }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void v_scales(const Raw<FMT, D>& w, float (&vs)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    vs[i] = FMT == kMX   ? __uint_as_float(w.vs[i] << 23)
+            : FMT == kNV ? __builtin_amdgcn_cvt_f32_fp8(w.vs[i], 0)
+                         : half_value(w.vs[i]);
+}
+
+// Zeros for the step's tokens outside [lo, hi).
+template <int FMT, int D>
+__device__ __forceinline__ void clear_v(Raw<FMT, D>& w, int t0, int lo, int hi) {
+  const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int t = t0 + 16 * (e / 4) + 4 * q + e % 4;
+    if (t < lo || t >= hi) {
+#pragma unroll
+      for (int i = 0; i < Raw<FMT, D>::kV; ++i) w.vc[e][i] = 0;
+      w.vs[e] = 0;
+    }
+  }
+}
+
+// Scores of tokens that a column does not see become -inf.
+template <int NQ>
+__device__ __forceinline__ void mask_scores(f32x4 (&s)[2][NQ], int t0, int lo, const int (&pos)[NQ], int window) {
+  const int q = (threadIdx.x & 63) >> 4;
+  // (The scores pass through an empty statement, so that this stays behind its branch: as
+  // selects it would be a third of every step's instructions.)
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int ct = 0; ct < NQ; ++ct) asm volatile("" : "+v"(s[u][ct]));
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = t0 + 16 * u + 4 * q + r;
+#pragma unroll
+      for (int ct = 0; ct < NQ; ++ct) {
+        const bool seen = t >= lo && t <= pos[ct] && (!window || t > pos[ct] - window);
+        s[u][ct][r] = seen ? s[u][ct][r] : -__builtin_inff();
+      }
+    }
+}
+
+// Scores of 32 tokens to probabilities, up to the running maximum m, as B operands.
+template <int NQ, int CH>
+__device__ __forceinline__ void softmax_step(const f32x4 (&s)[2][NQ], float scale, float (&m)[NQ], float (&l)[NQ],
+                                             f32x4 (&acc)[CH][NQ], bf16x8 (&pf)[NQ]) {
+  // The running maximum moves where a score passes it by more than the slack.
+  float high[NQ];
+  bool grown = false;
+#pragma unroll
+  for (int ct = 0; ct < NQ; ++ct) {
+    float v = s[0][ct][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v = fmaxf(v, s[i >> 2][ct][i & 3]);
+    high[ct] = v * scale;
+    grown |= high[ct] > m[ct] + kSlack;
+  }
+  if (__any(grown)) {
+#pragma unroll
+    for (int ct = 0; ct < NQ; ++ct) {
+      const float next = fmaxf(m[ct], column_max(high[ct]));
+      const float f = __builtin_amdgcn_exp2f(m[ct] - next);
+      m[ct] = next;
+      l[ct] *= f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][ct][r] *= f;
+    }
+  }
+#pragma unroll
+  for (int ct = 0; ct < NQ; ++ct) {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][ct][i & 3], scale, -m[ct]));
+      l[ct] += e[i];
+    }
+    pf[ct] = __builtin_bit_cast(bf16x8, (u32x4{pack(cvt_bf16(e[0], e[1])), pack(cvt_bf16(e[2], e[3])),
+                                              pack(cvt_bf16(e[4], e[5])), pack(cvt_bf16(e[6], e[7]))}));
+  }
+}
+
 // Orders this wave's LDS accesses.
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -573,12 +678,7 @@ template <int D>
 constexpr int kParts = D == 256 ? 2 : 1;
 template <int FMT, int D, int SHAPE, int PLANES>
 constexpr int q_floats() {
-  constexpr int tiles = kv_tiles(SHAPE, D) * (SHAPE == kKvPrompt ? 4 : 1);
-  return kStaged<FMT, D, SHAPE, PLANES> ? tiles * kQTile<D, PLANES> / 2 : 0;
-}
-template <int FMT, int D, int SHAPE, int PLANES>
-constexpr int lds_floats() {
-  return q_floats<FMT, D, SHAPE, PLANES>() + (SHAPE == kKvPrompt ? 0 : 4 * kCh<D> / kParts<D> * 4 * 64);
+  return kStaged<FMT, D, SHAPE, PLANES> ? kv_tiles(SHAPE, D) * kQTile<D, PLANES> / 2 : 0;
 }
 
 struct Piece {
@@ -589,27 +689,27 @@ struct Piece {
   Seq s;
 };
 
+// Row of the result for a column of the piece's sequence.
+__device__ __forceinline__ uint16_t* out_row(const KvAttnArgs& a, const Piece& p, int col, int D) {
+  const int i = col / a.group;
+  return a.out + ((int64_t)(p.s.start + i) * a.kv * a.group + p.h * a.group + col - i * a.group) * D;
+}
+
 template <int FMT, int D, int SHAPE, int PLANES>
 __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, float* lds, float (&stat)[2][4][32]) {
   constexpr int NQ = kv_tiles(SHAPE, D), KJ = D / 32, CH = kCh<D>, NC = kv_columns(SHAPE, D);
   constexpr bool kInLds = kStaged<FMT, D, SHAPE, PLANES>;
-  constexpr bool kAlone = SHAPE == kKvPrompt;  // waves have columns of their own
   using RawT = Raw<FMT, D>;
   const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
   const int all = p.s.count * a.group;  // columns of the sequence
-  const int c0 = p.t * NC + (kAlone ? wave * 16 * NQ : 0);
+  const int c0 = p.t * NC;
   const int past = p.s.len - p.s.count;  // place of query 0
 
   // The wave's tokens and tiles of them.
-  int lo = p.lo, hi = p.hi;
+  const int lo = p.lo, hi = p.hi;
   const int i0 = c0 / a.group, end = (c0 + 16 * NQ - 1) / a.group, i1 = end < p.s.count ? end : p.s.count - 1;
-  if (kAlone) {
-    const Span w = c0 < all ? span_of(a, p.s, i0, i1) : Span{0, 0};
-    lo = lo > w.lo ? lo : w.lo;
-    hi = hi < w.hi ? hi : w.hi;
-  }
-  const int first = lo / kTile + (kAlone ? 0 : wave), step = kAlone ? 1 : 4;
+  const int first = lo / kTile + wave, step = 4;
   const int last = (hi + kTile - 1) / kTile;
   const int steps = hi > lo && last > first ? (last - first + step - 1) / step : 0;
 
@@ -639,8 +739,8 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       const int page = __builtin_amdgcn_readlane(pages, 2 * (k & 31) + u);
       const int64_t row = (((int64_t)page * a.kv + p.h) << a.page_log2) + (half_at(k, u) & mask);
       constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
-      load_half<FMT, D>(w, u, a.k_codes + row * (D / 2), a.k_scales + row * kScaleRow, a.v_codes + row * (D / 2),
-                        a.v_scales + row * kScaleRow, o);
+      load_k<FMT, D>(w, u, a.k_codes + row * (D / 2), a.k_scales + row * kScaleRow, o);
+      load_v<FMT, D>(w, u, a.v_codes + row * (D / 2), a.v_scales + row * kScaleRow, o);
     }
   };
 
@@ -651,7 +751,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
   // Columns: query rows, their places, operands.
   int pos[NQ];
   bf16x8 held[kInLds ? 1 : NQ][kInLds ? 1 : KJ];
-  uint16_t* staged = reinterpret_cast<uint16_t*>(lds) + (kAlone ? wave * NQ * kQTile<D, PLANES> : 0);
+  uint16_t* staged = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
     const int col = c0 + 16 * ct + n;
@@ -666,21 +766,15 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       // Columns that the waves share are staged by all of them.
       uint16_t* to = staged + ct * kQTile<D, PLANES>;
       if constexpr (PLANES == 2) {
-        for (int c = kAlone ? 0 : wave; c < D / 16; c += kAlone ? 1 : 4)
+        for (int c = wave; c < D / 16; c += 4)
           transform_q<FMT, D>(row, a.T + (int64_t)p.h * D * (FMT == kNV ? 16 : 32), to, c);
       } else {
-        for (int c = kAlone ? 0 : wave; c < D / 32; c += kAlone ? 1 : 4)
+        for (int c = wave; c < D / 32; c += 4)
           *reinterpret_cast<u32x4*>(to + n * kQLine<D> + 32 * c + 8 * q) = *reinterpret_cast<const u32x4*>(row + 32 * c + 8 * q);
       }
     }
   }
-  if constexpr (kInLds) {
-    if (kAlone) {
-      wave_fence();
-    } else {
-      __syncthreads();
-    }
-  }
+  if constexpr (kInLds) __syncthreads();
   auto column = [&](int ct, int t, int j) {
     if constexpr (kInLds) {
       return *reinterpret_cast<const bf16x8*>(staged + ct * kQTile<D, PLANES> + (16 * t + n) * kQLine<D> + channel<FMT, D>(j, q));
@@ -727,15 +821,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int ct = 0; ct < NQ; ++ct) s[u][ct] = f32x4{0, 0, 0, 0};
-      if constexpr (FMT == kINT && D > 64) {
-#pragma unroll
-        for (int i = 0; i < D / 128; ++i) {
-          u32x4 c = {w.kc[u][4 * i], w.kc[u][4 * i + 1], w.kc[u][4 * i + 2], w.kc[u][4 * i + 3]};
-          transpose4(c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w.kc[u][4 * i + j] = c[j];
-        }
-      }
+      arrange_k(w, u);
     }
     each<KJ>([&](auto jc) {
       constexpr int j = jc;
@@ -771,72 +857,14 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       __builtin_amdgcn_sched_barrier(0);
     });
     if (!clear) {
-      // (The scores pass through an empty statement, so that this stays behind the
-      // branch: as selects it would be a third of every step's instructions.)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int ct = 0; ct < NQ; ++ct) asm volatile("" : "+v"(s[u][ct]));
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = t0 + 16 * u + 4 * q + r;
-          // Places without a token may hold anything, also what 0 does not cancel.
-          if (t < lo || t >= hi) {
-#pragma unroll
-            for (int i = 0; i < RawT::kV; ++i) w.vc[4 * u + r][i] = 0;
-            w.vs[4 * u + r] = 0;
-          }
-#pragma unroll
-          for (int ct = 0; ct < NQ; ++ct) {
-            const bool seen = t >= lo && t <= pos[ct] && (!a.window || t > pos[ct] - a.window);
-            s[u][ct][r] = seen ? s[u][ct][r] : -__builtin_inff();
-          }
-        }
-    }
-    // The running maximum moves where a score passes it by more than the slack.
-    float high[NQ];
-    bool grown = false;
-#pragma unroll
-    for (int ct = 0; ct < NQ; ++ct) {
-      float v = s[0][ct][0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) v = fmaxf(v, s[i >> 2][ct][i & 3]);
-      high[ct] = v * scale;
-      grown |= high[ct] > m[ct] + kSlack;
-    }
-    if (__any(grown)) {
-#pragma unroll
-      for (int ct = 0; ct < NQ; ++ct) {
-        const float next = fmaxf(m[ct], column_max(high[ct]));
-        const float f = __builtin_amdgcn_exp2f(m[ct] - next);
-        m[ct] = next;
-        l[ct] *= f;
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[j][ct][r] *= f;
-      }
+      mask_scores<NQ>(s, t0, lo, pos, a.window);
+      // Places without a token may hold anything, also what 0 does not cancel.
+      clear_v(w, t0, lo, hi);
     }
     bf16x8 pf[NQ];
-#pragma unroll
-    for (int ct = 0; ct < NQ; ++ct) {
-      float e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][ct][i & 3], scale, -m[ct]));
-        l[ct] += e[i];
-      }
-      pf[ct] = __builtin_bit_cast(bf16x8, (u32x4{pack(cvt_bf16(e[0], e[1])), pack(cvt_bf16(e[2], e[3])),
-                                                pack(cvt_bf16(e[4], e[5])), pack(cvt_bf16(e[6], e[7]))}));
-    }
+    softmax_step<NQ, CH>(s, scale, m, l, acc, pf);
     float vs[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      vs[i] = FMT == kMX   ? __uint_as_float(w.vs[i] << 23)
-              : FMT == kNV ? __builtin_amdgcn_cvt_f32_fp8(w.vs[i], 0)
-                           : half_value(w.vs[i]);
+    v_scales(w, vs);
 #pragma unroll
     for (int i = 0; i < RawT::kV; ++i)
 #pragma unroll
@@ -870,87 +898,296 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
   }
 
   const float vg = FMT == kNV ? a.v_gs[0] : 1.0f;
-  auto out_row = [&](int col) {
-    const int i = col / a.group;
-    return a.out + ((int64_t)(p.s.start + i) * a.kv * a.group + p.h * a.group + col - i * a.group) * D;
-  };
-  if constexpr (kAlone) {
+  // The four waves' results of a column meet in LDS: factors first, then quads of
+  // channels, one per lane, without conflicts between banks.
 #pragma unroll
-    for (int ct = 0; ct < NQ; ++ct) {
-      const int col = c0 + 16 * ct + n, mine = col - p.t * NC;
-      if (col >= all) continue;
-      const float f = p.whole ? (l[ct] != 0.0f ? vg / l[ct] : 0.0f) : 1.0f;
-      if (!p.whole && q == 0) {
-        p.part[mine] = m[ct];
-        p.part[NC + mine] = l[ct];
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int ch = CH * (4 * q + r);
-#pragma unroll
-        for (int j = 0; j < CH; j += 4) {
-          const f32x4 v = {acc[j][ct][r] * f, acc[j + 1][ct][r] * f, acc[j + 2][ct][r] * f, acc[j + 3][ct][r] * f};
-          if (p.whole) {
-            *reinterpret_cast<u32x2*>(out_row(col) + ch + j) = u32x2{pack(cvt_bf16(v[0], v[1])), pack(cvt_bf16(v[2], v[3]))};
-          } else {
-            *reinterpret_cast<f32x4*>(p.part + 2 * NC + mine * D + ch + j) = v;
-          }
-        }
-      }
+  for (int ct = 0; ct < NQ; ++ct)
+    if (q == 0) {
+      stat[0][wave][16 * ct + n] = m[ct];
+      stat[1][wave][16 * ct + n] = l[ct];
     }
-  } else {
-    // The four waves' results of a column meet in LDS: factors first, then quads of
-    // channels, one per lane, without conflicts between banks.
+  __syncthreads();
 #pragma unroll
-    for (int ct = 0; ct < NQ; ++ct)
-      if (q == 0) {
-        stat[0][wave][16 * ct + n] = m[ct];
-        stat[1][wave][16 * ct + n] = l[ct];
+  for (int ct = 0; ct < NQ; ++ct) {
+    const int at = 16 * ct + n, col = c0 + at;
+    float M = stat[0][0][at], L = 0.0f;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) M = fmaxf(M, stat[0][w][at]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) L += stat[1][w][at] * __builtin_amdgcn_exp2f(stat[0][w][at] - M);
+    const float f = __builtin_amdgcn_exp2f(m[ct] - M);
+    const float g = p.whole ? (L != 0.0f ? vg / L : 0.0f) : 1.0f;
+    if (!p.whole && wave == 0 && q == 0 && col < all) {
+      p.part[at] = M;
+      p.part[NC + at] = L;
+    }
+    constexpr int kQuads = CH / kParts<D>;  // quads of channels per lane: CH in all
+#pragma unroll
+    for (int part = 0; part < kParts<D>; ++part) {
+      f32x4* red = reinterpret_cast<f32x4*>(lds + q_floats<FMT, D, SHAPE, PLANES>());
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const int e = part * kQuads + i, r = e / (CH / 4), j = e % (CH / 4) * 4;
+        red[(wave * kQuads + i) * 64 + lane] = f32x4{acc[j][ct][r], acc[j + 1][ct][r], acc[j + 2][ct][r], acc[j + 3][ct][r]} * f;
       }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll
-    for (int ct = 0; ct < NQ; ++ct) {
-      const int at = 16 * ct + n, col = c0 + at;
-      float M = stat[0][0][at], L = 0.0f;
+      for (int i0q = 0; i0q < kQuads; i0q += 4) {
+        const int i = i0q + wave;
+        if (i < kQuads) {
+          f32x4 v = red[i * 64 + lane];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) M = fmaxf(M, stat[0][w][at]);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) L += stat[1][w][at] * __builtin_amdgcn_exp2f(stat[0][w][at] - M);
-      const float f = __builtin_amdgcn_exp2f(m[ct] - M);
-      const float g = p.whole ? (L != 0.0f ? vg / L : 0.0f) : 1.0f;
-      if (!p.whole && wave == 0 && q == 0 && col < all) {
-        p.part[at] = M;
-        p.part[NC + at] = L;
-      }
-      constexpr int kQuads = CH / kParts<D>;  // quads of channels per lane: CH in all
-#pragma unroll
-      for (int part = 0; part < kParts<D>; ++part) {
-        f32x4* red = reinterpret_cast<f32x4*>(lds + q_floats<FMT, D, SHAPE, PLANES>());
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-          const int e = part * kQuads + i, r = e / (CH / 4), j = e % (CH / 4) * 4;
-          red[(wave * kQuads + i) * 64 + lane] = f32x4{acc[j][ct][r], acc[j + 1][ct][r], acc[j + 2][ct][r], acc[j + 3][ct][r]} * f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i0q = 0; i0q < kQuads; i0q += 4) {
-          const int i = i0q + wave;
-          if (i < kQuads) {
-            f32x4 v = red[i * 64 + lane];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) v += red[(w * kQuads + i) * 64 + lane];
-            const int e = part * kQuads + i, ch = CH * (4 * q + e / (CH / 4)) + e % (CH / 4) * 4;
-            if (col < all) {
-              if (p.whole) {
-                *reinterpret_cast<u32x2*>(out_row(col) + ch) =
-                    u32x2{pack(cvt_bf16(v[0] * g, v[1] * g)), pack(cvt_bf16(v[2] * g, v[3] * g))};
-              } else {
-                *reinterpret_cast<f32x4*>(p.part + 2 * NC + at * D + ch) = v;
-              }
+          for (int w = 1; w < 4; ++w) v += red[(w * kQuads + i) * 64 + lane];
+          const int e = part * kQuads + i, ch = CH * (4 * q + e / (CH / 4)) + e % (CH / 4) * 4;
+          if (col < all) {
+            if (p.whole) {
+              *reinterpret_cast<u32x2*>(out_row(a, p, col, D) + ch) =
+                  u32x2{pack(cvt_bf16(v[0] * g, v[1] * g)), pack(cvt_bf16(v[2] * g, v[3] * g))};
+            } else {
+              *reinterpret_cast<f32x4*>(p.part + 2 * NC + at * D + ch) = v;
             }
           }
         }
-        __syncthreads();
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The same for many columns: each of the four waves has 32 (16 for D = 256) of its own, and
+// they share what K and V become.  Per stage every wave expands 32 tokens (for D = 256 pairs
+// of waves K or V of them) into LDS, as the operands that all four then read; the next
+// stage's codes are on their way meanwhile.  (Each wave expanding for itself, in registers,
+// spends 136 of 263 instructions of a step on it: 640 us for two prompts of 1000 queries
+// behind 16384 tokens.)
+template <int FMT, int D>
+constexpr int kStageTiles = D == 256 ? 2 : 4;
+template <int FMT, int D>
+constexpr int kTileLds = (2 * (D / 32) + kCh<D>) * 512 + (FMT == kINT ? 256 : 0);  // elements of 32 tokens
+
+template <int FMT, int D, int SHAPE, int PLANES>
+constexpr int lds_floats() {
+  if (SHAPE != kKvPrompt) return q_floats<FMT, D, SHAPE, PLANES>() + 4 * kCh<D> / kParts<D> * 4 * 64;
+  constexpr int tiles = kStageTiles<FMT, D> * kTileLds<FMT, D> / 2, queries = PLANES == 2 ? 4 * kQTile<D, 2> / 2 : 0;
+  return (tiles > queries ? tiles : queries) + 4;
+}
+
+template <int FMT, int D, int PLANES>
+__device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& p, float* lds) {
+  constexpr int NQ = kv_tiles(kKvPrompt, D), KJ = D / 32, CH = kCh<D>, NC = kv_columns(kKvPrompt, D);
+  constexpr int NS = kStageTiles<FMT, D>, kLds = kTileLds<FMT, D>;
+  using RawT = Raw<FMT, D>;
+  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int all = p.s.count * a.group;  // columns of the sequence
+  const int c0 = p.t * NC + wave * 16 * NQ;
+  const int past = p.s.len - p.s.count;  // place of query 0
+  uint16_t* tiles = reinterpret_cast<uint16_t*>(lds);
+  int* any_bad = reinterpret_cast<int*>(lds + lds_floats<FMT, D, kKvPrompt, PLANES>() - 4);
+
+  // Tokens of the wave's columns, and of the stages.
+  const int i0 = c0 / a.group, end = (c0 + 16 * NQ - 1) / a.group, i1 = end < p.s.count ? end : p.s.count - 1;
+  const Span mine = c0 < all ? span_of(a, p.s, i0, i1) : Span{0, 0};
+  const int lo = p.lo > mine.lo ? p.lo : mine.lo, hi = p.hi < mine.hi ? p.hi : mine.hi;
+  const int first = p.lo / kTile, last = p.hi > p.lo ? (p.hi + kTile - 1) / kTile : first;
+  const int stages = (last - first + NS - 1) / NS;
+
+  // What this wave expands: tile `sub` of each stage.
+  const int sub = D == 256 ? wave >> 1 : wave;
+  const bool does_k = D < 256 || !(wave & 1), does_v = D < 256 || (wave & 1);
+  const auto o = offsets<FMT, D>();
+  const int mask = (1 << a.page_log2) - 1;
+  const int top = (p.hi - 1) & ~15, bottom = p.lo & ~15;  // halves that hold tokens
+  auto half_at = [&](int k, int u) {
+    const int t = (first + k * NS + sub) * kTile + 16 * u;
+    return t > top ? top : t < bottom ? bottom : t;
+  };
+  int pages = 0;  // lane l: page of half l % 2 of stage 32 i + l / 2
+  bool bad = p.s.bad;
+  RawT w;
+  auto load = [&](int k) {
+    if ((k & 31) == 0) {
+      int v = a.table[p.b * a.ldt + (half_at(k + (lane >> 1), lane & 1) >> a.page_log2)];
+      if (v < 0 || v >= a.pages) {
+        bad = true;
+        v = 0;
+      }
+      pages = v;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int page = __builtin_amdgcn_readlane(pages, 2 * (k & 31) + u);
+      const int64_t row = (((int64_t)page * a.kv + p.h) << a.page_log2) + (half_at(k, u) & mask);
+      constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
+      if (does_k) load_k<FMT, D>(w, u, a.k_codes + row * (D / 2), a.k_scales + row * kScaleRow, o);
+      if (does_v) load_v<FMT, D>(w, u, a.v_codes + row * (D / 2), a.v_scales + row * kScaleRow, o);
+    }
+  };
+  if (stages > 0) load(0);
+
+  // Columns: query rows, their places, operands.
+  int pos[NQ];
+  bf16x8 qf[NQ][PLANES][KJ];
+#pragma unroll
+  for (int ct = 0; ct < NQ; ++ct) {
+    const int col = c0 + 16 * ct + n;
+    const int used = col < all ? col : all - 1;
+    const int i = used / a.group;
+    pos[ct] = col < all ? past + i : -1;
+    const uint16_t* row = a.q + (int64_t)(p.s.start + i) * a.ldq + (int64_t)(p.h * a.group + used - i * a.group) * D;
+    if constexpr (PLANES == 1) {
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) qf[ct][0][j] = *reinterpret_cast<const bf16x8*>(row + channel<FMT, D>(j, q));
+    } else {
+      uint16_t* to = tiles + wave * kQTile<D, 2>;
+      wave_fence();
+      for (int c = 0; c < D / 16; ++c) transform_q<FMT, D>(row, a.T + (int64_t)p.h * D * (FMT == kNV ? 16 : 32), to, c);
+      wave_fence();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+          qf[ct][t][j] = *reinterpret_cast<const bf16x8*>(to + (16 * t + n) * kQLine<D> + channel<FMT, D>(j, q));
+    }
+  }
+  float qs[FMT == kINT ? NQ : 1][FMT == kINT ? KJ : 1];
+  if constexpr (FMT == kINT) {
+    // K enters as code + 8 (see attend).
+    const uint32_t m8 = 0xC100C100u;  // bf16 -8, twice
+    const bf16x8 minus8 = __builtin_bit_cast(bf16x8, (u32x4{m8, m8, m8, m8}));
+#pragma unroll
+    for (int ct = 0; ct < NQ; ++ct)
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < PLANES; ++t) v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(minus8, qf[ct][t][j], v, 0, 0, 0);
+        qs[ct][j] = v[0];
+      }
+  }
+  const int clear_to = past + i0 + 1, clear_from = a.window ? past + i1 - a.window + 1 : 0;
+  const float scale = FMT == kNV ? fmaxf(a.scale * a.k_gs[0], 1e-30f) : fmaxf(a.scale, 1e-30f);
+  f32x4 acc[CH][NQ];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int ct = 0; ct < NQ; ++ct) {
+    m[ct] = -FLT_MAX;
+    l[ct] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) acc[j][ct] = f32x4{0, 0, 0, 0};
+  }
+  if (threadIdx.x == 0) *any_bad = 0;
+  __syncthreads();  // the queries' LDS is free
+
+  // A tile's operands: K's 2 KJ (half u, instruction j), then V's CH, 1 KB each, lane by lane.
+  auto operand = [&](int tile, int i) { return reinterpret_cast<bf16x8*>(tiles + tile * kLds + i * 512 + lane * 8); };
+  auto k_scale_dword = [&](int tile, int u) {
+    return reinterpret_cast<uint32_t*>(tiles + tile * kLds + (2 * KJ + CH) * 512) + u * 64 + lane;
+  };
+  auto expand_tile = [&](int k) {
+    const int t0 = (first + k * NS + sub) * kTile;
+    if (does_k) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        arrange_k(w, u);
+#pragma unroll
+        for (int j = 0; j < KJ; ++j)
+          *operand(sub, u * KJ + j) = expand<FMT>(w.kc[u][j], FMT == kINT ? 0.0f : k_scale(w, u, j));
+        if constexpr (FMT == kINT) *k_scale_dword(sub, u) = w.ks[u];
+      }
+    }
+    if (does_v) {
+      if (t0 < p.lo || t0 + kTile > p.hi) clear_v(w, t0, p.lo, p.hi);
+      float vs[8];
+      v_scales(w, vs);
+#pragma unroll
+      for (int i = 0; i < RawT::kV; ++i)
+#pragma unroll
+        for (int b = 0; b < (CH < 8 ? CH / 2 : 4); ++b) {
+          u32x4 even, odd;
+          expand_v<FMT, D>(w, vs, i, b, even, odd);
+          *operand(sub, 2 * KJ + 8 * i + 2 * b) = __builtin_bit_cast(bf16x8, even);
+          *operand(sub, 2 * KJ + 8 * i + 2 * b + 1) = __builtin_bit_cast(bf16x8, odd);
+        }
+    }
+  };
+  auto compute = [&](int tile, int t0) {
+    f32x4 s[2][NQ];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int ct = 0; ct < NQ; ++ct) s[u][ct] = f32x4{0, 0, 0, 0};
+    each<KJ>([&](auto jc) {
+      constexpr int j = jc;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bf16x8 kf = *operand(tile, u * KJ + j);
+        if constexpr (FMT == kINT) {
+          float sc[4];
+          k_scales<KJ, j>(*k_scale_dword(tile, u), sc);
+#pragma unroll
+          for (int ct = 0; ct < NQ; ++ct) {
+            f32x4 g = {qs[ct][j], qs[ct][j], qs[ct][j], qs[ct][j]};
+#pragma unroll
+            for (int t = 0; t < PLANES; ++t) g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[ct][t][j], g, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[u][ct][r] = __builtin_fmaf(sc[r], g[r], s[u][ct][r]);
+          }
+        } else {
+#pragma unroll
+          for (int ct = 0; ct < NQ; ++ct)
+#pragma unroll
+            for (int t = 0; t < PLANES; ++t)
+              s[u][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[ct][t][j], s[u][ct], 0, 0, 0);
+        }
+      }
+    });
+    if (!(t0 >= clear_from && t0 + kTile <= clear_to)) mask_scores<NQ>(s, t0, lo, pos, a.window);
+    bf16x8 pf[NQ];
+    softmax_step<NQ, CH>(s, scale, m, l, acc, pf);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const bf16x8 vf = *operand(tile, 2 * KJ + j);
+#pragma unroll
+      for (int ct = 0; ct < NQ; ++ct) acc[j][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[ct], acc[j][ct], 0, 0, 0);
+    }
+  };
+  for (int k = 0; k < stages; ++k) {
+    expand_tile(k);
+    load(k + 1);  // (behind the last one: a place in range)
+    meet();
+    for (int i = 0; i < NS; ++i) {
+      const int t0 = (first + k * NS + i) * kTile;
+      if (t0 < hi && t0 + kTile > lo) compute(i, t0);
+    }
+    meet();
+  }
+  if (__any(bad) && lane == 0) *any_bad = 1;
+  __syncthreads();
+  const bool nan = *any_bad != 0;
+  const float vg = FMT == kNV ? a.v_gs[0] : 1.0f;
+#pragma unroll
+  for (int ct = 0; ct < NQ; ++ct) {
+    l[ct] = column_sum(l[ct]);
+    if (nan) l[ct] = __builtin_nanf("");
+    const int col = c0 + 16 * ct + n, at = col - p.t * NC;
+    if (col >= all) continue;
+    const float f = p.whole ? (l[ct] != 0.0f ? vg / l[ct] : 0.0f) : 1.0f;
+    if (!p.whole && q == 0) {
+      p.part[at] = m[ct];
+      p.part[NC + at] = l[ct];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int ch = CH * (4 * q + r);
+#pragma unroll
+      for (int j = 0; j < CH; j += 4) {
+        const f32x4 v = {acc[j][ct][r] * f, acc[j + 1][ct][r] * f, acc[j + 2][ct][r] * f, acc[j + 3][ct][r] * f};
+        if (p.whole) {
+          *reinterpret_cast<u32x2*>(out_row(a, p, col, D) + ch + j) = u32x2{pack(cvt_bf16(v[0], v[1])), pack(cvt_bf16(v[2], v[3]))};
+        } else {
+          *reinterpret_cast<f32x4*>(p.part + 2 * NC + at * D + ch + j) = v;
+        }
       }
     }
   }
@@ -1012,7 +1249,11 @@ __global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D) / 256) void kv4_att
       plan.at = at;
       plan.left = left;
     }
-    attend<FMT, D, SHAPE, PLANES>(a, p, lds, stat);
+    if constexpr (SHAPE == kKvPrompt) {
+      attend_prompt<FMT, D, PLANES>(a, p, lds);
+    } else {
+      attend<FMT, D, SHAPE, PLANES>(a, p, lds, stat);
+    }
     __syncthreads();
     left = uniform(plan.left);
     if (left == 0) return;
