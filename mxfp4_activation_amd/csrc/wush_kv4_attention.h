@@ -164,9 +164,9 @@ struct Shares {
 };
 
 // Items are taken whole where nothing may be cut, and where there are enough of about the same
-// length: the longest times the rounds of them is at most 1.3 times the mean load.  (Two
-// prompts of 1000 queries behind 16384 tokens, 456 items for 512 places: cutting them made 60 MB
-// of pieces and 12% shorter runs.)  Short shares keep to one item, since a second one costs
+// length: the longest times the rounds of them is at most 1.1 times the mean load.  (Two
+// prompts of 1000 queries behind 16384 tokens, 456 items for 512 places, 1.17 times: 533 us
+// whole, 497 by runs, 22 of them for joining 60 MB of pieces.)    Short shares keep to one item, since a second one costs
 // a second start: 48 sequences of up to 8192 tokens, 3 units each, 27.5 us by runs and 25.7
 // by pieces.  Long ones are better equal: 16 sequences of up to 131072, 105 units, 341 and 379.
 constexpr int kRunUnits = 12;
@@ -204,7 +204,7 @@ __device__ __forceinline__ Shares shares_of(const KvAttnArgs& a, PlanLds& l, con
     most = uniform(most);
     __syncthreads();
   }
-  if ((float)most * (float)((items + a.runs - 1) / a.runs) * (float)a.runs <= 1.3f * (float)units) return r;
+  if ((float)most * (float)((items + a.runs - 1) / a.runs) * (float)a.runs <= 1.1f * (float)units) return r;
   r.share = units > a.runs ? (units - 1) / a.runs + 1 : 1;
   r.by_runs = r.share >= kRunUnits;
   r.total = units;
@@ -1271,9 +1271,10 @@ __global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D) / 256) void kv4_att
   }
 }
 
-// The pieces of the item whose first one is in place blockIdx.x, if that is one.  A workgroup
-// takes a column at a time; lanes take four channels each, so that it reads 1024 / D pieces
-// at once.
+// The pieces of the item whose first one is in place blockIdx.x, if that is one.  D / 4 lanes
+// take a row's channels, so that a workgroup reads 1024 / D rows at once: columns where there
+// are few pieces, pieces of one column where there are many.
+constexpr int kFewPieces = 4;
 template <int D, int SHAPE>
 __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv) {
   constexpr int NC = kv_columns(SHAPE, D), kLanes = D / 4, kAtOnce = kThreads / kLanes;
@@ -1287,6 +1288,34 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv
   const float vg = nv ? a.v_gs[0] : 1.0f;
   const float* base = a.part + (int64_t)blockIdx.x * kPiece;
   auto piece = [&](int i) { return i == 0 ? base : a.part + ((int64_t)j.next + (int64_t)(i - 1) * j.step) * kPiece; };
+  auto out = [&](int c) {
+    const int col = j.col0 + c, i = col / a.group;
+    return a.out + ((int64_t)(j.start + i) * a.kv * a.group + j.head * a.group + col - i * a.group) * D;
+  };
+  if (j.pieces <= kFewPieces) {
+    for (int c = (int)blockIdx.y * kAtOnce + mine; c < j.cols; c += (int)gridDim.y * kAtOnce) {
+      float m[kFewPieces], l[kFewPieces], M = -FLT_MAX, L = 0.0f;
+      f32x4 x[kFewPieces], v = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kFewPieces; ++i) {
+        const float* p = piece(i < j.pieces ? i : 0);
+        m[i] = i < j.pieces ? p[c] : -FLT_MAX;
+        l[i] = i < j.pieces ? p[NC + c] : 0.0f;
+        x[i] = *reinterpret_cast<const f32x4*>(p + 2 * NC + c * D + ch);
+        M = fmaxf(M, m[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kFewPieces; ++i) {
+        const float f = i < j.pieces ? __builtin_amdgcn_exp2f(m[i] - M) : 0.0f;
+        L = __builtin_fmaf(l[i], f, L);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = i < j.pieces ? __builtin_fmaf(x[i][e], f, v[e]) : v[e];
+      }
+      const float g = L != 0.0f ? vg / L : 0.0f;
+      *reinterpret_cast<u32x2*>(out(c) + ch) = u32x2{pack(cvt_bf16(v[0] * g, v[1] * g)), pack(cvt_bf16(v[2] * g, v[3] * g))};
+    }
+    return;
+  }
   for (int c = blockIdx.y; c < j.cols; c += gridDim.y) {
     float M = -FLT_MAX;
     for (int i = tid; i < j.pieces; i += kThreads) M = fmaxf(M, piece(i)[c]);
@@ -1315,9 +1344,7 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv
         sum += sums[i][tid];
         all += wave_l[i];
       }
-      const int col = j.col0 + c, i = col / a.group;
-      uint16_t* o = a.out + ((int64_t)(j.start + i) * a.kv * a.group + j.head * a.group + col - i * a.group) * D;
-      o[tid] = __builtin_bit_cast(uint16_t, (__bf16)(all != 0.0f ? sum * (vg / all) : 0.0f));
+      out(c)[tid] = __builtin_bit_cast(uint16_t, (__bf16)(all != 0.0f ? sum * (vg / all) : 0.0f));
     }
     __syncthreads();
   }
