@@ -479,7 +479,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
                                const int32_t* lengths, const int32_t* q_start, int64_t B, int64_t n, int64_t q_heads,
                                int64_t heads, int64_t D, int64_t page, int64_t pages, float scale, int64_t window,
                                void* out, void* workspace, int64_t workspace_bytes, hipStream_t stream);
-int64_t wush_kv4_attention_workspace(int64_t B, int64_t n, int64_t q_heads, int64_t heads, int64_t D, int64_t page,
+int64_t wush_kv4_attention_workspace(int fmt, int64_t B, int64_t n, int64_t q_heads, int64_t heads, int64_t D, int64_t page,
                                      int64_t width);
 
 /* ---- Around the products of a decode step ---------------------------------- */

@@ -50,7 +50,7 @@ SIGNATURES = {
     "wush_kv4_attention": (_c_int, [_c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
                                     _i64, _i64, _i64, _i64, _i64, _i64, _i64, ctypes.c_float, _i64, _vp, _vp, _i64,
                                     _vp]),
-    "wush_kv4_attention_workspace": (_i64, [_i64, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "wush_kv4_attention_workspace": (_i64, [_c_int, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
     "wush_linear_w4_lora": (_c_int, [_c_int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                                      _i64, _vp, _c_int, _vp, _i64, _vp]),
     "wush_linear_w4_lora_workspace": (_i64, [_i64, _i64, _i64, _i64, _c_int, _c_int]),

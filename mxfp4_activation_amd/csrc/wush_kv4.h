@@ -69,8 +69,10 @@ enum { kKvNarrow, kKvWide, kKvPrompt };  // four waves share columns, the same w
 // Tiles of 16 columns per wave: one where the results of two would not fit the registers.
 constexpr int kv_tiles(int shape, int D) { return shape == kKvNarrow || D > 128 ? 1 : 2; }
 constexpr int kv_columns(int shape, int D) { return 16 * kv_tiles(shape, D) * (shape == kKvPrompt ? 4 : 1); }
-// Workgroups that the chip holds at a time, by the kernels' registers.
-constexpr int kv_resident(int shape, int D) { return shape == kKvNarrow ? (D == 64 ? 1024 : D == 128 ? 768 : 512) : 512; }
+// Workgroups that the chip holds at a time, by the kernels' registers (INT4's scales take some).
+constexpr int kv_resident(int shape, int D, int fmt) {
+  return shape != kKvNarrow || D > 128 ? 512 : D == 128 ? (fmt == 2 ? 512 : 768) : fmt == 2 ? 768 : 1024;
+}
 
 struct KvPlan {
   int shape;
@@ -80,7 +82,7 @@ struct KvPlan {
 
 constexpr int64_t kKvWholeTokens = 512;  // up to here an item is not worth cutting
 
-inline KvPlan kv_plan(int64_t B, int64_t n, int64_t kv, int64_t group, int D, int64_t tokens) {
+inline KvPlan kv_plan(int fmt, int64_t B, int64_t n, int64_t kv, int64_t group, int D, int64_t tokens) {
   KvPlan p;
   const int64_t columns = B > 0 ? n * group / B : 0;  // of a sequence, on average
   p.shape = columns <= 16 ? kKvNarrow : columns <= (D > 128 ? 32 : 64) ? (D > 128 ? kKvNarrow : kKvWide) : kKvPrompt;
@@ -88,7 +90,7 @@ inline KvPlan kv_plan(int64_t B, int64_t n, int64_t kv, int64_t group, int D, in
   const int64_t seqs = B < n ? B : n;
   p.items = (n * group / kv_columns(p.shape, D) + seqs) * kv;
   const int64_t units = p.items * ((tokens + kKvUnit - 1) / kKvUnit + 1);
-  const int64_t resident = kv_resident(p.shape, D);
+  const int64_t resident = kv_resident(p.shape, D, fmt);
   p.runs = (int)(tokens <= kKvWholeTokens ? 0 : units < resident ? units : resident);
   // Pieces of ceil(all units / runs) are at most runs and one more per item.
   p.workgroups = p.items + p.runs;

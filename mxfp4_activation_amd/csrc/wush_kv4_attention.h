@@ -638,11 +638,11 @@ __device__ __forceinline__ void wave_fence() {
 template <int D>
 constexpr int kQLine = D + 8;  // of a query in LDS, elements
 
-// Whether the columns' operands stay in LDS (transformed ones in two planes, or long ones, or
-// two tiles beside INT4's scales) rather than in registers, and the elements that a tile of
+// Whether the columns' operands stay in LDS (transformed ones in two planes, long ones, or two
+// tiles of them, which spilled) rather than in registers, and the elements that a tile of
 // them takes there.
 template <int FMT, int D, int SHAPE, int PLANES>
-constexpr bool kStaged = PLANES == 2 || D == 256 || (FMT == kINT && SHAPE != kKvNarrow);
+constexpr bool kStaged = PLANES == 2 || D == 256 || SHAPE != kKvNarrow;
 template <int D, int PLANES>
 constexpr int kQTile = PLANES * 16 * kQLine<D>;
 
@@ -1194,7 +1194,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
 }
 
 template <int FMT, int D, int SHAPE, int PLANES>
-__global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D) / 256) void kv4_attention_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D, FMT) / 256) void kv4_attention_kernel(KvAttnArgs a) {
   constexpr int NC = kv_columns(SHAPE, D);
   extern __shared__ __attribute__((aligned(16))) float lds[];
   __shared__ float stat[2][4][32];

@@ -124,12 +124,13 @@ wush_status wush_kv4_append(int fmt, const void* K, int64_t ldk, const void* V, 
   return launched(wush::launch_kv4_append(a, stream));
 }
 
-int64_t wush_kv4_attention_workspace(int64_t B, int64_t n, int64_t q_heads, int64_t heads, int64_t D, int64_t page,
+int64_t wush_kv4_attention_workspace(int fmt, int64_t B, int64_t n, int64_t q_heads, int64_t heads, int64_t D, int64_t page,
                                      int64_t width) {
+  if (fmt < wush::kMXFP4 || fmt > wush::kINT4) return 0;
   if (B <= 0 || n <= 0 || heads <= 0 || q_heads <= 0 || q_heads % heads != 0 || page <= 0 || width <= 0) return 0;
   if (D != 64 && D != 128 && D != 256) return 0;
   if (B > kMaxTokens || n > kMaxTokens || heads > kMaxHeads || q_heads > kMaxHeads || width > kMaxTokens / page) return 0;
-  const wush::KvPlan p = wush::kv_plan(B, n, heads, q_heads / heads, (int)D, page * width);
+  const wush::KvPlan p = wush::kv_plan(fmt, B, n, heads, q_heads / heads, (int)D, page * width);
   return wush::kv_workspace(p, (int)D);
 }
 
@@ -160,11 +161,11 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   if (!aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(q_start, 4))
     return fail(WUSH_EALIGN, "block_table, lengths and q_start must be 4-byte aligned");
   if (!aligned(out, 16)) return fail(WUSH_EALIGN, "out must be 16-byte aligned");
-  const wush::KvPlan plan = wush::kv_plan(B, n, heads, q_heads / heads, (int)D, page * width);
+  const wush::KvPlan plan = wush::kv_plan(fmt, B, n, heads, q_heads / heads, (int)D, page * width);
   // Items and units are counted in 32 bits.
   if (plan.items > INT32_MAX / 2 / (page * width / wush::kKvUnit + 2))
     return fail(WUSH_EINVAL, "too many tokens for one launch");
-  const int64_t need = wush_kv4_attention_workspace(B, n, q_heads, heads, D, page, width);
+  const int64_t need = wush_kv4_attention_workspace(fmt, B, n, q_heads, heads, D, page, width);
   st = check_workspace(workspace, workspace_bytes, need);
   if (st != WUSH_OK) return st;
   const int64_t rows = pages * heads * page;

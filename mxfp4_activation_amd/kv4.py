@@ -124,7 +124,7 @@ def kv4_attention(fmt: str, q: torch.Tensor, cache: KV4Cache, block_table: torch
     else:
         po = _check(out, "out", torch.bfloat16, (n, hq, D), dev)
     lib = _lib.load()
-    nw = lib.wush_kv4_attention_workspace(B, n, hq, heads, D, page, width)
+    nw = lib.wush_kv4_attention_workspace(f, B, n, hq, heads, D, page, width)
     ws = _workspace(nw, dev)
     st = lib.wush_kv4_attention(f, q.data_ptr(), ldq, tq, kc, ks, kg, vc, vs, vg, block_table.data_ptr(),
                                 block_table.stride(0), width, pl, pq, B, n, hq, heads, D, page, pages,
