@@ -92,6 +92,28 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+_NATIVE = ("wush_kv4_append", "wush_kv4_attention", "wush_kv4_attention_workspace", "wush_linear_w4_lora",
+           "wush_linear_w4_lora_workspace", "wush_adjust_logits")
+_binding = False  # not looked for yet
+
+
+def binding():
+    """The native form of the wrappers' argument marshalling (csrc/binding.cpp), or None
+    where it is not built: the wrappers then do it in Python, some ten microseconds slower.
+    Needs torch to be imported."""
+    global _binding
+    if _binding is False:
+        try:
+            from . import _binding as module
+        except ImportError:
+            module = None
+        if module is not None:
+            lib = load()
+            module.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _NATIVE})
+        _binding = module
+    return _binding
+
+
 def check(status: int, where: str) -> None:
     if status != WUSH_OK:
         lib = load()

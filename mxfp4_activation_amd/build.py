@@ -1,4 +1,5 @@
-"""Build the HIP shared library libwush.so in-tree for gfx950.
+"""Build the HIP shared library libwush.so in-tree for gfx950, and the native
+argument marshalling of some of its Python wrappers (host code only).
 
 Usage: python -m mxfp4_activation_amd.build  (or call build()).
 """
@@ -9,10 +10,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwush.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["wush_kernels.hip", "wush_gemm.hip", "wush_dequant.hip", "wush_build.hip", "wush_gptq.hip", "wush_w4.hip",
            "wush_moe.hip", "wush_logprobs.hip", "wush_kv4.hip", "wush_kv4_mx.hip", "wush_kv4_nv.hip", "wush_kv4_int.hip",
            "wush_adjust.hip", "wush_abi.cpp", "wush_decode_abi.cpp", "wush_serving_abi.cpp"]
@@ -43,6 +46,27 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
+def build_binding(verbose: bool = False) -> str:
+    """csrc/binding.cpp against this torch's headers."""
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + os.path.join(at, "include"),
+           "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I/opt/rocm/include",
+           "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
+           "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("%s failed (exit %d)" % (cmd[0], r.returncode))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     tmp = LIB + ".tmp"
@@ -56,6 +80,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     if verbose and r.stderr.strip():
         sys.stderr.write(r.stderr)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
 
 

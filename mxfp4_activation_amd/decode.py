@@ -147,6 +147,13 @@ def linear_w4_lora(fmt: str, x: torch.Tensor, codes: torch.Tensor, scales: torch
     """``linear_w4`` plus each token's own low-rank adapter: x' W^T + scale[e] (x A[e]^T)
     B[e]^T with e = ids[m] (int32 [M]; negative: no adapter, out of range: NaN) and x
     untransformed.  The sums are fp32 and rounded once."""
+    native = _lib.binding()
+    if native is not None and out_dtype in _OUT:
+        r = native.lora(fmt, x, codes, scales, *adapters, ids, T, global_scale, out_dtype is torch.float32, out)
+        if r is not None:
+            if type(r) is int:
+                _lib.check(r, "wush_linear_w4_lora(%s)" % fmt)
+            return r
     f, G = _fmt(fmt)
     ot = _out_type(out_dtype)
     M, K, ldx = _rows(x, "x")
@@ -264,6 +271,13 @@ def adjust_logits(logits: torch.Tensor, prompt: Optional[torch.Tensor] = None, o
     bias_ids [R, n] (int32, -1 pads); tokens whose bit of allowed (int32 [R, (V + 31) // 32],
     bit v % 32 of word v // 32) is not set become -inf.  The penalties and biases are float32.
     Returns a new tensor, or out, which may be logits itself."""
+    native = _lib.binding()
+    if native is not None:
+        r = native.adjust(logits, prompt, output, repetition, frequency, presence, bias_ids, bias, allowed, out)
+        if r is not None:
+            if type(r) is int:
+                _lib.check(r, "wush_adjust_logits")
+            return r
     R, V, lt = _logits(logits, "logits")
     dev, stream = _enter(logits, "logits")
 

@@ -2,6 +2,8 @@
 
 Like ``decode``, these functions only marshal arguments: they allocate outputs
 and workspace with torch and enqueue the library call on torch's current stream.
+Where it is built, native code does that (``_lib.binding``), and leaves to the
+code here what is not plainly right.
 """
 
 from __future__ import annotations
@@ -74,6 +76,13 @@ def kv4_append(fmt: str, k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slot
     stride that is a multiple of 8) into the cache's slots [n] (int64; outside the
     cache, a negative one say: not written; otherwise all different), after the
     block transforms T_k, T_v [heads, D/G, G, G], if given."""
+    native = _lib.binding()
+    if native is not None:
+        st = native.append(fmt, k, v, *cache, slots, T_k, T_v)
+        if st is not None:
+            if st:
+                _lib.check(st, "wush_kv4_append(%s)" % fmt)
+            return
     f, G = _fmt(fmt)
     n, h, D, ldk = _heads(k, "k")
     dev, stream = _enter(k, "k")
@@ -104,6 +113,13 @@ def kv4_attention(fmt: str, q: torch.Tensor, cache: KV4Cache, block_table: torch
     up to its own, or the last `window` of them.  scale: D ** -0.5 unless given.  T_q
     [heads, D/G, G, G] goes with keys that were transformed.  Returns bf16
     [n, q_heads, D]; rows from q_start[B] on are not written."""
+    native = _lib.binding()
+    if native is not None:
+        r = native.attention(fmt, q, *cache, block_table, lengths, q_start, scale, window, T_q, out)
+        if r is not None:
+            if type(r) is int:
+                _lib.check(r, "wush_kv4_attention(%s)" % fmt)
+            return r
     f, G = _fmt(fmt)
     n, hq, D, ldq = _heads(q, "q")
     dev, stream = _enter(q, "q")
