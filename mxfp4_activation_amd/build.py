@@ -11,14 +11,17 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwush.so")
 BINDING = os.path.join(HERE, "_binding.so")
-SOURCES = ["wush_kernels.hip", "wush_gemm.hip", "wush_dequant.hip", "wush_build.hip", "wush_gptq.hip", "wush_w4.hip",
-           "wush_moe.hip", "wush_logprobs.hip", "wush_kv4.hip", "wush_kv4_mx.hip", "wush_kv4_nv.hip", "wush_kv4_int.hip",
-           "wush_adjust.hip", "wush_abi.cpp", "wush_decode_abi.cpp", "wush_serving_abi.cpp"]
+# (those that take longest first)
+SOURCES = ["wush_kernels.hip", "wush_w4.hip", "wush_kv4_int.hip", "wush_kv4_nv.hip", "wush_kv4_mx.hip", "wush_moe.hip",
+           "wush_logprobs.hip", "wush_gptq.hip", "wush_build.hip", "wush_gemm.hip", "wush_kv4.hip", "wush_adjust.hip",
+           "wush_dequant.hip", "wush_abi.cpp", "wush_decode_abi.cpp", "wush_serving_abi.cpp"]
 
 HIPCC_FLAGS = [
     "-O3",
@@ -59,26 +62,36 @@ def build_binding(verbose: bool = False) -> str:
            "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("%s failed (exit %d)" % (cmd[0], r.returncode))
+    _run(cmd)
     os.replace(tmp, BINDING)
     return BINDING
 
 
-def build(verbose: bool = False, extra_flags=None) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB + ".tmp"
-    cmd = [hipcc()] + HIPCC_FLAGS + list(extra_flags or []) + ["-o", tmp] + srcs
-    if verbose:
-        print(" ".join(cmd), flush=True)
+def _run(cmd) -> str:
+    """Runs a compiler; what it said, or RuntimeError."""
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed (exit %d)" % r.returncode)
-    if verbose and r.stderr.strip():
-        sys.stderr.write(r.stderr)
+        raise RuntimeError("%s failed (exit %d)" % (cmd[0], r.returncode))
+    return r.stderr
+
+
+def build(verbose: bool = False, extra_flags=None) -> str:
+    """Every source to an object of its own, several at a time, then the library."""
+    flags = HIPCC_FLAGS + list(extra_flags or [])
+    tmp = LIB + ".tmp"
+    jobs = int(os.environ.get("MAX_JOBS", 0)) or min(8, os.cpu_count() or 1)
+    with tempfile.TemporaryDirectory() as out, ThreadPoolExecutor(jobs) as pool:
+        objects = [os.path.join(out, s + ".o") for s in SOURCES]
+        cmds = [[hipcc()] + [f for f in flags if f != "-shared"] + ["-c", os.path.join(CSRC, s), "-o", o]
+                for s, o in zip(SOURCES, objects)]
+        link = [hipcc()] + flags + ["-o", tmp] + objects
+        if verbose:
+            for cmd in cmds + [link]:
+                print(" ".join(cmd), flush=True)
+        said = list(pool.map(_run, cmds)) + [_run(link)]
+    if verbose:
+        sys.stderr.write("".join(t for t in said if t.strip()))
     os.replace(tmp, LIB)
     build_binding(verbose)
     return LIB
