@@ -36,7 +36,12 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
   return __uint_as_float(((e + 120u) << 23) | (m << 20));
 }
 
+// x is rounded to fp32 before: behind an FMA the compiler would otherwise
+// round its unrounded sum to fp16 at once (v_fma_mixlo_f16), and a quotient
+// half way between two fp16 numbers by way of div7's correction, whose own
+// error then decides, would not go to the even one.
 __device__ __forceinline__ uint32_t f16_bits(float x) {
+  asm("" : "+v"(x));
   _Float16 h = (_Float16)x;  // v_cvt_f16_f32: round to nearest even
   return (uint32_t)__builtin_bit_cast(uint16_t, h);
 }

@@ -282,3 +282,31 @@ def test_transformed_keys_with_transformed_queries(fmt):
         part = lambda c: tuple(a[:, h] for a in c)  # noqa: E731
         want, bound = ref.attention(q[:, h], part(kc), part(vc), fmt, np.array([L - 1]), D**-0.5, T=H[h], kg=gn, vg=gn)
         assert np.all(np.abs(out[:, h] - want) <= bound)
+
+
+def test_int4_scales_half_way():
+    """Largest values a with a / 7 half way between two fp16 numbers: the scale is the even one."""
+    import mxfp4_activation_amd as wush
+
+    half = np.arange(2049, 4096, 2).astype(np.float64)  # 12 bits, the last one set
+    n, D, page = half.size, 64, 16
+    a = 7 * half * 2.0**-11
+    top = bf16(a)[0]
+    assert np.all(a == top + bf16(a - top)[0])
+    # A transform that adds two channels forms them without an error.
+    x = np.zeros((n, 1, D))
+    x[:, 0, 3], x[:, 0, 5] = top, a - top
+    x[:, 0, 40], x[:, 0, 41] = -top, top - a
+    T = np.zeros((1, 2, 32, 32))
+    T[0, 0, 7, [3, 5]] = T[0, 1, 9, [8, 9]] = 1
+    T[0, 0, 1, 3] = T[0, 1, 30, 9] = 0.25
+    (x, xb), (T, Tb) = bf16(x), bf16(T)
+    lead = (-(-n // page), 1, page)
+    cache = wush.KV4Cache(*(dev(np.zeros((*lead, D // 2), np.uint8)) if i % 2 == 0 else
+                            dev_scales("int4", np.zeros((*lead, D // 32), np.uint16)) for i in range(4)))
+    wush.kv4_append("int4", dev_bf16(xb), dev_bf16(xb), cache, dev(np.arange(n)), T_k=dev_bf16(Tb), T_v=dev_bf16(Tb))
+    codes, scales = ref.append(x, "int4", T)
+    assert np.all(scales % 2 == 0) and np.all(scales > 0)
+    for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert np.array_equal(s.view(torch.int16).cpu().numpy().view(np.uint16).reshape(n, 1, 2), scales)
+        assert np.array_equal(c.cpu().numpy().reshape(n, 1, D // 2), codes)
