@@ -587,7 +587,9 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2][NQ], int t0, int lo, c
     }
 }
 
-// Scores of 32 tokens to probabilities, up to the running maximum m, as B operands.
+// Scores of 32 tokens to probabilities, up to the running maximum m, as B operands.  These are
+// bf16: a probability is off by at most 2^-8 of itself, as the result is.  l sums the rounded
+// ones, so that where one token outweighs the others nothing of that is left.
 template <int NQ, int CH>
 __device__ __forceinline__ void softmax_step(const f32x4 (&s)[2][NQ], float scale, float (&m)[NQ], float (&l)[NQ],
                                              f32x4 (&acc)[CH][NQ], bf16x8 (&pf)[NQ]) {
@@ -619,12 +621,15 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[2][NQ], float scal
   for (int ct = 0; ct < NQ; ++ct) {
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][ct][i & 3], scale, -m[ct]));
-      l[ct] += e[i];
+    for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][ct][i & 3], scale, -m[ct]));
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf16x2 c = cvt_bf16(e[2 * i], e[2 * i + 1]);
+      w[i] = pack(c);
+      l[ct] = __builtin_amdgcn_fdot2_f32_bf16(c, bf16x2{(__bf16)1.0f, (__bf16)1.0f}, l[ct], false);
     }
-    pf[ct] = __builtin_bit_cast(bf16x8, (u32x4{pack(cvt_bf16(e[0], e[1])), pack(cvt_bf16(e[2], e[3])),
-                                              pack(cvt_bf16(e[4], e[5])), pack(cvt_bf16(e[6], e[7]))}));
+    pf[ct] = __builtin_bit_cast(bf16x8, w);
   }
 }
 

@@ -62,7 +62,9 @@ def attention(q, k, v, fmt, pos, scale, window=0, T=None, kg=None, vg=None):
     # may lie 2^8 below the largest), the exponential.
     dp = np.where(seen, ds + (4 * (gap + 16 + np.abs(m)) + 16) * U, 0.0)
     n = K.shape[0] + 64
-    # bf16 probabilities and INT4 values, fp32 sums; the denominator; the result.
+    # bf16 probabilities, of which the denominator is the sum, and INT4 values, fp32 sums; the
+    # denominator; the result.  (Probabilities w (1 + d), |d| <= BF16, move the result by
+    # sum w d (V - out) / (1 + sum w d): at most BF16 (w |V - out|) / (1 - BF16).)
     rel = BF16 + (BF16 if fmt == "int4" else 0) + n * U
-    bound = (w * (dp + rel)) @ np.abs(V) + np.abs(out) * ((w * dp).sum(1, keepdims=True) + n * U)
+    bound = (w * (dp + rel)) @ np.abs(V) + np.abs(out) * ((w * dp).sum(1, keepdims=True) + BF16 + n * U)
     return out, 1.05 * bound + BF16 * np.abs(out) + 1e-30
