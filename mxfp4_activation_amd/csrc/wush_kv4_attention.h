@@ -25,12 +25,15 @@
 // throughout, so the softmax needs one exchange between lanes where a maximum grows
 // by more than 2^8, and one at the end.
 //
-// Exactness.  E2M1 times E8M0 or E4M3 has at most 6 significant bits and is exact in
-// bf16, as are INT4's integers.  INT4's fp16 scale multiplies K's fp32 sums over
-// one group; V as integer times scale is rounded to bf16 (off by up to 2^-8, as P is: P is a
-// probability up to the running maximum's slack, and both errors are below the
-// result's own rounding, since a result averages over its tokens).  Sums are fp32; a
-// transformed query enters as two bf16 planes (16 bits).
+// Exactness.  K: E2M1 times E8M0 or E4M3 has at most 6 significant bits and is exact in
+// bf16, as are INT4's integers, whose fp16 scale multiplies the fp32 sums over one group.
+// P and V: MXFP4's values need bf16's range; P is then rounded to 8 bits, as the result is.
+// NVFP4's and INT4's enter as fp16, and P with 11 bits: E2M1 times E4M3 is exact, an
+// integer times INT4's scale is rounded to 11 bits.  P is at most 2^8 there and taken
+// times 2^7; what fp16's range cuts off is at most 2^-32 of the largest probability.
+// INT4's values are taken times 1/8, so that the largest scale's are finite: what that
+// cuts off is at most 2^-22, no more than rounding so small a scale to fp16 has lost.
+// Sums are fp32; a transformed query enters as two bf16 planes (16 bits).
 #ifndef WUSH_KV4_ATTENTION_H_
 #define WUSH_KV4_ATTENTION_H_
 
@@ -53,6 +56,31 @@ using namespace w4;
 constexpr int kThreads = 256;
 constexpr int kTile = 32;   // tokens of a wave's step
 constexpr float kSlack = 8.0f;  // log2 by which scores may pass the running maximum
+
+// Whether P and V are fp16 (else bf16), log2 of the factor at P and V's factor.
+template <int FMT>
+constexpr bool kHalf = FMT != kMX;
+template <int FMT>
+constexpr float kPShift = kHalf<FMT> ? 7.0f : 0.0f;
+template <int FMT>
+constexpr float kVFactor = FMT == kINT ? 0.125f : 1.0f;
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f16x2 half2_of(uint32_t v) { return __builtin_bit_cast(f16x2, v); }
+__device__ __forceinline__ uint32_t bits_of(f16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ f16x2 cvt_f16(float a, float b) { return __builtin_convertvector((f32x2{a, b}), f16x2); }
+
+// O^T += V^T P^T.
+template <int FMT>
+__device__ __forceinline__ f32x4 add_pv(const u32x4& v, const u32x4& p, const f32x4& c) {
+  if constexpr (kHalf<FMT>) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), __builtin_bit_cast(f16x8, p), c, 0, 0, 0);
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, p), c, 0, 0, 0);
+  }
+}
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -451,61 +479,64 @@ __device__ __forceinline__ float k_scale(const Raw<FMT, D>& w, int u, int j) {
   }
 }
 
-// Byte b (two channels) of V's dword i for all eight tokens, as the A operands of two
-// matrix instructions.
+// Byte B (two channels) of a dword of codes, with their scale or E2M1's own values.
+template <int B>
+__device__ __forceinline__ uint32_t mx_pair(uint32_t codes, float scale) {
+  return pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, B));
+}
+template <int B>
+__device__ __forceinline__ f16x2 e2m1_pair(uint32_t codes) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, 1.0f, B);
+}
+
+// Scales of V's eight tokens as expand_v wants them: fp32 (MXFP4), twice the same fp16
+// (NVFP4), pairs of fp16 (INT4).
+template <int FMT>
+struct VScales {
+  uint32_t s[FMT == kINT ? 4 : 8];
+};
 template <int FMT, int D>
-__device__ __forceinline__ void expand_v(const Raw<FMT, D>& w, const float (&s)[8], int i, int b, u32x4& even, u32x4& odd) {
+__device__ __forceinline__ VScales<FMT> v_scales(const Raw<FMT, D>& w) {
+  VScales<FMT> o;
+#pragma unroll
+  for (int i = 0; i < (FMT == kINT ? 4 : 8); ++i) {
+    if constexpr (FMT == kMX) {
+      o.s[i] = w.vs[i] << 23;
+    } else if constexpr (FMT == kNV) {
+      const float v = __builtin_amdgcn_cvt_f32_fp8(w.vs[i], 0);
+      o.s[i] = bits_of(cvt_f16(v, v));
+    } else {
+      o.s[i] = w.vs[2 * i] | w.vs[2 * i + 1] << 16;
+    }
+  }
+  return o;
+}
+
+// Byte B (two channels) of V's dword i for all eight tokens, as the A operands of two
+// matrix instructions.
+template <int FMT, int D, int B>
+__device__ __forceinline__ void expand_v(const Raw<FMT, D>& w, const VScales<FMT>& v, int i, u32x4& even, u32x4& odd) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const uint32_t d0 = w.vc[2 * p][i], d1 = w.vc[2 * p + 1][i];
-    if constexpr (FMT == kMX) {
+    if constexpr (FMT == kINT) {
+      // Both tokens' byte.  Codes with their sign bits turned over are codes + 8; as mantissa
+      // bits of fp16 numbers they stand for eighths: 128 + (code + 8) / 8, 8 + (code + 8) / 8.
+      const uint32_t t = __builtin_amdgcn_perm(d1, d0, 0x0C000C00u | (uint32_t)((4 + B) << 16 | B));
+      const f16x2 s = half2_of(v.s[p]);
+      even[p] = bits_of((half2_of((t & 0x000F000Fu) ^ 0x58085808u) - f16x2{129, 129}) * s);
+      odd[p] = bits_of((half2_of((t & 0x00F000F0u) ^ 0x48804880u) - f16x2{9, 9}) * s);
+    } else {
       uint32_t c0, c1;
-      switch (b) {
-        case 0:
-          c0 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d0, s[2 * p], 0));
-          c1 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d1, s[2 * p + 1], 0));
-          break;
-        case 1:
-          c0 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d0, s[2 * p], 1));
-          c1 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d1, s[2 * p + 1], 1));
-          break;
-        case 2:
-          c0 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d0, s[2 * p], 2));
-          c1 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d1, s[2 * p + 1], 2));
-          break;
-        default:
-          c0 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d0, s[2 * p], 3));
-          c1 = pack(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d1, s[2 * p + 1], 3));
+      if constexpr (FMT == kMX) {
+        c0 = mx_pair<B>(d0, __uint_as_float(v.s[2 * p]));
+        c1 = mx_pair<B>(d1, __uint_as_float(v.s[2 * p + 1]));
+      } else {
+        c0 = bits_of(e2m1_pair<B>(d0) * half2_of(v.s[2 * p]));
+        c1 = bits_of(e2m1_pair<B>(d1) * half2_of(v.s[2 * p + 1]));
       }
       even[p] = __builtin_amdgcn_perm(c1, c0, 0x05040100u);
       odd[p] = __builtin_amdgcn_perm(c1, c0, 0x07060302u);
-    } else if constexpr (FMT == kNV) {
-      f32x2 c0, c1;
-      switch (b) {
-        case 0:
-          c0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d0, 1.0f, 0);
-          c1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d1, 1.0f, 0);
-          break;
-        case 1:
-          c0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d0, 1.0f, 1);
-          c1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d1, 1.0f, 1);
-          break;
-        case 2:
-          c0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d0, 1.0f, 2);
-          c1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d1, 1.0f, 2);
-          break;
-        default:
-          c0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d0, 1.0f, 3);
-          c1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d1, 1.0f, 3);
-      }
-      even[p] = pack(cvt_bf16(c0[0] * s[2 * p], c1[0] * s[2 * p + 1]));
-      odd[p] = pack(cvt_bf16(c0[1] * s[2 * p], c1[1] * s[2 * p + 1]));
-    } else {
-      // The integer, exact in fp32, times the scale: exact too (15 bits), then rounded.
-      const int e0 = (int)(d0 << (28 - 8 * b)) >> 28, e1 = (int)(d1 << (28 - 8 * b)) >> 28;
-      const int o0 = (int)(d0 << (24 - 8 * b)) >> 28, o1 = (int)(d1 << (24 - 8 * b)) >> 28;
-      even[p] = pack(cvt_bf16((float)e0 * s[2 * p], (float)e1 * s[2 * p + 1]));
-      odd[p] = pack(cvt_bf16((float)o0 * s[2 * p], (float)o1 * s[2 * p + 1]));
     }
   }
 }
@@ -538,15 +569,6 @@ __device__ __forceinline__ void arrange_k(Raw<FMT, D>& w, int u) {
       for (int j = 0; j < 4; ++j) w.kc[u][4 * i + j] = c[j];
     }
   }
-}
-
-template <int FMT, int D>
-__device__ __forceinline__ void v_scales(const Raw<FMT, D>& w, float (&vs)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    vs[i] = FMT == kMX   ? __uint_as_float(w.vs[i] << 23)
-            : FMT == kNV ? __builtin_amdgcn_cvt_f32_fp8(w.vs[i], 0)
-                         : half_value(w.vs[i]);
 }
 
 // Zeros for the step's tokens outside [lo, hi).
@@ -587,12 +609,12 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2][NQ], int t0, int lo, c
     }
 }
 
-// Scores of 32 tokens to probabilities, up to the running maximum m, as B operands.  These are
-// bf16: a probability is off by at most 2^-8 of itself, as the result is.  l sums the rounded
-// ones, so that where one token outweighs the others nothing of that is left.
-template <int NQ, int CH>
+// Scores of 32 tokens to probabilities, up to the running maximum m, as B operands.  l sums
+// what they were rounded to, so that where one token outweighs the others nothing of the
+// rounding is left.
+template <int FMT, int NQ, int CH>
 __device__ __forceinline__ void softmax_step(const f32x4 (&s)[2][NQ], float scale, float (&m)[NQ], float (&l)[NQ],
-                                             f32x4 (&acc)[CH][NQ], bf16x8 (&pf)[NQ]) {
+                                             f32x4 (&acc)[CH][NQ], u32x4 (&pf)[NQ]) {
   // The running maximum moves where a score passes it by more than the slack.
   float high[NQ];
   bool grown = false;
@@ -620,16 +642,21 @@ __device__ __forceinline__ void softmax_step(const f32x4 (&s)[2][NQ], float scal
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
     float e[8];
+    const float shift = kPShift<FMT> - m[ct];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][ct][i & 3], scale, -m[ct]));
-    u32x4 w;
+    for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][ct][i & 3], scale, shift));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bf16x2 c = cvt_bf16(e[2 * i], e[2 * i + 1]);
-      w[i] = pack(c);
-      l[ct] = __builtin_amdgcn_fdot2_f32_bf16(c, bf16x2{(__bf16)1.0f, (__bf16)1.0f}, l[ct], false);
+      if constexpr (kHalf<FMT>) {
+        const f16x2 c = cvt_f16(e[2 * i], e[2 * i + 1]);
+        pf[ct][i] = bits_of(c);
+        l[ct] = __builtin_amdgcn_fdot2(c, f16x2{1, 1}, l[ct], false);
+      } else {
+        const bf16x2 c = cvt_bf16(e[2 * i], e[2 * i + 1]);
+        pf[ct][i] = pack(c);
+        l[ct] = __builtin_amdgcn_fdot2_f32_bf16(c, bf16x2{(__bf16)1.0f, (__bf16)1.0f}, l[ct], false);
+      }
     }
-    pf[ct] = __builtin_bit_cast(bf16x8, w);
   }
 }
 
@@ -866,25 +893,22 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       // Places without a token may hold anything, also what 0 does not cancel.
       clear_v(w, t0, lo, hi);
     }
-    bf16x8 pf[NQ];
-    softmax_step<NQ, CH>(s, scale, m, l, acc, pf);
-    float vs[8];
-    v_scales(w, vs);
+    u32x4 pf[NQ];
+    softmax_step<FMT, NQ, CH>(s, scale, m, l, acc, pf);
+    const VScales<FMT> vs = v_scales(w);
 #pragma unroll
     for (int i = 0; i < RawT::kV; ++i)
-#pragma unroll
-      for (int b = 0; b < (CH < 8 ? CH / 2 : 4); ++b) {
+      each<(CH < 8 ? CH / 2 : 4)>([&](auto bc) {
+        constexpr int b = bc;
         u32x4 even, odd;
-        expand_v<FMT, D>(w, vs, i, b, even, odd);
+        expand_v<FMT, D, b>(w, vs, i, even, odd);
 #pragma unroll
         for (int ct = 0; ct < NQ; ++ct) {
-          acc[8 * i + 2 * b][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), pf[ct],
-                                                                           acc[8 * i + 2 * b][ct], 0, 0, 0);
-          acc[8 * i + 2 * b + 1][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), pf[ct],
-                                                                               acc[8 * i + 2 * b + 1][ct], 0, 0, 0);
+          acc[8 * i + 2 * b][ct] = add_pv<FMT>(even, pf[ct], acc[8 * i + 2 * b][ct]);
+          acc[8 * i + 2 * b + 1][ct] = add_pv<FMT>(odd, pf[ct], acc[8 * i + 2 * b + 1][ct]);
         }
         __builtin_amdgcn_sched_barrier(0);
-      }
+      });
   };
 
   if (steps > 0) {
@@ -902,7 +926,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
     if (__any(bad)) l[ct] = __builtin_nanf("");
   }
 
-  const float vg = FMT == kNV ? a.v_gs[0] : 1.0f;
+  const float vg = FMT == kNV ? a.v_gs[0] : 1.0f / kVFactor<FMT>;
   // The four waves' results of a column meet in LDS: factors first, then quads of
   // channels, one per lane, without conflicts between banks.
 #pragma unroll
@@ -1085,7 +1109,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   __syncthreads();  // the queries' LDS is free
 
   // A tile's operands: K's 2 KJ (half u, instruction j), then V's CH, 1 KB each, lane by lane.
-  auto operand = [&](int tile, int i) { return reinterpret_cast<bf16x8*>(tiles + tile * kLds + i * 512 + lane * 8); };
+  auto operand = [&](int tile, int i) { return reinterpret_cast<u32x4*>(tiles + tile * kLds + i * 512 + lane * 8); };
   auto k_scale_dword = [&](int tile, int u) {
     return reinterpret_cast<uint32_t*>(tiles + tile * kLds + (2 * KJ + CH) * 512) + u * 64 + lane;
   };
@@ -1097,23 +1121,23 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
         arrange_k(w, u);
 #pragma unroll
         for (int j = 0; j < KJ; ++j)
-          *operand(sub, u * KJ + j) = expand<FMT>(w.kc[u][j], FMT == kINT ? 0.0f : k_scale(w, u, j));
+          *operand(sub, u * KJ + j) =
+              __builtin_bit_cast(u32x4, expand<FMT>(w.kc[u][j], FMT == kINT ? 0.0f : k_scale(w, u, j)));
         if constexpr (FMT == kINT) *k_scale_dword(sub, u) = w.ks[u];
       }
     }
     if (does_v) {
       if (t0 < p.lo || t0 + kTile > p.hi) clear_v(w, t0, p.lo, p.hi);
-      float vs[8];
-      v_scales(w, vs);
+      const VScales<FMT> vs = v_scales(w);
 #pragma unroll
       for (int i = 0; i < RawT::kV; ++i)
-#pragma unroll
-        for (int b = 0; b < (CH < 8 ? CH / 2 : 4); ++b) {
+        each<(CH < 8 ? CH / 2 : 4)>([&](auto bc) {
+          constexpr int b = bc;
           u32x4 even, odd;
-          expand_v<FMT, D>(w, vs, i, b, even, odd);
-          *operand(sub, 2 * KJ + 8 * i + 2 * b) = __builtin_bit_cast(bf16x8, even);
-          *operand(sub, 2 * KJ + 8 * i + 2 * b + 1) = __builtin_bit_cast(bf16x8, odd);
-        }
+          expand_v<FMT, D, b>(w, vs, i, even, odd);
+          *operand(sub, 2 * KJ + 8 * i + 2 * b) = even;
+          *operand(sub, 2 * KJ + 8 * i + 2 * b + 1) = odd;
+        });
     }
   };
   auto compute = [&](int tile, int t0) {
@@ -1126,7 +1150,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       constexpr int j = jc;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const bf16x8 kf = *operand(tile, u * KJ + j);
+        const bf16x8 kf = __builtin_bit_cast(bf16x8, *operand(tile, u * KJ + j));
         if constexpr (FMT == kINT) {
           float sc[4];
           k_scales<KJ, j>(*k_scale_dword(tile, u), sc);
@@ -1148,13 +1172,13 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       }
     });
     if (!(t0 >= clear_from && t0 + kTile <= clear_to)) mask_scores<NQ>(s, t0, lo, pos, a.window);
-    bf16x8 pf[NQ];
-    softmax_step<NQ, CH>(s, scale, m, l, acc, pf);
+    u32x4 pf[NQ];
+    softmax_step<FMT, NQ, CH>(s, scale, m, l, acc, pf);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const bf16x8 vf = *operand(tile, 2 * KJ + j);
+      const u32x4 vf = *operand(tile, 2 * KJ + j);
 #pragma unroll
-      for (int ct = 0; ct < NQ; ++ct) acc[j][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[ct], acc[j][ct], 0, 0, 0);
+      for (int ct = 0; ct < NQ; ++ct) acc[j][ct] = add_pv<FMT>(vf, pf[ct], acc[j][ct]);
     }
   };
   for (int k = 0; k < stages; ++k) {
@@ -1170,7 +1194,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   if (__any(bad) && lane == 0) *any_bad = 1;
   __syncthreads();
   const bool nan = *any_bad != 0;
-  const float vg = FMT == kNV ? a.v_gs[0] : 1.0f;
+  const float vg = FMT == kNV ? a.v_gs[0] : 1.0f / kVFactor<FMT>;
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
     l[ct] = column_sum(l[ct]);
@@ -1281,7 +1305,7 @@ __global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D, FMT) / 256) void kv
 // are few pieces, pieces of one column where there are many.
 constexpr int kFewPieces = 4;
 template <int D, int SHAPE>
-__global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv) {
+__global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv, float factor) {
   constexpr int NC = kv_columns(SHAPE, D), kLanes = D / 4, kAtOnce = kThreads / kLanes;
   __shared__ float wave_m[4], wave_l[kAtOnce];
   __shared__ __attribute__((aligned(16))) float sums[kAtOnce][D];
@@ -1290,7 +1314,7 @@ __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv
   if (j.pieces == 0) return;
   const int tid = threadIdx.x, mine = tid / kLanes, ch = tid % kLanes * 4;
   constexpr int64_t kPiece = NC * (D + 2);
-  const float vg = nv ? a.v_gs[0] : 1.0f;
+  const float vg = nv ? a.v_gs[0] : factor;
   const float* base = a.part + (int64_t)blockIdx.x * kPiece;
   auto piece = [&](int i) { return i == 0 ? base : a.part + ((int64_t)j.next + (int64_t)(i - 1) * j.step) * kPiece; };
   auto out = [&](int c) {
@@ -1361,7 +1385,7 @@ hipError_t go(const KvAttnArgs& a, hipStream_t s) {
                             4 * lds_floats<FMT, D, SHAPE, PLANES>(), s, a);
   if (e != hipSuccess || a.runs == 0) return e;
   hipLaunchKernelGGL((kv4_join_kernel<D, SHAPE>), dim3(2 * a.runs, kv_columns(SHAPE, D) / 4), dim3(kThreads), 0, s, a,
-                     FMT == kNV ? 1 : 0);
+                     FMT == kNV ? 1 : 0, 1.0f / kVFactor<FMT>);
   return hipGetLastError();
 }
 

@@ -62,9 +62,13 @@ def attention(q, k, v, fmt, pos, scale, window=0, T=None, kg=None, vg=None):
     # may lie 2^8 below the largest), the exponential.
     dp = np.where(seen, ds + (4 * (gap + 16 + np.abs(m)) + 16) * U, 0.0)
     n = K.shape[0] + 64
-    # bf16 probabilities, of which the denominator is the sum, and INT4 values, fp32 sums; the
-    # denominator; the result.  (Probabilities w (1 + d), |d| <= BF16, move the result by
-    # sum w d (V - out) / (1 + sum w d): at most BF16 (w |V - out|) / (1 - BF16).)
-    rel = BF16 + (BF16 if fmt == "int4" else 0) + n * U
-    bound = (w * (dp + rel)) @ np.abs(V) + np.abs(out) * ((w * dp).sum(1, keepdims=True) + BF16 + n * U)
+    # Rounded probabilities, of which the denominator is the sum: w (1 + d), |d| <= e, move the
+    # result by sum w d (V - out) / (1 + sum w d), at most e (w |V - out|) / (1 - e).  MXFP4
+    # has them in bf16, the others in fp16, cut off at 2^-32 of the largest, as are INT4's
+    # values, cut off at 2^-22.  fp32 sums; the denominator; the result.
+    e = BF16 if fmt == "mxfp4" else 2.0**-11
+    cut = 0.0 if fmt == "mxfp4" else 2.0**-32 * seen
+    rel = e + (e if fmt == "int4" else 0) + n * U
+    bound = (w * (dp + rel) + cut) @ np.abs(V) + (2.0**-22 if fmt == "int4" else 0)
+    bound = bound + np.abs(out) * ((w * dp + cut).sum(1, keepdims=True) + e + n * U)
     return out, 1.05 * bound + BF16 * np.abs(out) + 1e-30

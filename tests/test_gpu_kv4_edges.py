@@ -45,6 +45,8 @@ def test_one_token_outweighs_all(fmt, D, count):
         page, place = b.table[s, at // b.page], at % b.page
         b.k[0][page, :, place] = one
         v = weight_values(b.v[0][page, :, place], b.v[1][page, :, place], fmt, b.g[1])
+        if fmt == "int4":  # up to 14 bits: values enter the sums with fp16's 11, then the result has 8
+            v = (v / 8).astype(np.float16).astype(np.float64) * 8
         want[b.start[s] : b.start[s + 1]] = np.repeat(v, b.group, 0)
     got = b.run().double().cpu().numpy()
     assert np.array_equal(got, bf16(want)[0])
@@ -310,3 +312,14 @@ def test_int4_scales_half_way():
     for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
         assert np.array_equal(s.view(torch.int16).cpu().numpy().view(np.uint16).reshape(n, 1, 2), scales)
         assert np.array_equal(c.cpu().numpy().reshape(n, 1, D // 2), codes)
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 0x7C00), (0x7B00, 0x7C00), (1, 0x400), (0x400, 0x800)])
+@pytest.mark.parametrize("count", [1, 40])
+def test_int4_value_scales_of_every_size(lo, hi, count):
+    """The largest fp16 scales stay finite, the smallest ones keep what their own rounding leaves."""
+    rng = np.random.default_rng(hi + count)
+    b = Batch(rng, "int4", 128, 2, 4, 32, [200, count + 3], [count, count])
+    b.v[1][:] = rng.integers(lo, hi, size=b.v[1].shape)
+    got = b.check()
+    assert np.all(np.isfinite(got))
