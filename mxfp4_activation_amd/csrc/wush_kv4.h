@@ -34,14 +34,13 @@ hipError_t launch_kv4_append(const KvAppendArgs& a, hipStream_t s);
 // kKvUnit tokens of an item.
 constexpr int kKvUnit = 128;
 
-// Workspace: the number of places for pieces that may hold one (in the first one's `pieces`),
-// then one of these per place, then the pieces.
+// Workspace: the number of items that may be in several pieces (in the first one's `pieces`),
+// one of these for each, then the pieces.
 struct KvJoin {
-  int32_t pieces;       // of the item whose first piece is here; otherwise 0
-  int32_t next, step;   // the others' places: next, next + step, ...
-  int32_t cols, col0;   // columns, and the first one's place in the sequence
-  int32_t start, head;  // row of the sequence's first query, key head
-  int32_t pad;
+  int32_t pieces;             // of the item; 0: it is whole after all
+  int32_t first, next, step;  // their places: first, next, next + step, ...
+  int32_t cols, col0;         // columns, and the first one's place in the sequence
+  int32_t start, head;        // row of the sequence's first query, key head
 };
 
 struct KvAttnArgs {
@@ -56,12 +55,12 @@ struct KvAttnArgs {
   const int32_t* q_start;    // [B + 1], or null: query b is sequence b's
   const uint16_t* T;         // bf16 [kv][D/G][G][G] or null
   uint16_t* out;             // bf16 [n][kv * group][D]
-  KvJoin* join;              // [1 + 2 runs]
+  KvJoin* join;              // [1 + items]
   float* part;               // [2 runs] pieces
   int B, n, kv, group, D, page_log2, width, pages;
   int window;                // 0: none
   float scale;               // of the scores, times log2 e
-  int workgroups, runs;      // as in KvPlan
+  int items, workgroups, runs;  // as in KvPlan
 };
 
 // How a call is cut: columns per workgroup, and the pieces that the device aims at.
@@ -72,6 +71,13 @@ constexpr int kv_columns(int shape, int D) { return 16 * kv_tiles(shape, D) * (s
 // Workgroups that the chip holds at a time, by the kernels' registers (INT4's scales take some).
 constexpr int kv_resident(int shape, int D, int fmt) {
   return shape != kKvNarrow || D > 128 ? 512 : D == 128 ? (fmt == 2 ? 512 : 768) : fmt == 2 ? 768 : 1024;
+}
+
+// Workgroups per CU that the registers are cut for: as many as the units are shared out over, and
+// for two tiles of narrow heads a third one, since items' last pieces come on top of them
+// (16 sequences of up to 4000 tokens, 16 heads of 64, 20 columns: 24.8 us and 28.9).
+constexpr int kv_per_cu(int shape, int D, int fmt) {
+  return shape == kKvWide && D == 64 && fmt != 2 ? 3 : kv_resident(shape, D, fmt) / 256;
 }
 
 struct KvPlan {
@@ -97,12 +103,17 @@ inline KvPlan kv_plan(int fmt, int64_t B, int64_t n, int64_t kv, int64_t group, 
   return p;
 }
 
+constexpr int kKvJoins = 1024;  // items whose pieces are joined side by side, and
+constexpr int kKvFill = 2048;   // workgroups that do it, where their columns allow
+
 // Floats of one piece of an item: maxima, sums, results.
 inline int64_t kv_piece(int shape, int D) { return (int64_t)kv_columns(shape, D) * (D + 2); }
+// Bytes of the workspace in front of the pieces.
+inline int64_t kv_join_bytes(const KvPlan& p) { return (1 + p.items) * (int64_t)sizeof(KvJoin); }
 // Cut into pieces of a share, an item has less than 2 units / share of them, so all items together
 // less than 2 runs; cut by runs, every run has at most two pieces of items that are not whole.
 inline int64_t kv_workspace(const KvPlan& p, int D) {
-  return p.runs ? (1 + 2 * (int64_t)p.runs) * (int64_t)sizeof(KvJoin) + 2 * (int64_t)p.runs * 4 * kv_piece(p.shape, D) : 0;
+  return p.runs ? kv_join_bytes(p) + 2 * (int64_t)p.runs * 4 * kv_piece(p.shape, D) : 0;
 }
 
 hipError_t launch_kv4_attention_mx(const KvAttnArgs& a, int shape, hipStream_t s);

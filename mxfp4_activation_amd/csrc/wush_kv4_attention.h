@@ -144,34 +144,36 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // What a sequence and key head's items come to in units, all together and at most, and
-// cut for a share of units: in pieces, and in pieces of items that have several.
+// cut for a share of units: in pieces, in items that have several, and in pieces of those.
 struct Load {
-  int units, items, most, pieces, cut;
+  int units, items, most, pieces, several, cut;
 };
 template <int NC>
 __device__ __forceinline__ Load load_of(const KvAttnArgs& a, const Seq& s, int share) {
-  Load l = {0, items_of<NC>(a, s), 0, 0, 0};
+  Load l = {0, items_of<NC>(a, s), 0, 0, 0, 0};
   for (int t = 0; t < l.items; ++t) {
     const int u = units_of<NC>(a, s, t);
     const int p = (u - 1) / share + 1;
     l.units += u;
     l.most = l.most > u ? l.most : u;
     l.pieces += p;
+    l.several += p > 1;
     l.cut += p > 1 ? p : 0;
   }
   return l;
 }
 
 // A piece: sequence, key head, item, units of the item, of it from `off` on `take`; its place
-// in the workspace; how many there are of the item, and which one it is.
+// in the workspace; how many there are of the item, and which one it is; the item's place
+// among those with several.
 struct Place {
-  int b, h, t, units, off, take, slot, pieces, index;
+  int b, h, t, units, off, take, slot, pieces, index, rank;
   Seq s;
 };
 
 struct PlanLds {
   int sums[3][4];
-  int b, pieces, cut, per_head, cut_per_head;
+  int b, pieces, several, cut, per_head, several_per_head, cut_per_head;
   Seq s;
   Place at;  // of a run's piece, while the waves are at it
   int left;
@@ -191,14 +193,20 @@ struct Shares {
   int total;  // units, by runs
 };
 
-// Items are taken whole where nothing may be cut, and where there are enough of about the same
-// length: the longest times the rounds of them is at most 1.1 times the mean load.  (Two
-// prompts of 1000 queries behind 16384 tokens, 456 items for 512 places, 1.17 times: 533 us
-// whole, 497 by runs, 22 of them for joining 60 MB of pieces.)    Short shares keep to one item, since a second one costs
-// a second start: 48 sequences of up to 8192 tokens, 3 units each, 27.5 us by runs and 25.7
-// by pieces.  Long ones are better equal: 16 sequences of up to 131072, 105 units, 341 and 379.
+// Items are taken whole where nothing may be cut, and where that takes no longer: the longest
+// times the rounds of them is at most 1.1 times the mean load, and for few columns the pieces'
+// meeting, as long as 6 units, more.  (33 sequences, 16 heads, windows of 1000 tokens, 8 or 9
+// units: 15.9 us whole, 18.3 in two pieces each.  Two prompts of 1000 queries behind 16384
+// tokens, 456 items for 512 places, 1.17 times the mean: 533 us whole, 497 by runs.)
+// A share is what lets all pieces be there at once, but 4 units before it is a second
+// workgroup on a CU (8 sequences of 1000 tokens, 16 heads: 10.6 us in shares of 4, 13.4 of 1).
+// Short shares keep to one item, since a second one costs a second start: 48 sequences of up
+// to 8192 tokens, 7 units each, 27.5 us by runs and 25.7 by pieces.  Long ones are better
+// equal: 16 sequences of up to 131072, 105 units, 341 and 379.
 constexpr int kRunUnits = 12;
-template <int NC>
+constexpr float kJoinUnits = 6.0f;
+constexpr int kAloneUnits = 4;
+template <int NC, int SHAPE>
 __device__ __forceinline__ Shares shares_of(const KvAttnArgs& a, PlanLds& l, const Seq& first) {
   Shares r = {INT32_MAX, false, 0};
   if (a.runs == 0) return r;
@@ -232,23 +240,31 @@ __device__ __forceinline__ Shares shares_of(const KvAttnArgs& a, PlanLds& l, con
     most = uniform(most);
     __syncthreads();
   }
-  if ((float)most * (float)((items + a.runs - 1) / a.runs) * (float)a.runs <= 1.1f * (float)units) return r;
-  r.share = units > a.runs ? (units - 1) / a.runs + 1 : 1;
+  // (More only where q_start does not ascend: the workspace has no room for them.)
+  if (items > a.items) return r;
+  const float meeting = SHAPE == kKvPrompt ? 0.0f : kJoinUnits * (float)a.runs;
+  if ((float)most * (float)((items + a.runs - 1) / a.runs) * (float)a.runs <= 1.1f * (float)units + meeting) return r;
+  r.share = (units - 1) / a.runs + 1;
+  if (SHAPE != kKvPrompt) {
+    const int alone = (units - 1) / 256 + 1, least = alone < kAloneUnits ? alone : kAloneUnits;
+    r.share = r.share < least ? least : r.share;
+  }
   r.by_runs = r.share >= kRunUnits;
   r.total = units;
   return r;
 }
 
 // Piece number w of all, with `share` units at most, for the whole workgroup; false if there
-// are not so many.  `total`: pieces of items that have several (for w = 0, or few sequences).
+// are not so many.  `total`: items that have several (for w = 0, or few sequences).
 template <int NC>
 __device__ __forceinline__ bool find(const KvAttnArgs& a, PlanLds& l, const Seq& first, int share, int w, Place& p, int& total) {
-  int pieces, cut, per_head, cut_per_head;
+  int pieces, several, cut, per_head, several_per_head, cut_per_head;
   total = 0;
   if (few(a)) {
     const Load o = load_of<NC>(a, first, share);
-    const int own = a.kv * o.pieces, many = a.kv * o.cut, upto = wave_scan(own), many_upto = wave_scan(many);
-    total = __builtin_amdgcn_readlane(many_upto, 63);
+    const int own = a.kv * o.pieces, items = a.kv * o.several, many = a.kv * o.cut;
+    const int upto = wave_scan(own), items_upto = wave_scan(items), many_upto = wave_scan(many);
+    total = __builtin_amdgcn_readlane(items_upto, 63);
     if (w >= __builtin_amdgcn_readlane(upto, 63)) return false;
     const int b = __builtin_ctzll(__ballot(w < upto));
     p.b = b;
@@ -257,39 +273,46 @@ __device__ __forceinline__ bool find(const KvAttnArgs& a, PlanLds& l, const Seq&
     p.s.len = __builtin_amdgcn_readlane(first.len, b);
     p.s.bad = __builtin_amdgcn_readlane(first.bad, b);
     pieces = __builtin_amdgcn_readlane(upto - own, b);
+    several = __builtin_amdgcn_readlane(items_upto - items, b);
     cut = __builtin_amdgcn_readlane(many_upto - many, b);
     per_head = __builtin_amdgcn_readlane(o.pieces, b);
+    several_per_head = __builtin_amdgcn_readlane(o.several, b);
     cut_per_head = __builtin_amdgcn_readlane(o.cut, b);
   } else {
-    int base = 0;
+    int base = 0, cut_base = 0;
     bool found = false;
     for (int c = 0; c < a.B; c += kThreads) {
       const int b = c + (int)threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
       const Seq s = c == 0 ? first : seq_or_none(a, b);
       const Load o = load_of<NC>(a, s, share);
-      const int own = a.kv * o.pieces, many = a.kv * o.cut;
-      const int upto = wave_scan(own), many_upto = wave_scan(many);
+      const int own = a.kv * o.pieces, items = a.kv * o.several, many = a.kv * o.cut;
+      const int upto = wave_scan(own), items_upto = wave_scan(items), many_upto = wave_scan(many);
       __syncthreads();
       if (lane == 63) {
         l.sums[0][wave] = upto;
         l.sums[1][wave] = many_upto;
+        l.sums[2][wave] = items_upto;
       }
       __syncthreads();
-      int before = base + upto - own, many_before = total + many_upto - many;
+      int before = base + upto - own, many_before = cut_base + many_upto - many, items_before = total + items_upto - items;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < wave) {
           before += l.sums[0][i];
           many_before += l.sums[1][i];
+          items_before += l.sums[2][i];
         }
         base += l.sums[0][i];
-        total += l.sums[1][i];
+        cut_base += l.sums[1][i];
+        total += l.sums[2][i];
       }
       if (w >= before && w - before < own) {
         l.b = b;
         l.pieces = before;
+        l.several = items_before;
         l.cut = many_before;
         l.per_head = o.pieces;
+        l.several_per_head = o.several;
         l.cut_per_head = o.cut;
         l.s = s;
       }
@@ -306,19 +329,23 @@ __device__ __forceinline__ bool find(const KvAttnArgs& a, PlanLds& l, const Seq&
     p.s.len = uniform(l.s.len);
     p.s.bad = uniform(l.s.bad);
     pieces = uniform(l.pieces);
+    several = uniform(l.several);
     cut = uniform(l.cut);
     per_head = uniform(l.per_head);
+    several_per_head = uniform(l.several_per_head);
     cut_per_head = uniform(l.cut_per_head);
   }
   const int at = w - pieces;
   p.h = at / per_head;
   p.index = at - p.h * per_head;
+  p.rank = several + p.h * several_per_head;
   p.slot = cut + p.h * cut_per_head;
   for (p.t = 0;; ++p.t) {
     p.units = units_of<NC>(a, p.s, p.t);
     p.pieces = (p.units - 1) / share + 1;
     if (p.index < p.pieces) break;
     p.index -= p.pieces;
+    p.rank += p.pieces > 1;
     p.slot += p.pieces > 1 ? p.pieces : 0;
   }
   p.slot += p.index;
@@ -332,6 +359,7 @@ __device__ __forceinline__ bool find(const KvAttnArgs& a, PlanLds& l, const Seq&
 // The item behind p's.
 template <int NC>
 __device__ __forceinline__ void next_item(const KvAttnArgs& a, Place& p) {
+  p.rank += p.units > 1;
   if (++p.t == items_of<NC>(a, p.s)) {
     p.t = 0;
     if (++p.h == a.kv) {
@@ -1223,40 +1251,40 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
 }
 
 template <int FMT, int D, int SHAPE, int PLANES>
-__global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D, FMT) / 256) void kv4_attention_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(kThreads, kv_per_cu(SHAPE, D, FMT)) void kv4_attention_kernel(KvAttnArgs a) {
   constexpr int NC = kv_columns(SHAPE, D);
   extern __shared__ __attribute__((aligned(16))) float lds[];
   __shared__ float stat[2][4][32];
   __shared__ PlanLds plan;
   const int w = blockIdx.x;
   const Seq first = seq_or_none(a, place_of(a));
-  const Shares s = shares_of<NC>(a, plan, first);
+  const Shares s = shares_of<NC, SHAPE>(a, plan, first);
   Place at;
-  int cut, left = 0;  // units left of the run
+  bool any;
+  int several = 0, left = 0;  // units left of the run
   if (s.by_runs) {
     if (w >= a.runs) return;
     const int64_t begin = (int64_t)w * s.share;
     left = (int)(begin >= s.total ? 0 : s.total - begin < s.share ? s.total - begin : s.share);
-    if (threadIdx.x == 0) {
-      if (w == 0) a.join[0].pieces = 2 * a.runs;
-      a.join[1 + 2 * w].pieces = a.join[2 + 2 * w].pieces = 0;
-    }
     // A unit is a piece of one.
-    if (left == 0 || !find<NC>(a, plan, first, 1, (int)begin, at, cut)) return;
+    any = left > 0 && find<NC>(a, plan, first, 1, (int)begin, at, several);
     at.slot = 2 * w;
   } else {
-    const bool any = find<NC>(a, plan, first, s.share, w, at, cut);
-    if (w == 0 && threadIdx.x == 0 && a.runs > 0) a.join[0].pieces = cut;
-    if (!any) return;
+    any = find<NC>(a, plan, first, s.share, w, at, several);
   }
+  // How many there are to join is written also where there is nothing at all.
+  if (w == 0 && threadIdx.x == 0 && a.runs > 0) a.join[0].pieces = several;
+  if (!any) return;
   for (;;) {
-    KvJoin join = {at.index == 0 ? at.pieces : 0, at.slot + 1, 1, 0, 0, at.s.start, at.h, 0};
+    KvJoin join = {at.pieces, at.slot, at.slot + 1, 1, 0, 0, at.s.start, at.h};
+    bool listed = at.pieces > 1;
     if (s.by_runs) {
       at.take = at.units - at.off < left ? at.units - at.off : left;
       left -= at.take;
       // The rest of the item is at the beginnings of the runs behind.
       const int rest = at.units - at.off - at.take;
-      join = KvJoin{at.off == 0 && rest > 0 ? (rest - 1) / s.share + 2 : 0, 2 * w + 2, 2, 0, 0, at.s.start, at.h, 0};
+      join = KvJoin{rest > 0 ? (rest - 1) / s.share + 2 : 0, at.slot, 2 * w + 2, 2, 0, 0, at.s.start, at.h};
+      listed = at.units > 1;
     }
     const int i0 = at.t * NC / a.group, il = (at.t * NC + NC - 1) / a.group, cols = at.s.count * a.group - at.t * NC;
     join.cols = cols < NC ? cols : NC;
@@ -1272,7 +1300,7 @@ __global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D, FMT) / 256) void kv
     p.hi = all.hi < to ? all.hi : (int)to;
     p.whole = at.take == at.units;
     p.part = p.whole ? nullptr : a.part + (int64_t)at.slot * (NC * (D + 2));
-    if (!p.whole && threadIdx.x == 0) a.join[1 + at.slot] = join;
+    if (listed && at.off == 0 && threadIdx.x == 0) a.join[1 + at.rank] = join;
     // (Kept here rather than in registers.)
     if (threadIdx.x == 0) {
       plan.at = at;
@@ -1289,6 +1317,8 @@ __global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D, FMT) / 256) void kv
     at.b = uniform(plan.at.b);
     at.h = uniform(plan.at.h);
     at.t = uniform(plan.at.t);
+    at.units = uniform(plan.at.units);
+    at.rank = uniform(plan.at.rank);
     at.s.start = uniform(plan.at.s.start);
     at.s.count = uniform(plan.at.s.count);
     at.s.len = uniform(plan.at.s.len);
@@ -1300,82 +1330,92 @@ __global__ __launch_bounds__(kThreads, kv_resident(SHAPE, D, FMT) / 256) void kv
   }
 }
 
-// The pieces of the item whose first one is in place blockIdx.x, if that is one.  D / 4 lanes
-// take a row's channels, so that a workgroup reads 1024 / D rows at once: columns where there
-// are few pieces, pieces of one column where there are many.
+// The pieces of the items that have several: an item per blockIdx.x, its columns shared out
+// over blockIdx.y.  D / 4 lanes take a row's channels, so that a workgroup reads 1024 / D rows
+// at once: columns where there are few pieces, pieces of one column where there are many.
 constexpr int kFewPieces = 4;
 template <int D, int SHAPE>
 __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv, float factor) {
   constexpr int NC = kv_columns(SHAPE, D), kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  __shared__ float wave_m[4], wave_l[kAtOnce];
+  __shared__ float row_m[kAtOnce], row_l[kAtOnce];
   __shared__ __attribute__((aligned(16))) float sums[kAtOnce][D];
-  if ((int)blockIdx.x >= a.join[0].pieces) return;
-  const KvJoin j = a.join[1 + blockIdx.x];
-  if (j.pieces == 0) return;
   const int tid = threadIdx.x, mine = tid / kLanes, ch = tid % kLanes * 4;
   constexpr int64_t kPiece = NC * (D + 2);
   const float vg = nv ? a.v_gs[0] : factor;
-  const float* base = a.part + (int64_t)blockIdx.x * kPiece;
-  auto piece = [&](int i) { return i == 0 ? base : a.part + ((int64_t)j.next + (int64_t)(i - 1) * j.step) * kPiece; };
-  auto out = [&](int c) {
-    const int col = j.col0 + c, i = col / a.group;
-    return a.out + ((int64_t)(j.start + i) * a.kv * a.group + j.head * a.group + col - i * a.group) * D;
-  };
-  if (j.pieces <= kFewPieces) {
-    for (int c = (int)blockIdx.y * kAtOnce + mine; c < j.cols; c += (int)gridDim.y * kAtOnce) {
-      float m[kFewPieces], l[kFewPieces], M = -FLT_MAX, L = 0.0f;
-      f32x4 x[kFewPieces], v = {0, 0, 0, 0};
+  // (Both on their way at once.)
+  KvJoin j = a.join[1 + blockIdx.x];
+  const int count = a.join[0].pieces;
+  for (int item = blockIdx.x; item < count;) {
+    auto piece = [&](int i) {
+      return a.part + (i == 0 ? (int64_t)j.first : (int64_t)j.next + (int64_t)(i - 1) * j.step) * kPiece;
+    };
+    auto out = [&](int c) {
+      const int col = j.col0 + c, i = col / a.group;
+      return a.out + ((int64_t)(j.start + i) * a.kv * a.group + j.head * a.group + col - i * a.group) * D;
+    };
+    // `several` of them from number i0 on, `by` apart, all on their way at once.
+    auto add = [&](int c, int i0, int by, float& M, float& L, f32x4& v) {
+      float m[kFewPieces], l[kFewPieces], next = M;
+      f32x4 x[kFewPieces];
 #pragma unroll
-      for (int i = 0; i < kFewPieces; ++i) {
-        const float* p = piece(i < j.pieces ? i : 0);
-        m[i] = i < j.pieces ? p[c] : -FLT_MAX;
-        l[i] = i < j.pieces ? p[NC + c] : 0.0f;
-        x[i] = *reinterpret_cast<const f32x4*>(p + 2 * NC + c * D + ch);
-        M = fmaxf(M, m[i]);
+      for (int u = 0; u < kFewPieces; ++u) {
+        const int i = i0 + u * by;
+        const float* p = piece(i < j.pieces ? i : i0);
+        m[u] = p[c];
+        l[u] = p[NC + c];
+        x[u] = *reinterpret_cast<const f32x4*>(p + 2 * NC + c * D + ch);
+        next = fmaxf(next, m[u]);
       }
+      const float f0 = __builtin_amdgcn_exp2f(M - next);
+      M = next;
+      L *= f0;
+      v *= f0;
 #pragma unroll
-      for (int i = 0; i < kFewPieces; ++i) {
-        const float f = i < j.pieces ? __builtin_amdgcn_exp2f(m[i] - M) : 0.0f;
-        L = __builtin_fmaf(l[i], f, L);
+      for (int u = 0; u < kFewPieces; ++u) {
+        const bool there = i0 + u * by < j.pieces;
+        const float f = __builtin_amdgcn_exp2f(m[u] - M);
+        L = there ? __builtin_fmaf(l[u], f, L) : L;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = i < j.pieces ? __builtin_fmaf(x[i][e], f, v[e]) : v[e];
+        for (int e = 0; e < 4; ++e) v[e] = there ? __builtin_fmaf(x[u][e], f, v[e]) : v[e];
       }
-      const float g = L != 0.0f ? vg / L : 0.0f;
-      *reinterpret_cast<u32x2*>(out(c) + ch) = u32x2{pack(cvt_bf16(v[0] * g, v[1] * g)), pack(cvt_bf16(v[2] * g, v[3] * g))};
-    }
-    return;
-  }
-  for (int c = blockIdx.y; c < j.cols; c += gridDim.y) {
-    float M = -FLT_MAX;
-    for (int i = tid; i < j.pieces; i += kThreads) M = fmaxf(M, piece(i)[c]);
-    M = wave_max(M);
-    if ((tid & 63) == 0) wave_m[tid >> 6] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(wave_m[0], wave_m[1]), fmaxf(wave_m[2], wave_m[3]));
-    float L = 0.0f;
-    f32x4 v = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int i = mine; i < j.pieces; i += kAtOnce) {
-      const float* p = piece(i);
-      const float f = __builtin_amdgcn_exp2f(p[c] - M);
-      const f32x4 x = *reinterpret_cast<const f32x4*>(p + 2 * NC + c * D + ch);
-      L = __builtin_fmaf(p[NC + c], f, L);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(x[e], f, v[e]);
-    }
-    *reinterpret_cast<f32x4*>(&sums[mine][ch]) = v;
-    if (ch == 0) wave_l[mine] = L;
-    __syncthreads();
-    if (tid < D) {
-      float sum = 0.0f, all = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        sum += sums[i][tid];
-        all += wave_l[i];
+    };
+    if (j.pieces > 1 && j.pieces <= kFewPieces) {
+      for (int c = (int)blockIdx.y * kAtOnce + mine; c < j.cols; c += (int)gridDim.y * kAtOnce) {
+        float M = -FLT_MAX, L = 0.0f;
+        f32x4 v = {0, 0, 0, 0};
+        add(c, 0, 1, M, L, v);
+        const float g = L != 0.0f ? vg / L : 0.0f;
+        *reinterpret_cast<u32x2*>(out(c) + ch) = u32x2{pack(cvt_bf16(v[0] * g, v[1] * g)), pack(cvt_bf16(v[2] * g, v[3] * g))};
       }
-      out(c)[tid] = __builtin_bit_cast(uint16_t, (__bf16)(all != 0.0f ? sum * (vg / all) : 0.0f));
+    } else if (j.pieces > 1) {
+      for (int c = blockIdx.y; c < j.cols; c += gridDim.y) {
+        float M = -FLT_MAX, L = 0.0f;
+        f32x4 v = {0, 0, 0, 0};
+        for (int i = mine; i < j.pieces; i += kFewPieces * kAtOnce) add(c, i, kAtOnce, M, L, v);
+        *reinterpret_cast<f32x4*>(&sums[mine][ch]) = v;
+        if (ch == 0) {
+          row_m[mine] = M;
+          row_l[mine] = L;
+        }
+        __syncthreads();
+        if (tid < D) {
+          float sum = 0.0f, all = 0.0f;
+          M = row_m[0];
+#pragma unroll
+          for (int i = 1; i < kAtOnce; ++i) M = fmaxf(M, row_m[i]);
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) {
+            const float f = __builtin_amdgcn_exp2f(row_m[i] - M);
+            sum = __builtin_fmaf(sums[i][tid], f, sum);
+            all = __builtin_fmaf(row_l[i], f, all);
+          }
+          out(c)[tid] = __builtin_bit_cast(uint16_t, (__bf16)(all != 0.0f ? sum * (vg / all) : 0.0f));
+        }
+        __syncthreads();
+      }
     }
-    __syncthreads();
+    item += gridDim.x;
+    if (item < count) j = a.join[1 + item];
   }
 }
 
@@ -1384,8 +1424,14 @@ hipError_t go(const KvAttnArgs& a, hipStream_t s) {
   hipError_t e = launch_lds(kv4_attention_kernel<FMT, D, SHAPE, PLANES>, dim3(a.workgroups), kThreads,
                             4 * lds_floats<FMT, D, SHAPE, PLANES>(), s, a);
   if (e != hipSuccess || a.runs == 0) return e;
-  hipLaunchKernelGGL((kv4_join_kernel<D, SHAPE>), dim3(2 * a.runs, kv_columns(SHAPE, D) / 4), dim3(kThreads), 0, s, a,
-                     FMT == kNV ? 1 : 0, 1.0f / kVFactor<FMT>);
+  const int64_t columns = (int64_t)a.n * a.group / (a.B < a.n ? a.B : a.n);  // of a sequence, on average
+  const int64_t most = kv_columns(SHAPE, D);
+  // Enough workgroups to fill the chip, but at least as many as a pass over the columns takes
+  // and at most one each.
+  const int x = a.items < kKvJoins ? a.items : kKvJoins, cols = (int)(columns < most ? columns : most);
+  const int pass = (cols * D + 4 * kThreads - 1) / (4 * kThreads), fill = (kKvFill + x - 1) / x;
+  const int y = fill < pass ? pass : fill < cols ? fill : cols;
+  hipLaunchKernelGGL((kv4_join_kernel<D, SHAPE>), dim3(x, y), dim3(kThreads), 0, s, a, FMT == kNV ? 1 : 0, 1.0f / kVFactor<FMT>);
   return hipGetLastError();
 }
 

@@ -203,7 +203,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.T = static_cast<const uint16_t*>(T_q);
   a.out = static_cast<uint16_t*>(out);
   a.join = static_cast<wush::KvJoin*>(workspace);
-  a.part = plan.runs ? reinterpret_cast<float*>(a.join + 1 + 2 * (int64_t)plan.runs) : nullptr;
+  a.part = plan.runs ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + wush::kv_join_bytes(plan)) : nullptr;
   a.B = (int)B;
   a.n = (int)n;
   a.kv = (int)heads;
@@ -216,6 +216,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.scale = (float)(scale * 1.4426950408889634);  // the kernels take powers of two
   a.workgroups = (int)plan.workgroups;
   a.runs = plan.runs;
+  a.items = (int)plan.items;
   if (fmt == wush::kMXFP4) return launched(wush::launch_kv4_attention_mx(a, plan.shape, stream));
   if (fmt == wush::kNVFP4) return launched(wush::launch_kv4_attention_nv(a, plan.shape, stream));
   return launched(wush::launch_kv4_attention_int(a, plan.shape, stream));

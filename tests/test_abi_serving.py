@@ -144,7 +144,7 @@ def test_pieces_fit_their_workspace():
     """The rules by which the kernels cut items into pieces, restated, over random batches:
     all pieces have a workgroup, and those of cut items a place in the workspace."""
     lib, rng = wush.load(), random.Random(5)
-    unit, run_units = 128, 12
+    unit, run_units, join_units, alone_units = 128, 12, 6, 4
     for _ in range(400):
         B, kv, group, D, page = rng.choice((1, 3, 40, 200)), rng.choice((1, 8)), rng.choice((1, 4, 7)), 128, 16
         most = rng.choice((1, 3, 30, 500))
@@ -161,8 +161,8 @@ def test_pieces_fit_their_workspace():
         items = (n * group // nc + min(B, n)) * kv
         ws = lib.wush_kv4_attention_workspace(0, B, n, kv * group, kv, D, page, width)
         piece = 4 * nc * (D + 2)
-        runs = (ws - 32) // (2 * (32 + piece))
-        assert runs > 0 and ws == 32 + 2 * runs * (32 + piece)
+        runs = (ws - 32 * (1 + items)) // (2 * piece)
+        assert runs > 0 and ws == 32 * (1 + items) + 2 * runs * piece
         all_units = []
         for c, L in zip(counts, lengths):
             for t in range(-(-c * group // nc)):
@@ -171,10 +171,11 @@ def test_pieces_fit_their_workspace():
                 all_units += [-(-hi // unit) - lo // unit if hi > lo else 1] * kv
         assert len(all_units) <= items
         total = sum(all_units)
-        if max(all_units) * -(-len(all_units) // runs) * runs <= 1.1 * total:
+        meeting = 0 if shape == 2 else join_units * runs
+        if max(all_units) * -(-len(all_units) // runs) * runs <= 1.1 * total + meeting:
             assert len(all_units) <= items + runs
             continue
-        share = max(1, -(-total // runs))
+        share = max(-(-total // runs), 1 if shape == 2 else min(alone_units, -(-total // 256)))
         if share >= run_units:
             assert share * runs >= total
             continue

@@ -323,3 +323,10 @@ def test_int4_value_scales_of_every_size(lo, hi, count):
     b.v[1][:] = rng.integers(lo, hi, size=b.v[1].shape)
     got = b.check()
     assert np.all(np.isfinite(got))
+
+
+def test_more_items_to_join_than_join_at_once():
+    """1120 items of 12 units by runs of 14: most of them are in two pieces."""
+    rng = np.random.default_rng(77)
+    lengths = rng.integers(1420, 1537, size=140)
+    Batch(rng, "mxfp4", 64, 8, 1, 16, lengths, [1] * 140).check()
