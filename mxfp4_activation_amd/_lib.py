@@ -93,7 +93,7 @@ def load() -> ctypes.CDLL:
 
 
 _NATIVE = ("wush_kv4_append", "wush_kv4_attention", "wush_kv4_attention_workspace", "wush_linear_w4_lora",
-           "wush_linear_w4_lora_workspace", "wush_adjust_logits")
+           "wush_linear_w4_lora_workspace", "wush_adjust_logits", "wush_dequant")
 _binding = False  # not looked for yet
 
 

@@ -1,5 +1,5 @@
-// The wrappers of the entries around the 4-bit products (kv4.py, decode.py) in native
-// code, for the calls on one token, whose time is the host's: the same checks,
+// The wrappers of the entries around the 4-bit products (kv4.py, decode.py) and of dequant, by
+// which a cache is read back, in native code, for the calls on one token, whose time is the host's: the same checks,
 // outputs and workspaces, in about a microsecond where Python takes ten.
 //
 // Every function returns its result; an int, the status of a library call that
@@ -25,6 +25,7 @@ decltype(&wush_kv4_attention_workspace) f_attention_workspace;
 decltype(&wush_linear_w4_lora) f_lora;
 decltype(&wush_linear_w4_lora_workspace) f_lora_workspace;
 decltype(&wush_adjust_logits) f_adjust;
+decltype(&wush_dequant) f_dequant;
 
 using at::ScalarType;
 using at::Tensor;
@@ -271,6 +272,24 @@ PyObject* adjust(PyObject*, PyObject* const* a, Py_ssize_t count) {
   return given ? answer(st, a[9]) : answer(st, fresh);
 }
 
+// (fmt, codes, scales, global_scale, out)
+PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  Call c;
+  if (count != 5) Py_RETURN_NONE;
+  const int fmt = c.format(a[0]);
+  const Tensor* codes = c.first(a[1], at::kByte, 2);
+  if (!c.ok || !codes->is_contiguous()) Py_RETURN_NONE;
+  const int64_t M = codes->size(0), K = codes->size(1) * 2;
+  const void* scales = c.address(a[2], scale_type(fmt), {M, K / group_of(fmt)});
+  const float* g = c.global(a[3], fmt);
+  void* given = c.maybe(a[4], at::kFloat, {M, K});
+  if (!c.ok) Py_RETURN_NONE;
+  const Tensor out = given ? Tensor() : at::empty({M, K}, codes->options().dtype(at::kFloat));
+  const wush_status st = f_dequant(fmt, codes->data_ptr(), scales, g, M, K, static_cast<float*>(given ? given : out.data_ptr()),
+                                   stream_of(c.device));
+  return given ? answer(st, a[4]) : answer(st, out);
+}
+
 // Functions above, with C++ exceptions (an allocation that fails, say) as Python's.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t count) {
@@ -290,13 +309,15 @@ PyObject* bind(PyObject*, PyObject* entries) {
   };
   if (take("wush_kv4_append", f_append) && take("wush_kv4_attention", f_attention) &&
       take("wush_kv4_attention_workspace", f_attention_workspace) && take("wush_linear_w4_lora", f_lora) &&
-      take("wush_linear_w4_lora_workspace", f_lora_workspace) && take("wush_adjust_logits", f_adjust))
+      take("wush_linear_w4_lora_workspace", f_lora_workspace) && take("wush_adjust_logits", f_adjust) &&
+      take("wush_dequant", f_dequant))
     Py_RETURN_NONE;
   return nullptr;
 }
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(append), FAST(attention), FAST(lora), FAST(adjust), {"bind", bind, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(append), FAST(attention), FAST(lora), FAST(adjust), FAST(dequant),
+                         {"bind", bind, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -127,6 +127,13 @@ def build_transforms(W: torch.Tensor, Xcal: torch.Tensor, G: int, damp: float = 
 def dequant(fmt: str, codes: torch.Tensor, scales: torch.Tensor, global_scale: Optional[torch.Tensor] = None,
             out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """fp32 values of quantized rows (codes [M][K/2], scales [M][K/G])."""
+    native = _lib.binding()
+    if native is not None:
+        r = native.dequant(fmt, codes, scales, global_scale, out)
+        if r is not None:
+            if type(r) is int:
+                _lib.check(r, "wush_dequant")
+            return r
     G = _G[fmt]
     if codes.dtype != torch.uint8 or not codes.is_cuda or not codes.is_contiguous() or codes.dim() != 2:
         raise ValueError("codes must be a contiguous 2-D uint8 device tensor")

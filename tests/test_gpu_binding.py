@@ -82,6 +82,11 @@ def test_same_results(both, fmt, T):
 
     for p, q in zip(*both(append)):
         assert p is None or torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+    rows = lambda t: t.view(-1, t.shape[-1])  # noqa: E731
+    x, y = both(lambda: wush.dequant(fmt, rows(cache.k_codes), rows(cache.k_scales), cache.k_global))
+    assert x.dtype == torch.float32 and x.shape[1] == 128 and torch.equal(x, y)
+    x, y = both(lambda: wush.dequant(fmt, rows(cache.v_codes), rows(cache.v_scales), cache.v_global, out=y))
+    assert x is y
     lora = Lora(fmt, 12, 100, 256, 16, 3, T=T).args()
     for dtype in (torch.bfloat16, torch.float32):
         x, y = both(lambda: wush.linear_w4_lora(**lora, out_dtype=dtype))
@@ -121,6 +126,10 @@ def test_same_refusals():
     with pytest.raises(wush.WushError, match="page"):
         wush.kv4_append("mxfp4", q[:, :2], q[:, :2], wush.kv4_cache("mxfp4", 4, 2, 24, 128),
                         torch.zeros(2, dtype=torch.int64, device="cuda"))
+    codes, scales = (t.view(-1, t.shape[-1]) for t in cache[:2])
+    for bad in (dict(scales=scales[1:]), dict(codes=codes[:, ::2]), dict(out=torch.empty(1, 128, device="cuda")), dict(fmt="nvfp4")):
+        with pytest.raises(ValueError, match="contiguous|shape|global_scale"):
+            wush.dequant(**{**dict(fmt="mxfp4", codes=codes, scales=scales), **bad})
     a = Lora("nvfp4", 3, 40, 64, 8, 2).args()
     with pytest.raises(ValueError, match="global_scale"):
         wush.linear_w4_lora(**{**a, "global_scale": None})
