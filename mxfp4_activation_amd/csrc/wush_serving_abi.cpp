@@ -64,7 +64,7 @@ LoraWorkspace lora_workspace(int64_t M, int64_t N, int64_t K, int64_t rank, bool
   LoraWorkspace w;
   w.h = 0;
   w.delta = round16(c * rank * 4);
-  w.planes = w.delta + (M > wush::kLoraTogether ? round16(c * N * 4) : 0);
+  w.planes = w.delta + (wush::lora_together(M, N, rank) ? 0 : round16(c * N * 4));
   w.total = w.planes + (transform ? 2 * terms_of(out_type) * c * K : 0);
   return w;
 }
@@ -288,7 +288,7 @@ wush_status wush_linear_w4_lora(int fmt, const void* X, int64_t ldx, const void*
   a.lora.B = static_cast<const uint16_t*>(B);
   a.lora.scale = adapter_scale;
   a.lora.h = reinterpret_cast<float*>(ws + w.h);
-  a.lora.delta = M > wush::kLoraTogether ? reinterpret_cast<float*>(ws + w.delta) : nullptr;
+  a.lora.delta = wush::lora_together(M, N, rank) ? nullptr : reinterpret_cast<float*>(ws + w.delta);
   a.lora.K = K;
   a.lora.E = adapters;
   a.lora.rank = (int)rank;

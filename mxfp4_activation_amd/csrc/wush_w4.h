@@ -31,7 +31,15 @@ struct SplitArgs {
 // Low-rank adapters of a batch: Y[m] += h[m] B[ids[m]]^T, h from launch_lora.  The product
 // takes what it adds from delta, which launch_lora_expand writes, or for a few tokens
 // forms it itself, which saves a launch.
-constexpr int kLoraTogether = 8;    // tokens up to which it does
+// One lane then reads a result's whole row of B, which is slower than a launch of its own made
+// for that where the rows are long or many.  N x rank, tokens: together, apart, us (MXFP4, K =
+// 4096, 40 adapters): 4096 x 16, 16: 12.8, 16.2; 24576 x 16, 32: 29.2, 34.2; 24576 x 16, 64: 49.5,
+// 50.0; 4096 x 32, 64: 18.3, 20.4; 24576 x 32, 16: 26.6, 27.7, and 32: 39.7, 37.8; 24576 x 64,
+// 8: 25.2, 26.0, and 16: 38.1, 34.4; 4096 x 64, 64: 24.6, 22.7; 4096 x 128, 1: 10.4, 11.6;
+// 4096 x 256, 1: 13.1, 12.4.  INT4 alike.
+inline bool lora_together(int64_t M, int64_t N, int64_t rank) {
+  return M <= 64 && rank <= (M <= 8 ? 128 : 32) && N * rank <= (3 << 22) / M;
+}
 constexpr int64_t kLoraChunk = 256;  // tokens that share a workspace
 struct LoraArgs {
   const uint16_t* X;   // bf16 [M], row stride ldx

@@ -227,11 +227,11 @@ static void lora() {
           const int64_t need = wush_linear_w4_lora_workspace(M, 40, 4 * G, 16, t, out), c = M < 256 ? M : 256;
           const int chunks = (int)((M + 255) / 256);
           g_lora_tokens = 0;
-          ACCEPT(call([&](Call& k) { k.M = M; k.out = out; k.T = t ? 11 * A : 0; }), chunks * (M > 8 ? 3 : 2));
+          ACCEPT(call([&](Call& k) { k.M = M; k.out = out; k.T = t ? 11 * A : 0; }), chunks * (M > 64 ? 3 : 2));
           EXPECT(g_lora_tokens == M, "tokens of the chunks");
           const uintptr_t h = (uintptr_t)g_last_lora.h, d = (uintptr_t)g_last_lora.delta, end = 10 * A + (uintptr_t)need;
           EXPECT(h == 10 * A && h + c * 16 * 4 <= (d ? d : end), "h");
-          EXPECT((M > 8) == (d != 0), "delta");
+          EXPECT((M > 64) == (d != 0), "delta");
           if (t) {
             const uintptr_t p = (uintptr_t)g_last_split.out;
             EXPECT(p % 16 == 0 && p >= (d ? d + c * 40 * 4 : h + c * 64) && p + (out ? 2 : 3) * c * 4 * G * 2 == end, "planes");
