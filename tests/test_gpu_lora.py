@@ -60,6 +60,9 @@ class Case:
     (1, 64, 256, 8, 1, False, "f32"), (1, 4096, 1024, 16, 3, False, "bf16"), (3, 77, 96, 24, 2, True, "f32"),
     (13, 500, 672, 64, 5, True, "bf16"), (33, 130, 2080, 16, 40, False, "f32"), (64, 1000, 512, 128, 7, True, "f32"),
     (70, 48, 256, 512, 2, False, "bf16"), (200, 33, 64, 8, 9, False, "f32"),
+    # added in the product, and just not
+    (64, 129, 256, 8, 3, False, "bf16"), (50, 300, 512, 32, 6, True, "f32"), (17, 65, 96, 24, 4, False, "f32"),
+    (9, 200, 128, 40, 3, False, "bf16"), (8, 70, 128, 128, 2, True, "f32"), (8, 70, 128, 136, 2, False, "bf16"),
 ])
 def test_lora(fmt, M, N, K, rank, E, T, out):
     import mxfp4_activation_amd as wush
