@@ -1021,10 +1021,10 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
 // they share what K and V become.  Per stage every wave expands 32 tokens (for D = 256 pairs
 // of waves K or V of them) into LDS, as the operands that all four then read; the next
 // stage's codes are on their way meanwhile.  Two chunks of 1000 queries of 32 heads behind 15000 to
-// 16384 tokens take 495 us with the joining: 928 TFLOP/s; matrix cores 37%, vector instructions
+// 16384 tokens take 490 us with the joining: 937 TFLOP/s; matrix cores 37%, vector instructions
 // 41% of the time, a quarter of the waves' cycles waiting.  (Each wave expanding for itself, in
 // registers, spends 136 of 263 instructions of a step on it: 640 us.  The next tile's scores
-// among this one's exponentials: 607, for registers; in this order 495.)
+// among this one's exponentials: 607, for registers.)
 template <int FMT, int D>
 constexpr int kStageTiles = D == 256 ? 2 : 4;
 template <int FMT, int D>
@@ -1182,6 +1182,10 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int ct = 0; ct < NQ; ++ct) s[u][ct] = f32x4{0, 0, 0, 0};
+    // A wave among its matrix instructions goes before one among its exponentials: the other way
+    // round, or without, the former wait for the latter (INT4 645 us and 706 above, MXFP4 490 and 497,
+    // heads of 256 627 and 647).
+    __builtin_amdgcn_s_setprio(1);
     each<KJ>([&](auto jc) {
       constexpr int j = jc;
 #pragma unroll
@@ -1207,15 +1211,18 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
         }
       }
     });
+    __builtin_amdgcn_s_setprio(0);
     if (!(t0 >= clear_from && t0 + kTile <= clear_to)) mask_scores<NQ>(s, t0, lo, pos, a.window);
     u32x4 pf[NQ];
     softmax_step<FMT, NQ, CH>(s, scale, m, l, acc, pf);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const u32x4 vf = *operand(tile, 2 * KJ + j);
 #pragma unroll
       for (int ct = 0; ct < NQ; ++ct) acc[j][ct] = add_pv<FMT>(vf, pf[ct], acc[j][ct]);
     }
+    __builtin_amdgcn_s_setprio(0);
   };
   for (int k = 0; k < stages; ++k) {
     expand_tile(k);
