@@ -330,3 +330,13 @@ def test_more_items_to_join_than_join_at_once():
     rng = np.random.default_rng(77)
     lengths = rng.integers(1420, 1537, size=140)
     Batch(rng, "mxfp4", 64, 8, 1, 16, lengths, [1] * 140).check()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_many_sequences_of_every_length(fmt):
+    """More sequences than a wave has lanes, some without tokens or queries, a few cut into pieces."""
+    rng = np.random.default_rng(101)
+    lengths = np.where(rng.random(300) < 0.1, rng.integers(1000, 9000, size=300), rng.integers(0, 300, size=300))
+    counts = rng.integers(0, 4, size=300)
+    Batch(rng, fmt, 64, 2, 2, 32, lengths, counts).check()
+    Batch(rng, fmt, 128, 1, 4, 16, lengths[:70], np.where(counts[:70] == 3, 40, counts[:70])).check(window=700)
