@@ -401,10 +401,10 @@ struct Offsets {
 };
 
 template <int FMT, int D>
-__device__ __forceinline__ Offsets<FMT, D> offsets() {
+__device__ __forceinline__ Offsets<FMT, D> offsets(int lane) {
   constexpr int kRow = D / 2;
   constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
-  const int lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int n = lane & 15, q = lane >> 4;
   Offsets<FMT, D> o;
   if (FMT == kINT) {
     o.k = n * kRow + (D == 64 ? 4 : 16) * q;
@@ -599,10 +599,24 @@ __device__ __forceinline__ void arrange_k(Raw<FMT, D>& w, int u) {
   }
 }
 
-// Zeros for the step's tokens outside [lo, hi).
+// Scales whose values may not be finite: fp16's infinities and NaN, E4M3's NaN, and the E8M0 scales
+// with which a code passes bf16's range.
+template <int FMT>
+constexpr uint32_t kOpenBits = FMT == kMX ? 0xFF : FMT == kNV ? 0x7F : 0x7C00;
+template <int FMT>
+constexpr uint32_t kOpenFrom = FMT == kMX ? 253 : kOpenBits<FMT>;
+template <int FMT>
+__device__ __forceinline__ bool open_scale(uint32_t s) {
+  return (s & kOpenBits<FMT>) >= kOpenFrom<FMT>;
+}
+
+// Zeros for the tokens outside [lo, hi) of a step that some column does not see whole, which may hold
+// anything, and a scale of 0 for values that may not be finite, which a probability of 0 would
+// not cancel (spoil has what they are to the columns that see them); whether there were any of those.
 template <int FMT, int D>
-__device__ __forceinline__ void clear_v(Raw<FMT, D>& w, int t0, int lo, int hi) {
+__device__ __forceinline__ bool clear_v(Raw<FMT, D>& w, int t0, int lo, int hi) {
   const int q = (threadIdx.x & 63) >> 4;
+  uint32_t most = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int t = t0 + 16 * (e / 4) + 4 * q + e % 4;
@@ -611,8 +625,14 @@ __device__ __forceinline__ void clear_v(Raw<FMT, D>& w, int t0, int lo, int hi) 
       for (int i = 0; i < Raw<FMT, D>::kV; ++i) w.vc[e][i] = 0;
       w.vs[e] = 0;
     }
+    most = max(most, w.vs[e] & kOpenBits<FMT>);
+    w.vs[e] = open_scale<FMT>(w.vs[e]) ? 0 : w.vs[e];
   }
+  return __any(most >= kOpenFrom<FMT>);
 }
+
+// Whether a column sees token t.
+__device__ __forceinline__ bool sees(int t, int pos, int window) { return t <= pos && (!window || t > pos - window); }
 
 // Scores of tokens that a column does not see become -inf.
 template <int NQ>
@@ -631,8 +651,7 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2][NQ], int t0, int lo, c
       const int t = t0 + 16 * u + 4 * q + r;
 #pragma unroll
       for (int ct = 0; ct < NQ; ++ct) {
-        const bool seen = t >= lo && t <= pos[ct] && (!window || t > pos[ct] - window);
-        s[u][ct][r] = seen ? s[u][ct][r] : -__builtin_inff();
+        s[u][ct][r] = t >= lo && sees(t, pos[ct], window) ? s[u][ct][r] : -__builtin_inff();
       }
     }
 }
@@ -755,6 +774,53 @@ __device__ __forceinline__ uint16_t* out_row(const KvAttnArgs& a, const Piece& p
   return a.out + ((int64_t)(p.s.start + i) * a.kv * a.group + p.h * a.group + col - i * a.group) * D;
 }
 
+// What clear_v took out, for the columns that see it: NaN in the channels of its group.  Goes
+// once more over the scales of the wave's steps, `step` from `first` on, that do not lie in
+// [clear_from, clear_to).  Lane (n, q) has results of the channels that lanes 4 q + r of V have.
+template <int FMT, int D, int NQ, int CH>
+__device__ __forceinline__ void spoil(const KvAttnArgs& a, const Piece& p, f32x4 (&acc)[CH][NQ], const int (&pos)[NQ], int first,
+                                      int step, int clear_from, int clear_to) {
+  constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
+  // (Lane and NaN are made here, so that no registers are kept for them over the steps.)
+  uint32_t none = 0;
+  asm volatile("" : "+s"(none));
+  const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, none)), q = lane >> 4;
+  const float nan = __uint_as_float(0x7FC00000u + none);
+  const uint32_t at = offsets<FMT, D>(lane).vs;
+  uint32_t bad[NQ] = {};
+#pragma unroll 1
+  for (int t0 = first * kTile; t0 < p.hi; t0 += step * kTile) {
+    if (t0 >= clear_from && t0 + kTile <= clear_to) continue;
+#pragma unroll 1
+    for (int u = 0; u < kTile; u += 16) {
+      const int half = t0 + u;
+      if (half + 16 <= p.lo || half >= p.hi) continue;
+      const int page = a.table[p.b * a.ldt + (half >> a.page_log2)];
+      if (page < 0 || page >= a.pages) continue;
+      const int64_t row = (((int64_t)page * a.kv + p.h) << a.page_log2) + (half & ((1 << a.page_log2) - 1));
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const uint8_t* s = a.v_scales + row * kScaleRow + at + e * kScaleRow;
+        const int mine = half + 4 * q + e;
+        const bool open = mine >= p.lo && mine < p.hi && open_scale<FMT>(FMT == kINT ? load_unaligned<uint16_t>(s) : *s);
+        const uint64_t lanes = __ballot(open);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t rows = (uint32_t)(lanes >> (16 * k)) >> (4 * q) & 15u;
+#pragma unroll
+          for (int ct = 0; ct < NQ; ++ct) bad[ct] |= sees(half + 4 * k + e, pos[ct], a.window) ? rows : 0u;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int ct = 0; ct < NQ; ++ct)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[j][ct][r] = bad[ct] >> r & 1u ? nan : acc[j][ct][r];
+}
+
 // A piece for few columns, its 32-token steps dealt to the four waves.  Measured, with the
 // joining: 16 sequences of up to 131072 tokens, 8 heads of 128, INT4, 295 us: 5.0 TB/s, as a
 // device copy, vector instructions two thirds of the time.  One of 131072, MXFP4, 34 us: 4.1 TB/s.
@@ -779,7 +845,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
   const int last = (hi + kTile - 1) / kTile;
   const int steps = hi > lo && last > first ? (last - first + step - 1) / step : 0;
 
-  const auto o = offsets<FMT, D>();
+  const auto o = offsets<FMT, D>(lane);
   const int mask = (1 << a.page_log2) - 1;
   const int top = (hi - 1) & ~15, bottom = lo & ~15;  // halves that hold tokens
   // First token of half u of step k, or of the nearest half that holds tokens.
@@ -879,6 +945,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
     for (int j = 0; j < CH; ++j) acc[j][ct] = f32x4{0, 0, 0, 0};
   }
 
+  int open = 0;
   auto compute = [&](RawT& w, int k) {
     const int t0 = (first + k * step) * kTile;
     const bool clear = t0 >= clear_from && t0 + kTile <= clear_to;
@@ -924,8 +991,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
     });
     if (!clear) {
       mask_scores<NQ>(s, t0, lo, pos, a.window);
-      // Places without a token may hold anything, also what 0 does not cancel.
-      clear_v(w, t0, lo, hi);
+      if (clear_v(w, t0, lo, hi)) open = 1;
     }
     u32x4 pf[NQ];
     softmax_step<FMT, NQ, CH>(s, scale, m, l, acc, pf);
@@ -954,6 +1020,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       if (k + 1 < steps) compute(w1, k + 1);
     }
   }
+  if (open) spoil<FMT, D>(a, p, acc, pos, first, step, clear_from, clear_to);
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
     l[ct] = column_sum(l[ct]);
@@ -1034,7 +1101,7 @@ template <int FMT, int D, int SHAPE, int PLANES>
 constexpr int lds_floats() {
   if (SHAPE != kKvPrompt) return q_floats<FMT, D, SHAPE, PLANES>() + 4 * kCh<D> / kParts<D> * 4 * 64;
   constexpr int tiles = kStageTiles<FMT, D> * kTileLds<FMT, D> / 2, queries = PLANES == 2 ? 4 * kQTile<D, 2> / 2 : 0;
-  return (tiles > queries ? tiles : queries) + 4;
+  return (tiles > queries ? tiles : queries) + 4;  // (and two flags)
 }
 
 template <int FMT, int D, int PLANES>
@@ -1049,6 +1116,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   const int past = p.s.len - p.s.count;  // place of query 0
   uint16_t* tiles = reinterpret_cast<uint16_t*>(lds);
   int* any_bad = reinterpret_cast<int*>(lds + lds_floats<FMT, D, kKvPrompt, PLANES>() - 4);
+  int* any_open = any_bad + 1;
 
   // Tokens of the wave's columns, and of the stages.
   const int i0 = c0 / a.group, end = (c0 + 16 * NQ - 1) / a.group, i1 = end < p.s.count ? end : p.s.count - 1;
@@ -1060,7 +1128,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   // What this wave expands: tile `sub` of each stage.
   const int sub = D == 256 ? wave >> 1 : wave;
   const bool does_k = D < 256 || !(wave & 1), does_v = D < 256 || (wave & 1);
-  const auto o = offsets<FMT, D>();
+  const auto o = offsets<FMT, D>(lane);
   const int mask = (1 << a.page_log2) - 1;
   const int top = (p.hi - 1) & ~15, bottom = p.lo & ~15;  // halves that hold tokens
   auto half_at = [&](int k, int u) {
@@ -1131,6 +1199,11 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       }
   }
   const int clear_to = past + i0 + 1, clear_from = a.window ? past + i1 - a.window + 1 : 0;
+  // The same for all four waves' columns.
+  const int il = (p.t * NC + NC - 1) / a.group;
+  const int all_clear_to = past + p.t * NC / a.group + 1;
+  const int all_clear_from = a.window ? past + (il < p.s.count ? il : p.s.count - 1) - a.window + 1 : 0;
+  bool open = false;
   const float scale = FMT == kNV ? fmaxf(a.scale * a.k_gs[0], 1e-30f) : fmaxf(a.scale, 1e-30f);
   f32x4 acc[CH][NQ];
   float m[NQ], l[NQ];
@@ -1141,7 +1214,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
 #pragma unroll
     for (int j = 0; j < CH; ++j) acc[j][ct] = f32x4{0, 0, 0, 0};
   }
-  if (threadIdx.x == 0) *any_bad = 0;
+  if (threadIdx.x == 0) *any_bad = *any_open = 0;
   __syncthreads();  // the queries' LDS is free
 
   // A tile's operands: K's 2 KJ (half u, instruction j), then V's CH, 1 KB each, lane by lane.
@@ -1163,7 +1236,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       }
     }
     if (does_v) {
-      if (t0 < p.lo || t0 + kTile > p.hi) clear_v(w, t0, p.lo, p.hi);
+      if (t0 < all_clear_from || t0 + kTile > all_clear_to) open |= clear_v(w, t0, p.lo, p.hi);
       const VScales<FMT> vs = v_scales(w);
 #pragma unroll
       for (int i = 0; i < RawT::kV; ++i)
@@ -1235,8 +1308,10 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
     meet();
   }
   if (__any(bad) && lane == 0) *any_bad = 1;
+  if (open && lane == 0) *any_open = 1;
   __syncthreads();
   const bool nan = *any_bad != 0;
+  if (uniform(*any_open)) spoil<FMT, D>(a, p, acc, pos, first, 1, all_clear_from, all_clear_to);
   const float vg = FMT == kNV ? a.v_gs[0] : 1.0f / kVFactor<FMT>;
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
