@@ -432,7 +432,7 @@ int64_t wush_token_logprobs_workspace(int64_t R, int64_t V, int logit_type, int 
  *   k_codes, v_codes    u8 [pages][heads][page][D/2]
  *   k_scales, v_scales  [pages][heads][page][D/G] (fp16 for INT4), G the format's group
  * all 16-byte aligned, in the formats above with groups along D, and for NVFP4
- * the tensor scales k_global, v_global (device fp32, one each).  Token slot s is place
+ * the tensor scales k_global, v_global (device fp32, one each, not negative).  Token slot s is place
  * s % page of page s / page.  page: a power of two, 16 .. 65536.  D: 64, 128 or 256.
  * 1 <= heads <= 4096.  What no call wrote may hold anything. */
 
@@ -471,7 +471,7 @@ wush_status wush_kv4_append(int fmt, const void* K, int64_t ldk, const void* V, 
  * A sequence whose length passes width * page, or with a page outside the cache among those
  * read, has NaN results; no access leaves the buffers.  Values that are not finite (an infinite
  * INT4 scale, say) spoil the results of the queries that see them, in their group's channels, and
- * no others.  Scores and sums are fp32, T q is kept
+ * no others; with a k_global that is NaN or negative all are NaN.  Scores and sums are fp32, T q is kept
  * to 16 significant bits, probabilities enter the sum over v with bf16's 8 for MXFP4 and fp16's
  * 11 otherwise (as do INT4's values).  scale is positive and finite.  Results repeat bit for bit.
  * workspace: wush_kv4_attention_workspace bytes (0 where width * page is small). */

@@ -656,6 +656,16 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2][NQ], int t0, int lo, c
     }
 }
 
+// Of the scores, with K's tensor scale.  One of 0 must not meet a masked score; one that is not
+// a number makes the results so, as does a negative one, with which the running maximum
+// would be a minimum.
+template <int FMT>
+__device__ __forceinline__ float score_scale(const KvAttnArgs& a) {
+  if (FMT != kNV) return a.scale;
+  const float f = a.scale * a.k_gs[0];
+  return f > 0.0f ? f : f == 0.0f ? FLT_MIN : __builtin_nanf("");
+}
+
 // Scores of 32 tokens to probabilities, up to the running maximum m, as B operands.  l sums
 // what they were rounded to, so that where one token outweighs the others nothing of the
 // rounding is left.
@@ -932,8 +942,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
   }
   // Tiles that every column of the wave sees whole need no mask.
   const int clear_to = past + i0 + 1, clear_from = a.window ? past + i1 - a.window + 1 : 0;
-  // (a tensor scale of 0 must not meet a masked score)
-  const float scale = FMT == kNV ? fmaxf(a.scale * a.k_gs[0], 1e-30f) : fmaxf(a.scale, 1e-30f);
+  const float scale = score_scale<FMT>(a);
 
   f32x4 acc[CH][NQ];
   float m[NQ], l[NQ];
@@ -1204,7 +1213,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   const int all_clear_to = past + p.t * NC / a.group + 1;
   const int all_clear_from = a.window ? past + (il < p.s.count ? il : p.s.count - 1) - a.window + 1 : 0;
   bool open = false;
-  const float scale = FMT == kNV ? fmaxf(a.scale * a.k_gs[0], 1e-30f) : fmaxf(a.scale, 1e-30f);
+  const float scale = score_scale<FMT>(a);
   f32x4 acc[CH][NQ];
   float m[NQ], l[NQ];
 #pragma unroll

@@ -4,7 +4,7 @@ any kind: each query's result depends on the tokens that it sees alone."""
 import numpy as np
 import pytest
 
-from tests.decode_cases import FMTS, values
+from tests.decode_cases import FMTS, bf16, values
 from tests.kv4_cases import GROUP, Batch
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +47,22 @@ def test_values_that_are_not_finite_stay_with_their_tokens(fmt, D, counts, windo
     got = values(b.run(window=window))
     assert not np.isfinite(got[hit]).any()
     assert np.all(np.abs(got - want)[~hit] <= bound[~hit])
+
+
+@pytest.mark.parametrize("counts", [[3, 5, 2], [12, 20, 16], [150, 70, 131]])
+def test_key_tensor_scales_of_every_kind(counts):
+    """A tensor scale of 0 makes all scores 0, a tiny one counts with its own size, and one that
+    is NaN or negative shows in every result."""
+    rng = np.random.default_rng(counts[0])
+    b = Batch(rng, "nvfp4", 128, 2, 2, 32, [333, 90, 2000], counts)
+    vg = b.g[1]
+    b.check()
+    for bad in (np.nan, -b.g[0]):
+        b.g = np.float32(bad), vg
+        assert torch.isnan(b.run()).all()
+    b.g = np.float32(0.0), vg
+    b.check()
+    # The same scores, from larger queries.
+    b.g = np.float32(2e-3) * np.float32(2.0**-100), vg
+    b.q, b.q_bits = bf16(b.q * 2.0**100)
+    b.check()
