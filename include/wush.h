@@ -473,7 +473,7 @@ wush_status wush_kv4_append(int fmt, const void* K, int64_t ldk, const void* V, 
  * INT4 scale, say) spoil the results of the queries that see them, in their group's channels, and
  * no others; with a k_global that is NaN or negative all are NaN.  Scores and sums are fp32, T q is kept
  * to 16 significant bits, probabilities enter the sum over v with bf16's 8 for MXFP4 and fp16's
- * 11 otherwise (as do INT4's values).  scale is positive and finite.  Results repeat bit for bit.
+ * 11 otherwise (as do INT4's values).  scale is positive, and finite times log2 e.  Results repeat bit for bit.
  * workspace: wush_kv4_attention_workspace bytes (0 where width * page is small). */
 wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* T_q, const void* k_codes,
                                const void* k_scales, const float* k_global, const void* v_codes, const void* v_scales,

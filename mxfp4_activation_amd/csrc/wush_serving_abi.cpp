@@ -148,7 +148,9 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
     return fail(WUSH_EINVAL, "q_heads must be a multiple of heads, at most %lld (got %lld)", (long long)kMaxHeads, (long long)q_heads);
   if (B < 0 || n < 0) return fail(WUSH_EINVAL, "B and n must be >= 0");
   if (!q_start && B != n) return fail(WUSH_EINVAL, "without q_start every sequence has one query (B %lld, n %lld)", (long long)B, (long long)n);
-  if (!(scale > 0.0f) || !(scale < INFINITY)) return fail(WUSH_EINVAL, "scale must be positive and finite");
+  // (The kernels take powers of two.)
+  const float scale2 = (float)(scale * 1.4426950408889634);
+  if (!(scale > 0.0f) || !(scale2 < INFINITY)) return fail(WUSH_EINVAL, "scale must be positive and finite");
   if (window < 0 || window > kMaxTokens) return fail(WUSH_EINVAL, "window must be 0 (none) .. 2^30 (got %lld)", (long long)window);
   if (width < 1 || width > kMaxTokens / page) return fail(WUSH_EINVAL, "width must be 1 .. 2^30 / page (got %lld)", (long long)width);
   if (B == 0 || n == 0) return WUSH_OK;
@@ -213,7 +215,7 @@ wush_status wush_kv4_attention(int fmt, const void* Q, int64_t ldq, const void* 
   a.width = (int)width;
   a.pages = (int)pages;
   a.window = (int)window;
-  a.scale = (float)(scale * 1.4426950408889634);  // the kernels take powers of two
+  a.scale = scale2;
   a.workgroups = (int)plan.workgroups;
   a.runs = plan.runs;
   a.items = (int)plan.items;

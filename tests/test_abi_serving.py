@@ -185,3 +185,15 @@ def test_pieces_fit_their_workspace():
         for u, p in zip(all_units, pieces):
             each = -(-u // p)
             assert each <= share and (p - 1) * each < u <= p * each
+
+
+def test_attention_refuses_scales_past_fp32_as_powers_of_two():
+    """The kernels take scale * log2 e: a finite scale whose product is not is refused."""
+    lib = wush.load()
+
+    def attend(scale):
+        return lib.wush_kv4_attention(0, A, 1024, None, A * 10, A * 11, None, A * 13, A * 14, None, A * 3, 40, 40, A * 4, None,
+                                      0, 0, 8, 2, 128, 16, 9, scale, 0, A * 5, A * 6, 1 << 40, None)
+
+    assert attend(2.35e38) == OK and attend(1e-45) == OK
+    assert attend(2.4e38) == EINVAL and b"scale" in lib.wush_last_error()
