@@ -513,7 +513,8 @@ int64_t wush_linear_w4_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t r
  *   logits, out: [R][V] of one type, row strides ld, ld_out >= V elements; out may be logits
  *      itself (same pointer and stride).
  *   prompt: int32 [R][n_prompt], output: int32 [R][n_output], bias_ids: int32 [R][n_bias]; entries
- *      outside 0 .. V - 1 (padding: -1) count for nothing.  A length of 0: no list.
+ *      outside 0 .. V - 1 (padding: -1) count for nothing.  A length of 0: no list.  n_prompt and n_bias
+ *      are at most 2^31 - 1, n_output 2^30 - 1.
  *   repetition, frequency, presence: fp32 [R] or NULL (1, 0, 0).  bias: fp32 [R][n_bias].
  *   allowed: int32 [R][(V + 31) / 32] or NULL (all).
  * 1 <= V < 2^31, 0 <= R <= 65535 (0 is a no-op).  Results repeat bit for bit. */

@@ -27,6 +27,7 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 constexpr int64_t kMaxLoraRows = 65535 * 16;
 constexpr int64_t kMaxRank = 512;
 constexpr int64_t kMaxAdjustRows = 65535;
+constexpr int64_t kMaxOutputs = ((int64_t)1 << 30) - 1;  // a token's count in the kernel has 30 bits
 
 int log2_of(int64_t v) {
   int n = 0;
@@ -339,6 +340,7 @@ wush_status wush_adjust_logits(const void* logits, int logit_type, int64_t ld, i
   if (V < 1 || V > INT32_MAX) return fail(WUSH_EINVAL, "V must be 1 .. 2^31 - 1 (got %lld)", (long long)V);
   if (n_prompt < 0 || n_output < 0 || n_bias < 0 || n_prompt > INT32_MAX || n_output > INT32_MAX || n_bias > INT32_MAX)
     return fail(WUSH_EINVAL, "the lists' lengths must be 0 .. 2^31 - 1");
+  if (n_output > kMaxOutputs) return fail(WUSH_EINVAL, "n_output must be less than 2^30 (got %lld)", (long long)n_output);
   if (R == 0) return WUSH_OK;
   if (R > kMaxAdjustRows) return fail(WUSH_EINVAL, "R too large for one launch");
   if (R > 1 && (ld < V || ld > ((int64_t)1 << 36) || ld_out < V || ld_out > ((int64_t)1 << 36)))

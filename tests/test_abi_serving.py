@@ -197,3 +197,14 @@ def test_attention_refuses_scales_past_fp32_as_powers_of_two():
 
     assert attend(2.35e38) == OK and attend(1e-45) == OK
     assert attend(2.4e38) == EINVAL and b"scale" in lib.wush_last_error()
+
+
+def test_adjust_refuses_outputs_that_its_counts_cannot_hold():
+    """A token's count shares its word with two marks: 30 bits."""
+    lib = wush.load()
+
+    def adjust(n):
+        return lib.wush_adjust_logits(A, 0, 50, 0, 50, None, 0, A * 3, n, None, None, None, None, None, 0, None, A * 9, 50, None)
+
+    assert adjust((1 << 30) - 1) == OK
+    assert adjust(1 << 30) == EINVAL and b"n_output" in lib.wush_last_error()
