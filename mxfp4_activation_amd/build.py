@@ -19,8 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwush.so")
 BINDING = os.path.join(HERE, "_binding.so")
 # (those that take longest first)
-SOURCES = ["wush_kernels.hip", "wush_w4.hip", "wush_kv4_int.hip", "wush_kv4_nv.hip", "wush_kv4_mx.hip", "wush_moe.hip",
-           "wush_logprobs.hip", "wush_gptq.hip", "wush_build.hip", "wush_gemm.hip", "wush_kv4.hip", "wush_adjust.hip",
+SOURCES = ["wush_kernels.hip", "wush_w4.hip", "wush_w4_lora.hip", "wush_kv4_int.hip", "wush_kv4_nv.hip", "wush_kv4_mx.hip",
+           "wush_moe.hip", "wush_logprobs.hip", "wush_gptq.hip", "wush_build.hip", "wush_gemm.hip", "wush_kv4.hip", "wush_adjust.hip",
            "wush_dequant.hip", "wush_abi.cpp", "wush_decode_abi.cpp", "wush_serving_abi.cpp"]
 
 HIPCC_FLAGS = [

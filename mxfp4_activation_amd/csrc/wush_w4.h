@@ -111,6 +111,7 @@ hipError_t launch_moe(const MoeArgs& a, hipStream_t s);
 
 hipError_t launch_split(const SplitArgs& a, hipStream_t s);
 hipError_t launch_linear_w4(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_w4_lora(const LinearArgs& a, hipStream_t s);  // where a.lora.ids is not null
 // h of the adapters and, where t is not null, also what launch_split does.
 hipError_t launch_lora(const LoraArgs& a, const SplitArgs* t, hipStream_t s);
 hipError_t launch_lora_expand(const LoraArgs& a, int64_t N, hipStream_t s);

@@ -39,3 +39,12 @@ def test_attention_keeps_its_workgroups():
         else:
             want = 3 if shape == 1 and D == 64 and fmt != 2 else 2
         assert 512 // (-(-n["vgpr_count"] // 8) * 8) >= want, (name, n)
+
+
+def test_products_without_adapters_have_kernels_of_their_own():
+    """What adapters need of registers is not taken from linear layers without them."""
+    found = {name: n["vgpr_count"] for name, n in _notes("linear_kernel").items()}
+    plain = [name for name in found if name.endswith("ELb0EEEvNS_10LinearArgsE")]
+    assert plain and len(plain) * 2 == len(found)
+    for name in plain:
+        assert found[name] <= found[name.replace("ELb0EEEvNS", "ELb1EEEvNS")], name
