@@ -97,6 +97,17 @@ hipStream_t stream_of(int device) { return c10::hip::getCurrentHIPStream(device)
 Tensor workspace(int64_t n, const Tensor& like) { return n ? at::empty({n}, like.options().dtype(at::kByte)) : Tensor(); }
 void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
+// f() without Python's lock, which other threads may want: allocations and launches can wait for
+// the device, and for a host callback that needs the lock.
+template <typename F>
+auto unlocked(F f) {
+  struct Lock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return f();
+}
+
 PyObject* answer(wush_status st, const Tensor& t) {
   if (st != WUSH_OK) return PyLong_FromLong(st);
   return THPVariable_Wrap(t);
@@ -153,9 +164,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const void* tk = c.maybe(a[10], at::kBFloat16, {heads, D / G, G, G});
   const void* tv = c.maybe(a[11], at::kBFloat16, {heads, D / G, G, G});
   if (!c.ok || e.heads != heads) Py_RETURN_NONE;
-  const wush_status st = f_append(fmt, k->data_ptr(), k->stride(0), v->data_ptr(), v->stride(0), tk, tv,
-                                  static_cast<const int64_t*>(slots), n, heads, D, e.page, e.pages, e.kc, e.ks, e.kg, e.vc, e.vs,
-                                  e.vg, stream_of(c.device));
+  const wush_status st = unlocked([&] {
+    return f_append(fmt, k->data_ptr(), k->stride(0), v->data_ptr(), v->stride(0), tk, tv, static_cast<const int64_t*>(slots), n,
+                    heads, D, e.page, e.pages, e.kc, e.ks, e.kg, e.vc, e.vs, e.vg, stream_of(c.device));
+  });
   return PyLong_FromLong(st);
 }
 
@@ -187,13 +199,15 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
   void* given = c.maybe(a[14], at::kBFloat16, {n, hq, D});
   if (!c.ok || (D != 64 && D != 128 && D != 256)) Py_RETURN_NONE;
   const int64_t nw = f_attention_workspace(fmt, B, n, hq, e.heads, D, e.page, width);
-  const Tensor out = given ? Tensor() : at::empty({n, hq, D}, q->options());
-  const Tensor ws = workspace(nw, *q);
-  const wush_status st = f_attention(fmt, q->data_ptr(), q->stride(0), T, e.kc, e.ks, e.kg, e.vc, e.vs, e.vg,
-                                     static_cast<const int32_t*>(table->data_ptr()), table->stride(0), width,
-                                     static_cast<const int32_t*>(lengths), static_cast<const int32_t*>(start), B, n, hq, e.heads, D,
-                                     e.page, e.pages, (float)scale, window, given ? given : out.data_ptr(), data(ws), nw,
-                                     stream_of(c.device));
+  Tensor out;
+  const wush_status st = unlocked([&] {
+    if (!given) out = at::empty({n, hq, D}, q->options());
+    const Tensor ws = workspace(nw, *q);
+    return f_attention(fmt, q->data_ptr(), q->stride(0), T, e.kc, e.ks, e.kg, e.vc, e.vs, e.vg,
+                       static_cast<const int32_t*>(table->data_ptr()), table->stride(0), width, static_cast<const int32_t*>(lengths),
+                       static_cast<const int32_t*>(start), B, n, hq, e.heads, D, e.page, e.pages, (float)scale, window,
+                       given ? given : out.data_ptr(), data(ws), nw, stream_of(c.device));
+  });
   return given ? answer(st, a[14]) : answer(st, out);
 }
 
@@ -221,11 +235,14 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (!c.ok) Py_RETURN_NONE;
   const int ot = f32 ? WUSH_OUT_F32 : WUSH_OUT_BF16;
   const int64_t nw = f_lora_workspace(M, N, K, rank, T != nullptr, ot);
-  const Tensor out = given ? Tensor() : at::empty({M, N}, x->options().dtype(type));
-  const Tensor ws = workspace(nw, *x);
-  const wush_status st = f_lora(fmt, x->data_ptr(), x->stride(0), T, pc, ps, g, pa, pb, static_cast<const float*>(pe),
-                                static_cast<const int32_t*>(ids), E, rank, M, N, K, given ? given : out.data_ptr(), ot, data(ws),
-                                nw, stream_of(c.device));
+  Tensor out;
+  const wush_status st = unlocked([&] {
+    if (!given) out = at::empty({M, N}, x->options().dtype(type));
+    const Tensor ws = workspace(nw, *x);
+    return f_lora(fmt, x->data_ptr(), x->stride(0), T, pc, ps, g, pa, pb, static_cast<const float*>(pe),
+                  static_cast<const int32_t*>(ids), E, rank, M, N, K, given ? given : out.data_ptr(), ot, data(ws), nw,
+                  stream_of(c.device));
+  });
   return given ? answer(st, a[11]) : answer(st, out);
 }
 
@@ -263,12 +280,14 @@ PyObject* adjust(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (!c.ok || (given && (given->scalar_type() != type || given->sizes() != l->sizes() || !given->is_cuda() ||
                           given->get_device() != c.device || (V > 1 && given->stride(1) != 1))))
     Py_RETURN_NONE;
-  const Tensor fresh = given ? Tensor() : at::empty({R, V}, l->options());
-  const Tensor& out = given ? *given : fresh;
-  const wush_status st = f_adjust(l->data_ptr(), lt, l->stride(0), R, V, p, np, o, no, static_cast<const float*>(rep),
-                                  static_cast<const float*>(freq), static_cast<const float*>(pres), bi,
-                                  static_cast<const float*>(b), nb, static_cast<const int32_t*>(m), out.data_ptr(), out.stride(0),
-                                  stream_of(c.device));
+  Tensor fresh;
+  const wush_status st = unlocked([&] {
+    if (!given) fresh = at::empty({R, V}, l->options());
+    const Tensor& out = given ? *given : fresh;
+    return f_adjust(l->data_ptr(), lt, l->stride(0), R, V, p, np, o, no, static_cast<const float*>(rep),
+                    static_cast<const float*>(freq), static_cast<const float*>(pres), bi, static_cast<const float*>(b), nb,
+                    static_cast<const int32_t*>(m), out.data_ptr(), out.stride(0), stream_of(c.device));
+  });
   return given ? answer(st, a[9]) : answer(st, fresh);
 }
 
@@ -284,9 +303,12 @@ PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const float* g = c.global(a[3], fmt);
   void* given = c.maybe(a[4], at::kFloat, {M, K});
   if (!c.ok) Py_RETURN_NONE;
-  const Tensor out = given ? Tensor() : at::empty({M, K}, codes->options().dtype(at::kFloat));
-  const wush_status st = f_dequant(fmt, codes->data_ptr(), scales, g, M, K, static_cast<float*>(given ? given : out.data_ptr()),
-                                   stream_of(c.device));
+  Tensor out;
+  const wush_status st = unlocked([&] {
+    if (!given) out = at::empty({M, K}, codes->options().dtype(at::kFloat));
+    return f_dequant(fmt, codes->data_ptr(), scales, g, M, K, static_cast<float*>(given ? given : out.data_ptr()),
+                     stream_of(c.device));
+  });
   return given ? answer(st, a[4]) : answer(st, out);
 }
 
