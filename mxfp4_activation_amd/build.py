@@ -13,6 +13,7 @@ import sys
 import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -49,17 +50,43 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
-def build_binding(verbose: bool = False) -> str:
-    """csrc/binding.cpp against this torch's headers."""
+def _binding_needs() -> str:
+    """What csrc/binding.cpp cannot be compiled without and is not here, or nothing."""
+    try:
+        import torch
+    except ImportError:
+        return "torch"
+    if shutil.which(_cxx()[0]) is None:
+        return "a C++ compiler (%s)" % _cxx()[0]
+    for name, at in (("Python", os.path.join(sysconfig.get_paths()["include"], "Python.h")),
+                     ("torch's HIP", os.path.join(os.path.dirname(torch.__file__), "include", "c10", "hip", "HIPStream.h"))):
+        if not os.path.exists(at):
+            return "%s headers (%s)" % (name, at)
+    return ""
+
+
+def _cxx():
+    return os.environ.get("CXX", "g++").split() or ["g++"]
+
+
+def build_binding(verbose: bool = False) -> Optional[str]:
+    """csrc/binding.cpp against this torch's headers.  None where something that it takes is
+    not here: the library needs none of it, and the wrappers do without the binding."""
+    needs = _binding_needs()
+    if needs:
+        sys.stderr.write("_binding.so is not built, for want of %s: the wrappers marshal in Python\n" % needs)
+        if os.path.exists(BINDING):  # of another build
+            os.remove(BINDING)
+        return None
     import torch
 
     at = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + os.path.join(at, "include"),
-           "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I/opt/rocm/include",
-           "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
-           "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    cmd = _cxx() + ["-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+                    "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + os.path.join(at, "include"),
+                    "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I/opt/rocm/include",
+                    "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
+                    "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     if verbose:
         print(" ".join(cmd), flush=True)
     _run(cmd)
