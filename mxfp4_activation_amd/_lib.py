@@ -8,9 +8,12 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwush.so")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 WUSH_OK, WUSH_EINVAL, WUSH_EALIGN, WUSH_EUNSUPPORTED, WUSH_EHIP = range(5)
 FMT = {"mxfp4": 0, "nvfp4": 1, "int4": 2}
@@ -97,16 +100,32 @@ _NATIVE = ("wush_kv4_append", "wush_kv4_attention", "wush_kv4_attention_workspac
 _binding = False  # not looked for yet
 
 
+def built_for() -> str:
+    """What a binding has to have been built for."""
+    import torch
+
+    return "torch %s, Python %d.%d, ABI %d" % (torch.__version__, *sys.version_info[:2], ABI_VERSION)
+
+
 def binding():
     """The native form of the wrappers' argument marshalling (csrc/binding.cpp), or None
     where it is not built: the wrappers then do it in Python, some ten microseconds slower.
-    Needs torch to be imported."""
+    One that cannot be loaded, or was built for something else, is left aside with a
+    warning.  Needs torch to be imported."""
     global _binding
     if _binding is False:
+        module, why = None, ""
         try:
             from . import _binding as module
-        except ImportError:
-            module = None
+        except ImportError as e:
+            why = "cannot be loaded (%s)" % e if os.path.exists(BINDING_PATH) else ""
+        if module is not None:
+            made_for = getattr(module, "built_for", "something else")
+            if made_for != built_for():
+                module, why = None, "was built for %s, this is %s" % (made_for, built_for())
+        if why:
+            warnings.warn("_binding.so %s: the wrappers marshal in Python; run `python -m mxfp4_activation_amd.build`" % why,
+                          RuntimeWarning, stacklevel=3)
         if module is not None:
             lib = load()
             module.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _NATIVE})

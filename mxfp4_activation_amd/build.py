@@ -15,6 +15,8 @@ import tempfile
 from concurrent.futures import ThreadPoolExecutor
 from typing import Optional
 
+from . import _lib
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libwush.so")
@@ -83,6 +85,7 @@ def build_binding(verbose: bool = False) -> Optional[str]:
     at = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
     cmd = _cxx() + ["-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM",
+                    '-DBUILT_FOR="%s"' % _lib.built_for(),
                     "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + os.path.join(at, "include"),
                     "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I/opt/rocm/include",
                     "-I" + sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
