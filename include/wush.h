@@ -468,8 +468,8 @@ wush_status wush_kv4_append(int fmt, const void* K, int64_t ldk, const void* V, 
  *   q_start: int32 [B + 1], ascending from 0: the queries of sequence b are rows
  *      q_start[b] .. q_start[b + 1] - 1.  NULL: one each (B == n).
  *   out: bf16 [n][q_heads][D], 16-byte aligned.  Rows from q_start[B] on are not written.
- * A sequence whose length passes width * page, or with a page outside the cache among those
- * read, has NaN results; no access leaves the buffers.  Values that are not finite (an infinite
+ * A sequence whose length passes width * page has NaN results, and so has a query that sees a token
+ * in a page outside the cache (others of its sequence may); no access leaves the buffers.  Values that are not finite (an infinite
  * INT4 scale, say) spoil the results of the queries that see them, in their group's channels, and
  * no others; with a k_global that is NaN or negative all are NaN.  Scores and sums are fp32, T q is kept
  * to 16 significant bits, probabilities enter the sum over v with bf16's 8 for MXFP4 and fp16's
