@@ -28,10 +28,11 @@ __device__ __forceinline__ float dot8(const u32x4& w, const f32x4& h0, const f32
   return v;
 }
 
-// What token m's adapter adds to result n: nothing without one, NaN for one that is not there.
+// What token m's adapter adds to result n: without one -0, which also a result of -0 keeps,
+// NaN for one that is not there.
 __device__ __forceinline__ float lora_term(const LoraArgs& a, int64_t N, int64_t m, int64_t n) {
   const int64_t id = a.ids[m];
-  if (id < 0) return 0.0f;
+  if (id < 0) return -0.0f;
   if (id >= a.E) return __builtin_nanf("");
   const uint16_t* b = a.B + (id * N + n) * a.rank;
   const float* h = a.h + m * a.rank;

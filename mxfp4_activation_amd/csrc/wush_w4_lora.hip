@@ -83,7 +83,7 @@ __device__ __forceinline__ float sum_group(float v) {
   return v;
 }
 
-// delta[m][n] = B[ids[m]] h[m]; 0 without an adapter, NaN for one that is not there.  A row of B is read by 1 << LOG2
+// delta[m][n] = B[ids[m]] h[m]; -0 without an adapter, NaN for one that is not there.  A row of B is read by 1 << LOG2
 // neighbouring lanes, 16 bytes each, so that a wave reads whole lines, kLoraBlocks times 1 KB at
 // a time; the lanes of a row add up.  Many small waves: B is most of what a batch over many
 // adapters reads, and the product's own workgroups are too few to wait for it.  64 tokens,
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int64_t N)
   const int piece = lane & ((1 << LOG2) - 1), pieces = a.rank / 8;
   const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * (kPer * kLoraBlocks) + (lane >> LOG2);
   if (!with) {
-    const float none = id < 0 ? 0.0f : __builtin_nanf("");
+    const float none = id < 0 ? -0.0f : __builtin_nanf("");
 #pragma unroll
     for (int u = 0; u < kLoraBlocks; ++u)
       if (piece == 0 && n0 + u * kPer < N) a.delta[m * N + n0 + u * kPer] = none;

@@ -107,3 +107,19 @@ def test_adapters_out_of_range_and_strides():
     z = wush.linear_w4_lora(**a, out_dtype=torch.float32)
     keep = [0, 1, 2, 4, 5]
     assert np.all(np.abs(values(z) - want)[keep] <= bound[keep]) and not torch.isfinite(z[3]).all()
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_no_adapter_keeps_results_of_minus_zero(M):
+    """A tensor scale that takes small negative sums below the fp32 range leaves -0, with
+    adapters beside it as without."""
+    import mxfp4_activation_amd as wush
+
+    a = Case("nvfp4", M, 300, 64, 16, 2).args()
+    a["global_scale"] = torch.full((1,), 2.0**-149, device="cuda")
+    a["scales"] = torch.full_like(a["scales"], 1)  # 2^-9
+    a["ids"] = torch.full_like(a["ids"], -1)
+    got = wush.linear_w4_lora(**a, out_dtype=torch.float32)
+    want = wush.linear_w4("nvfp4", a["x"], a["codes"], a["scales"], global_scale=a["global_scale"], out_dtype=torch.float32)
+    assert torch.any((want == 0) & torch.signbit(want))
+    assert torch.equal(got.view(torch.int32), want.view(torch.int32))
