@@ -612,7 +612,7 @@ __device__ __forceinline__ bool open_scale(uint32_t s) {
 
 // Zeros for the tokens outside [lo, hi) of a step that some column does not see whole, which may hold
 // anything, and a scale of 0 for values that may not be finite, which a probability of 0 would
-// not cancel (spoil has what they are to the columns that see them); whether there were any of those.
+// not cancel (spoiled has what they are to the columns that see them); whether there were any of those.
 template <int FMT, int D>
 __device__ __forceinline__ bool clear_v(Raw<FMT, D>& w, int t0, int lo, int hi) {
   const int q = (threadIdx.x & 63) >> 4;
@@ -661,7 +661,7 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2][NQ], int t0, int lo, c
 // would be a minimum.
 template <int FMT>
 __device__ __forceinline__ float score_scale(const KvAttnArgs& a) {
-  if (FMT != kNV) return a.scale;
+  if (FMT != kNV) return fmaxf(a.scale, 0x1p-149f);  // (in a vector register: INT4 prompts 641 us, 681 from a scalar one)
   const float f = a.scale * a.k_gs[0];
   return f > 0.0f ? f : f == 0.0f ? FLT_MIN : __builtin_nanf("");
 }
@@ -778,57 +778,91 @@ struct Piece {
   Seq s;
 };
 
+// Tokens of the units that a place takes.
+template <int NC>
+__device__ __forceinline__ Span tokens_of(const KvAttnArgs& a, const Place& at) {
+  const int i0 = at.t * NC / a.group, il = (at.t * NC + NC - 1) / a.group;
+  const Span all = span_of(a, at.s, i0, il < at.s.count ? il : at.s.count - 1);
+  const int64_t from = (int64_t)(all.lo / kKvUnit + at.off) * kKvUnit, to = from + (int64_t)at.take * kKvUnit;
+  return Span{all.lo > from ? all.lo : (int)from, all.hi < to ? all.hi : (int)to};
+}
+
 // Row of the result for a column of the piece's sequence.
 __device__ __forceinline__ uint16_t* out_row(const KvAttnArgs& a, const Piece& p, int col, int D) {
   const int i = col / a.group;
   return a.out + ((int64_t)(p.s.start + i) * a.kv * a.group + p.h * a.group + col - i * a.group) * D;
 }
 
-// What clear_v took out, for the columns that see it: NaN in the channels of its group.  Goes
-// once more over the scales of the wave's steps, `step` from `first` on, that do not lie in
-// [clear_from, clear_to).  Lane (n, q) has results of the channels that lanes 4 q + r of V have.
-template <int FMT, int D, int NQ, int CH>
-__device__ __forceinline__ void spoil(const KvAttnArgs& a, const Piece& p, f32x4 (&acc)[CH][NQ], const int (&pos)[NQ], int first,
-                                      int step, int clear_from, int clear_to) {
+// What clear_v took out, for the columns that see it: their results are NaN in the channels of its
+// group.  Sets bit r for row r of the lane's results, whose channels are those of lane 4 q + r of
+// V.  Goes once more over the scales of the piece's tokens.
+template <int FMT, int D, int NQ>
+__device__ __forceinline__ void spoiled(const KvAttnArgs& a, int b, int h, const Span& tokens, const int (&pos)[NQ],
+                                        uint32_t (&bad)[NQ]) {
   constexpr int kScaleRow = FMT == kMX ? D / 32 : D / 16;
-  // (Lane and NaN are made here, so that no registers are kept for them over the steps.)
+  // (The lane is counted here, so that no register is kept for it over the steps.)
   uint32_t none = 0;
   asm volatile("" : "+s"(none));
   const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, none)), q = lane >> 4;
-  const float nan = __uint_as_float(0x7FC00000u + none);
   const uint32_t at = offsets<FMT, D>(lane).vs;
-  uint32_t bad[NQ] = {};
-#pragma unroll 1
-  for (int t0 = first * kTile; t0 < p.hi; t0 += step * kTile) {
-    if (t0 >= clear_from && t0 + kTile <= clear_to) continue;
-#pragma unroll 1
-    for (int u = 0; u < kTile; u += 16) {
-      const int half = t0 + u;
-      if (half + 16 <= p.lo || half >= p.hi) continue;
-      const int page = a.table[p.b * a.ldt + (half >> a.page_log2)];
-      if (page < 0 || page >= a.pages) continue;
-      const int64_t row = (((int64_t)page * a.kv + p.h) << a.page_log2) + (half & ((1 << a.page_log2) - 1));
-#pragma unroll 1
-      for (int e = 0; e < 4; ++e) {
-        const uint8_t* s = a.v_scales + row * kScaleRow + at + e * kScaleRow;
-        const int mine = half + 4 * q + e;
-        const bool open = mine >= p.lo && mine < p.hi && open_scale<FMT>(FMT == kINT ? load_unaligned<uint16_t>(s) : *s);
-        const uint64_t lanes = __ballot(open);
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t rows = (uint32_t)(lanes >> (16 * k)) >> (4 * q) & 15u;
 #pragma unroll
-          for (int ct = 0; ct < NQ; ++ct) bad[ct] |= sees(half + 4 * k + e, pos[ct], a.window) ? rows : 0u;
-        }
+  for (int ct = 0; ct < NQ; ++ct) bad[ct] = 0;
+#pragma unroll 1
+  for (int half = tokens.lo & ~15; half < tokens.hi; half += 16) {
+    const int page = a.table[b * a.ldt + (half >> a.page_log2)];
+    if (page < 0 || page >= a.pages) continue;
+    const int64_t row = (((int64_t)page * a.kv + h) << a.page_log2) + (half & ((1 << a.page_log2) - 1));
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+      const uint8_t* s = a.v_scales + row * kScaleRow + at + e * kScaleRow;
+      const int mine = half + 4 * q + e;
+      const bool open =
+          mine >= tokens.lo && mine < tokens.hi && open_scale<FMT>(FMT == kINT ? load_unaligned<uint16_t>(s) : *s);
+      const uint64_t lanes = __ballot(open);
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t rows = (uint32_t)(lanes >> (16 * k)) >> (4 * q) & 15u;
+#pragma unroll
+        for (int ct = 0; ct < NQ; ++ct) bad[ct] |= sees(half + 4 * k + e, pos[ct], a.window) ? rows : 0u;
       }
     }
   }
+}
+
+// The same for a wave's columns of a prompt's piece, c0 of the item's on, with operands from where
+// they are kept anyway: registers that held them through the steps cost NVFP4 and INT4 prompts up
+// to 17% of their time.
+template <int FMT, int D, int NC, int NQ>
+__device__ __forceinline__ void spoiled(const PlanLds& plan, int c0, uint32_t (&bad)[NQ]) {
+  typedef const KvAttnArgs __attribute__((address_space(4))) Kernarg;
+  Kernarg* k = (Kernarg*)__builtin_amdgcn_kernarg_segment_ptr();
+  uint32_t none = 0;
+  asm volatile("" : "+s"(k), "+s"(none));  // (not what was read or counted before)
+  KvAttnArgs a{};
+  a.table = k->table;
+  a.ldt = k->ldt;
+  a.v_scales = k->v_scales;
+  a.kv = k->kv;
+  a.group = k->group;
+  a.page_log2 = k->page_log2;
+  a.pages = k->pages;
+  a.window = k->window;
+  Place at;
+  at.b = uniform(plan.at.b);
+  at.h = uniform(plan.at.h);
+  at.t = uniform(plan.at.t);
+  at.off = uniform(plan.at.off);
+  at.take = uniform(plan.at.take);
+  at.s.count = uniform(plan.at.s.count);
+  at.s.len = uniform(plan.at.s.len);
+  const int n = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, none)) & 15, columns = at.s.count * a.group;
+  int pos[NQ];
 #pragma unroll
-  for (int j = 0; j < CH; ++j)
-#pragma unroll
-    for (int ct = 0; ct < NQ; ++ct)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[j][ct][r] = bad[ct] >> r & 1u ? nan : acc[j][ct][r];
+  for (int ct = 0; ct < NQ; ++ct) {
+    const int col = at.t * NC + c0 + 16 * ct + n;
+    pos[ct] = col < columns ? at.s.len - at.s.count + col / a.group : -1;
+  }
+  spoiled<FMT, D>(a, at.b, at.h, tokens_of<NC>(a, at), pos, bad);
 }
 
 // A piece for few columns, its 32-token steps dealt to the four waves.  Measured, with the
@@ -1029,7 +1063,17 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
       if (k + 1 < steps) compute(w1, k + 1);
     }
   }
-  if (open) spoil<FMT, D>(a, p, acc, pos, first, step, clear_from, clear_to);
+  if (open) {
+    uint32_t bad[NQ], nan = 0x7FC00000u;
+    spoiled<FMT, D>(a, p.b, p.h, Span{lo, hi}, pos, bad);
+    asm volatile("" : "+s"(nan));  // (no register is kept for it either)
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int ct = 0; ct < NQ; ++ct)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][ct][r] = bad[ct] >> r & 1u ? __uint_as_float(nan) : acc[j][ct][r];
+  }
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
     l[ct] = column_sum(l[ct]);
@@ -1113,8 +1157,18 @@ constexpr int lds_floats() {
   return (tiles > queries ? tiles : queries) + 4;  // (and two flags)
 }
 
+// f, or NaN for the rows that are.
+__device__ __forceinline__ f32x4 row_factors(float f, uint32_t bad) {
+  uint32_t nan = 0x7FC00000u;
+  asm("" : "+s"(nan));  // (not a vector register's constant over the steps)
+  f32x4 v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = bad >> r & 1u ? __uint_as_float(nan) : f;
+  return v;
+}
+
 template <int FMT, int D, int PLANES>
-__device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& p, float* lds) {
+__device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& p, const PlanLds& plan, float* lds) {
   constexpr int NQ = kv_tiles(kKvPrompt, D), KJ = D / 32, CH = kCh<D>, NC = kv_columns(kKvPrompt, D);
   constexpr int NS = kStageTiles<FMT, D>, kLds = kTileLds<FMT, D>;
   using RawT = Raw<FMT, D>;
@@ -1207,12 +1261,11 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
         qs[ct][j] = v[0];
       }
   }
-  const int clear_to = past + i0 + 1, clear_from = a.window ? past + i1 - a.window + 1 : 0;
-  // The same for all four waves' columns.
+  // Tiles that every column of the four waves sees whole need no mask.
   const int il = (p.t * NC + NC - 1) / a.group;
-  const int all_clear_to = past + p.t * NC / a.group + 1;
-  const int all_clear_from = a.window ? past + (il < p.s.count ? il : p.s.count - 1) - a.window + 1 : 0;
-  bool open = false;
+  const int clear_to = past + p.t * NC / a.group + 1;
+  const int clear_from = a.window ? past + (il < p.s.count ? il : p.s.count - 1) - a.window + 1 : 0;
+  int open = 0;
   const float scale = score_scale<FMT>(a);
   f32x4 acc[CH][NQ];
   float m[NQ], l[NQ];
@@ -1226,6 +1279,9 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   if (threadIdx.x == 0) *any_bad = *any_open = 0;
   __syncthreads();  // the queries' LDS is free
 
+  // INT4: whether a group's sums and the next operands fit the registers (two prompts as above, heads of
+  // 256: 826 us with and 870 without, but with T 1158 and 1110).
+  constexpr bool kGroups = FMT == kINT && (PLANES == 1 || D == 64);
   // A tile's operands: K's 2 KJ (half u, instruction j), then V's CH, 1 KB each, lane by lane.
   auto operand = [&](int tile, int i) { return reinterpret_cast<u32x4*>(tiles + tile * kLds + i * 512 + lane * 8); };
   auto k_scale_dword = [&](int tile, int u) {
@@ -1245,7 +1301,9 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       }
     }
     if (does_v) {
-      if (t0 < all_clear_from || t0 + kTile > all_clear_to) open |= clear_v(w, t0, p.lo, p.hi);
+      if (t0 < clear_from || t0 + kTile > clear_to) {
+        if (clear_v(w, t0, p.lo, p.hi)) open = 1;
+      }
       const VScales<FMT> vs = v_scales(w);
 #pragma unroll
       for (int i = 0; i < RawT::kV; ++i)
@@ -1268,12 +1326,16 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
     // round, or without, the former wait for the latter (INT4 645 us and 706 above, MXFP4 490 and 497,
     // heads of 256 627 and 647).
     __builtin_amdgcn_s_setprio(1);
-    each<KJ>([&](auto jc) {
-      constexpr int j = jc;
+    // K's operands, and what becomes of their products, in an order that the compiler, left to itself,
+    // gives up when registers are short: read just before they are used they cost NVFP4 and INT4
+    // 4 to 17% of the time.
+    if constexpr (FMT == kINT && !kGroups) {
+      each<KJ>([&](auto jc) {
+        constexpr int j = jc;
+        if constexpr (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8 kf = __builtin_bit_cast(bf16x8, *operand(tile, u * KJ + j));
-        if constexpr (FMT == kINT) {
+        for (int u = 0; u < 2; ++u) {
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, *operand(tile, u * KJ + j));
           float sc[4];
           k_scales<KJ, j>(*k_scale_dword(tile, u), sc);
 #pragma unroll
@@ -1284,15 +1346,42 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[u][ct][r] = __builtin_fmaf(sc[r], g[r], s[u][ct][r]);
           }
-        } else {
-#pragma unroll
-          for (int ct = 0; ct < NQ; ++ct)
-#pragma unroll
-            for (int t = 0; t < PLANES; ++t)
-              s[u][ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[ct][t][j], s[u][ct], 0, 0, 0);
         }
-      }
-    });
+      });
+    } else {
+      // The next operands are asked for before the instructions on these.
+      u32x4 next[2] = {*operand(tile, 0), *operand(tile, KJ)};
+      each<KJ>([&](auto jc) {
+        constexpr int j = jc;
+        const bf16x8 kf[2] = {__builtin_bit_cast(bf16x8, next[0]), __builtin_bit_cast(bf16x8, next[1])};
+        if constexpr (j + 1 < KJ) {
+          next[0] = *operand(tile, j + 1);
+          next[1] = *operand(tile, KJ + j + 1);
+        }
+        if constexpr (!kGroups) __builtin_amdgcn_sched_barrier(0x76);  // of LDS and matrix instructions alone
+        f32x4 g[2][NQ];  // INT4: sums over a group, all of them before the first one's scales
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int ct = 0; ct < NQ; ++ct) {
+            f32x4& sum = kGroups ? g[u][ct] : s[u][ct];
+            if constexpr (kGroups) sum = f32x4{qs[ct][j], qs[ct][j], qs[ct][j], qs[ct][j]};
+#pragma unroll
+            for (int t = 0; t < PLANES; ++t) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[u], qf[ct][t][j], sum, 0, 0, 0);
+          }
+        if constexpr (kGroups) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float sc[4];
+            k_scales<KJ, j>(*k_scale_dword(tile, u), sc);
+#pragma unroll
+            for (int ct = 0; ct < NQ; ++ct)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[u][ct][r] = __builtin_fmaf(sc[r], g[u][ct][r], s[u][ct][r]);
+          }
+        }
+      });
+    }
     __builtin_amdgcn_s_setprio(0);
     if (!(t0 >= clear_from && t0 + kTile <= clear_to)) mask_scores<NQ>(s, t0, lo, pos, a.window);
     u32x4 pf[NQ];
@@ -1320,7 +1409,8 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
   if (open && lane == 0) *any_open = 1;
   __syncthreads();
   const bool nan = *any_bad != 0;
-  if (uniform(*any_open)) spoil<FMT, D>(a, p, acc, pos, first, 1, all_clear_from, all_clear_to);
+  uint32_t bad_rows[NQ] = {};
+  if (uniform(*any_open)) spoiled<FMT, D, NC>(plan, wave * 16 * NQ, bad_rows);
   const float vg = FMT == kNV ? a.v_gs[0] : 1.0f / kVFactor<FMT>;
 #pragma unroll
   for (int ct = 0; ct < NQ; ++ct) {
@@ -1328,7 +1418,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
     if (nan) l[ct] = __builtin_nanf("");
     const int col = c0 + 16 * ct + n, at = col - p.t * NC;
     if (col >= all) continue;
-    const float f = p.whole ? (l[ct] != 0.0f ? vg / l[ct] : 0.0f) : 1.0f;
+    const f32x4 f = row_factors(p.whole ? (l[ct] != 0.0f ? vg / l[ct] : 0.0f) : 1.0f, bad_rows[ct]);
     if (!p.whole && q == 0) {
       p.part[at] = m[ct];
       p.part[NC + at] = l[ct];
@@ -1338,7 +1428,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       const int ch = CH * (4 * q + r);
 #pragma unroll
       for (int j = 0; j < CH; j += 4) {
-        const f32x4 v = {acc[j][ct][r] * f, acc[j + 1][ct][r] * f, acc[j + 2][ct][r] * f, acc[j + 3][ct][r] * f};
+        const f32x4 v = {acc[j][ct][r] * f[r], acc[j + 1][ct][r] * f[r], acc[j + 2][ct][r] * f[r], acc[j + 3][ct][r] * f[r]};
         if (p.whole) {
           *reinterpret_cast<u32x2*>(out_row(a, p, col, D) + ch + j) = u32x2{pack(cvt_bf16(v[0], v[1])), pack(cvt_bf16(v[2], v[3]))};
         } else {
@@ -1385,18 +1475,17 @@ __global__ __launch_bounds__(kThreads, kv_per_cu(SHAPE, D, FMT)) void kv4_attent
       join = KvJoin{rest > 0 ? (rest - 1) / s.share + 2 : 0, at.slot, 2 * w + 2, 2, 0, 0, at.s.start, at.h};
       listed = at.units > 1;
     }
-    const int i0 = at.t * NC / a.group, il = (at.t * NC + NC - 1) / a.group, cols = at.s.count * a.group - at.t * NC;
+    const int cols = at.s.count * a.group - at.t * NC;
     join.cols = cols < NC ? cols : NC;
     join.col0 = at.t * NC;
-    const Span all = span_of(a, at.s, i0, il < at.s.count ? il : at.s.count - 1);
-    const int64_t from = (int64_t)(all.lo / kKvUnit + at.off) * kKvUnit, to = from + (int64_t)at.take * kKvUnit;
+    const Span tokens = tokens_of<NC>(a, at);
     Piece p;
     p.b = at.b;
     p.h = at.h;
     p.t = at.t;
     p.s = at.s;
-    p.lo = all.lo > from ? all.lo : (int)from;
-    p.hi = all.hi < to ? all.hi : (int)to;
+    p.lo = tokens.lo;
+    p.hi = tokens.hi;
     p.whole = at.take == at.units;
     p.part = p.whole ? nullptr : a.part + (int64_t)at.slot * (NC * (D + 2));
     if (listed && at.off == 0 && threadIdx.x == 0) a.join[1 + at.rank] = join;
@@ -1406,7 +1495,7 @@ __global__ __launch_bounds__(kThreads, kv_per_cu(SHAPE, D, FMT)) void kv4_attent
       plan.left = left;
     }
     if constexpr (SHAPE == kKvPrompt) {
-      attend_prompt<FMT, D, PLANES>(a, p, lds);
+      attend_prompt<FMT, D, PLANES>(a, p, plan, lds);
     } else {
       attend<FMT, D, SHAPE, PLANES>(a, p, lds, stat);
     }
