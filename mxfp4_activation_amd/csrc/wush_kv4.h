@@ -1,6 +1,6 @@
 // Internal interface of the 4-bit key/value cache (wush_kv4.hip) and of the
 // attention over it (wush_kv4_attention.h) for their C-ABI layer
-// (wush_kv4_abi.cpp).  Not part of the public ABI.
+// (wush_serving_abi.cpp).  Not part of the public ABI.
 #ifndef WUSH_KV4_H_
 #define WUSH_KV4_H_
 
@@ -86,7 +86,11 @@ struct KvPlan {
   int64_t items, workgroups;  // at most
 };
 
-constexpr int64_t kKvWholeTokens = 512;  // up to here an item is not worth cutting
+// Up to here an item is not worth cutting: tables of 512 tokens, 8 heads, us whole and cut: 1 sequence
+// 8.3, 10.2; 8 8.4, 10.1; 128 20.8, 24.2.  Of 768: 9.6, 11.4; 9.8, 11.5; 29.0, 31.5.  Of 1024: 10.9,
+// 9.9; 11.3, 10.4; 34.7, 39.3.  The host knows the table's width alone: a sequence of 500 tokens
+// takes 8.2 in a table of 512 and 10.1 in one of 131072, with the shares and a join of nothing.
+constexpr int64_t kKvWholeTokens = 512;
 
 inline KvPlan kv_plan(int fmt, int64_t B, int64_t n, int64_t kv, int64_t group, int D, int64_t tokens) {
   KvPlan p;

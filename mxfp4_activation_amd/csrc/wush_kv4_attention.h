@@ -6,14 +6,16 @@
 // over the tokens t that query i sees, with the running maximum of the scores
 // taken out of the exponent.
 //
-// Work.  An item is one key head's queries of one sequence: up to 16, 32 or 128
+// Work.  An item is one key head's queries of one sequence: up to 16, 32 or 128 (64 for heads of 256)
 // columns (query, head of the group).  Its tokens come in units of 128.  Items
 // and units are counted on the device, from the lengths as they are when the kernel
 // runs, and items of more than a share of them are cut into pieces of about that many, one
 // per workgroup, so that one long sequence among short ones is spread over the whole chip.
 // Pieces (maximum, sum, unscaled result) meet in a second kernel by way of the workspace.
 //
-// A wave's step is 32 tokens, all of it in registers: no LDS, no barrier.
+// A wave's step is 32 tokens.  K, V and the scores stay in registers, without a barrier; so do the
+// queries of up to 16 columns (transformed ones, heads of 256 and more columns are read from LDS).
+// Prompts have K and V in LDS, expanded once per workgroup (attend_prompt).
 //   S = K Q^T with v_mfma_f32_16x16x32_bf16, A = 16 tokens, B = 16 columns: lane
 //     (n = lane % 16, q = lane / 16) of D holds column n, tokens 4 q + r.
 //   O^T += V^T P^T, A = 16 channels, B = the columns: lane (n, q) of B holds 8
@@ -200,9 +202,10 @@ struct Shares {
 // tokens, 456 items for 512 places, 1.17 times the mean: 533 us whole, 497 by runs.)
 // A share is what lets all pieces be there at once, but 4 units before it is a second
 // workgroup on a CU (8 sequences of 1000 tokens, 16 heads: 10.6 us in shares of 4, 13.4 of 1).
-// Short shares keep to one item, since a second one costs a second start: 48 sequences of up
-// to 8192 tokens, 7 units each, 27.5 us by runs and 25.7 by pieces.  Long ones are better
-// equal: 16 sequences of up to 131072, 105 units, 341 and 379.
+// Short shares keep to one item, since a second one costs a second start: 48 sequences of 1 to
+// 8192 tokens, 7 units each, 30.8 us by runs and 22.1 by pieces.  Long ones are better equal: 48
+// of 3584 to 9557, 14 units, 45.6 and 48.7, 16 of up to 131072, 105 units, 302 and 383.  Between them it
+// depends: 8 to 10 units in 48 sequences of about the same length, INT4, 31.8 and 34.5, MXFP4 37.2 and 37.4.
 constexpr int kRunUnits = 12;
 constexpr float kJoinUnits = 6.0f;
 constexpr int kAloneUnits = 4;
@@ -866,10 +869,10 @@ __device__ __forceinline__ void spoiled(const PlanLds& plan, int c0, uint32_t (&
 }
 
 // A piece for few columns, its 32-token steps dealt to the four waves.  Measured, with the
-// joining: 16 sequences of up to 131072 tokens, 8 heads of 128, INT4, 295 us: 5.0 TB/s, as a
-// device copy, vector instructions two thirds of the time.  One of 131072, MXFP4, 34 us: 4.1 TB/s.
-// 48 of up to 8192, 4 heads, NVFP4 with T_q, 20 us: 1.5 TB/s, a start of 5 us and 7 units of
-// 0.9 (waves wait for 43% of their cycles).  One of 500, 7.9 us: a launch, the lengths, the table
+// joining: 16 sequences of up to 131072 tokens, 8 heads of 128, INT4, 297 to 305 us: 4.9 TB/s, nearly a
+// device copy's 5.04, vector instructions two thirds of the time.  One of 131072, MXFP4, 34.7 us: 4.1 TB/s.
+// 48 of up to 8192, 4 heads, NVFP4 with T_q, 21.5 us: 1.4 TB/s, a start of 5 us and 7 units of
+// 0.9 (waves wait for 42% of their cycles).  One of 500, 8.2 us: a launch, the lengths, the table
 // and the codes one after the other, then 4 steps.
 template <int FMT, int D, int SHAPE, int PLANES>
 __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, float* lds, float (&stat)[2][4][32]) {
@@ -1141,8 +1144,10 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
 // they share what K and V become.  Per stage every wave expands 32 tokens (for D = 256 pairs
 // of waves K or V of them) into LDS, as the operands that all four then read; the next
 // stage's codes are on their way meanwhile.  Two chunks of 1000 queries of 32 heads behind 15000 to
-// 16384 tokens take 490 us with the joining: 937 TFLOP/s; matrix cores 37%, vector instructions
-// 41% of the time, a quarter of the waves' cycles waiting.  (Each wave expanding for itself, in
+// 16384 tokens take 480 us with the joining: 957 TFLOP/s; matrix cores 38%, vector instructions
+// 42% of the time, a quarter of the waves' cycles waiting.  (Prefills are bound by the plan instead:
+// one sequence of 2000 queries 134 us, 243 TFLOP/s, for one lane walks all of its 63 items, in load_of
+// twice and then in find, and the last items, which see most tokens, begin last.)  (Each wave expanding for itself, in
 // registers, spends 136 of 263 instructions of a step on it: 640 us.  The next tile's scores
 // among this one's exponentials: 607, for registers.)
 template <int FMT, int D>
@@ -1323,8 +1328,8 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
 #pragma unroll
       for (int ct = 0; ct < NQ; ++ct) s[u][ct] = f32x4{0, 0, 0, 0};
     // A wave among its matrix instructions goes before one among its exponentials: the other way
-    // round, or without, the former wait for the latter (INT4 645 us and 706 above, MXFP4 490 and 497,
-    // heads of 256 627 and 647).
+    // round, or without, the former wait for the latter (the prompts above: MXFP4 490 us with and 497
+    // without, heads of 256 627 and 647, before K's operands were asked for ahead).
     __builtin_amdgcn_s_setprio(1);
     // K's operands, and what becomes of their products, in an order that the compiler, left to itself,
     // gives up when registers are short: read just before they are used they cost NVFP4 and INT4
@@ -1521,7 +1526,7 @@ __global__ __launch_bounds__(kThreads, kv_per_cu(SHAPE, D, FMT)) void kv4_attent
 // The pieces of the items that have several: an item per blockIdx.x, its columns shared out
 // over blockIdx.y.  D / 4 lanes take a row's channels, so that a workgroup reads 1024 / D rows
 // at once: columns where there are few pieces, pieces of one column where there are many.
-// 4.3 us behind 48 sequences' 192 items, 13.7 (62 MB read, 4.5 TB/s) behind the two prompts above.
+// 4.6 us behind 48 sequences' 192 items, 14.0 (62 MB read, 4.4 TB/s) behind the two prompts above.
 constexpr int kFewPieces = 4;
 template <int D, int SHAPE>
 __global__ __launch_bounds__(kThreads) void kv4_join_kernel(KvAttnArgs a, int nv, float factor) {

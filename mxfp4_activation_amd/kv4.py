@@ -19,8 +19,8 @@ from .decode import _check, _check_global, _enter, _fmt, _scale_dtype, _workspac
 class KV4Cache(NamedTuple):
     """One layer's keys and values: codes uint8 [pages, heads, page, D/2], scales
     [pages, heads, page, D/G] (uint8, or float16 for INT4), for NVFP4 the tensor
-    scales (float32, one element each).  Token slot s is place s % page of page
-    s // page; page is a power of two from 16 on, D 64, 128 or 256."""
+    scales (float32, one element each, not negative).  Token slot s is place s % page of
+    page s // page; page is a power of two from 16 on, D 64, 128 or 256."""
     k_codes: torch.Tensor
     k_scales: torch.Tensor
     v_codes: torch.Tensor
@@ -110,7 +110,8 @@ def kv4_attention(fmt: str, q: torch.Tensor, cache: KV4Cache, block_table: torch
     rows contiguous), and lengths [B] (int32) counts its tokens, the queries' own
     included.  q_start [B + 1] (int32) gives each sequence's rows of q; without it each
     has one.  The last query of a sequence is its last token; a query sees the tokens
-    up to its own, or the last `window` of them.  scale: D ** -0.5 unless given.  T_q
+    up to its own, or the last `window` of them, and its result depends on those alone.
+    scale: D ** -0.5 unless given.  T_q
     [heads, D/G, G, G] goes with keys that were transformed.  Returns bf16
     [n, q_heads, D]; rows from q_start[B] on are not written."""
     native = _lib.binding()
