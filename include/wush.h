@@ -469,9 +469,11 @@ wush_status wush_kv4_append(int fmt, const void* K, int64_t ldk, const void* V, 
  *      q_start[b] .. q_start[b + 1] - 1.  NULL: one each (B == n).
  *   out: bf16 [n][q_heads][D], 16-byte aligned.  Rows from q_start[B] on are not written.
  * A sequence whose length passes width * page has NaN results, and so has a query that sees a token
- * in a page outside the cache (others of its sequence may); no access leaves the buffers.  Values that are not finite (an infinite
- * INT4 scale, say) spoil the results of the queries that see them, in their group's channels, and
- * no others; with a k_global that is NaN or negative all are NaN.  Scores and sums are fp32, T q is kept
+ * in a page outside the cache (others of its sequence may); no access leaves the buffers.  Values of
+ * a scale with which a code is not finite in bf16 (INT4 and NVFP4: a scale that is infinite or
+ * NaN, MXFP4: 2^126 and up) make the results of queries that see them infinite or NaN, in their
+ * group's channels at most, and leave all others alone; with a k_global that is NaN or negative all
+ * are NaN.  Scores and sums are fp32, T q is kept
  * to 16 significant bits, probabilities enter the sum over v with bf16's 8 for MXFP4 and fp16's
  * 11 otherwise (as do INT4's values).  scale is positive, and finite times log2 e.  Results repeat bit for bit.
  * workspace: wush_kv4_attention_workspace bytes (0 where width * page is small). */

@@ -143,3 +143,28 @@ def test_graph_replays_between_runs_and_pieces(fmt, case):
         assert torch.isfinite(replayed).all()
         assert torch.equal(call().clone(), replayed)
     assert {"runs", "pieces"} <= ways
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("case", [_RUNS[1], _RUNS[4], _RUNS[6]], ids=["narrow", "wide", "prompt"])
+@pytest.mark.parametrize("window", [0, 4000])
+def test_values_that_are_not_finite_among_runs(fmt, case, window):
+    """They spoil their group's channels for the queries that see them; everything else stays, bit for bit."""
+    rng = np.random.default_rng(8)
+    case = (*case[:7], (2, 3)) if case[0] == NARROW else case  # several queries, so that some do not see it
+    b = _batch(rng, fmt, case)
+    assert _plan(b, 0).by_runs and _plan(b, 0).shape == case[0]
+    good = b.run(window=window)
+    G = 16 if fmt == "nvfp4" else 32
+    hit = np.zeros((b.n, b.heads * b.group, b.D), bool)
+    for s in range(0, len(b.lengths), 2):
+        L, c = int(b.lengths[s]), int(b.counts[s])
+        for at in (L - 1, L - 1 - c // 2, L - c - 2500, 40):
+            page, place, g = b.table[s, at // b.page], at % b.page, int(rng.integers(0, b.D // G))
+            b.v[1][page, :, place, g] = {"mxfp4": 0xFF, "nvfp4": 0x7F, "int4": 0x7C00}[fmt]
+            b.v[0][page, :, place, g * G // 2 : (g + 1) * G // 2] = 0x77
+            pos = L - c + np.arange(c)
+            rows = b.start[s] + np.nonzero((at <= pos) & ((window == 0) | (at > pos - window)))[0]
+            hit[rows, :, g * G : (g + 1) * G] = True
+    got, hit = b.run(window=window), torch.from_numpy(hit).cuda()
+    assert torch.equal(got[~hit], good[~hit]) and not torch.isfinite(got[hit]).any()
