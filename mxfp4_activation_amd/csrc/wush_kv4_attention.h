@@ -790,15 +790,28 @@ __device__ __forceinline__ Span tokens_of(const KvAttnArgs& a, const Place& at) 
   return Span{all.lo > from ? all.lo : (int)from, all.hi < to ? all.hi : (int)to};
 }
 
+// Tokens that all columns of item t see.
+template <int NC>
+__device__ __forceinline__ Span clear_of(const KvAttnArgs& a, const Seq& s, int t) {
+  const int past = s.len - s.count, il = (t * NC + NC - 1) / a.group;
+  return Span{a.window ? past + (il < s.count ? il : s.count - 1) - a.window + 1 : 0, past + t * NC / a.group + 1};
+}
+
 // Row of the result for a column of the piece's sequence.
 __device__ __forceinline__ uint16_t* out_row(const KvAttnArgs& a, const Piece& p, int col, int D) {
   const int i = col / a.group;
   return a.out + ((int64_t)(p.s.start + i) * a.kv * a.group + p.h * a.group + col - i * a.group) * D;
 }
 
+// Of a piece's tokens, without a window, those of steps that do not lie before clear_to.
+__device__ __forceinline__ Span behind(const Span& tokens, int clear_to, int window) {
+  const int from = clear_to & -kTile;
+  return Span{!window && from > tokens.lo ? from : tokens.lo, tokens.hi};
+}
+
 // What clear_v took out, for the columns that see it: their results are NaN in the channels of its
 // group.  Sets bit r for row r of the lane's results, whose channels are those of lane 4 q + r of
-// V.  Goes once more over the scales of the piece's tokens.
+// V.  Goes once more over the scales of these of the piece's tokens.
 template <int FMT, int D, int NQ>
 __device__ __forceinline__ void spoiled(const KvAttnArgs& a, int b, int h, const Span& tokens, const int (&pos)[NQ],
                                         uint32_t (&bad)[NQ]) {
@@ -865,7 +878,7 @@ __device__ __forceinline__ void spoiled(const PlanLds& plan, int c0, uint32_t (&
     const int col = at.t * NC + c0 + 16 * ct + n;
     pos[ct] = col < columns ? at.s.len - at.s.count + col / a.group : -1;
   }
-  spoiled<FMT, D>(a, at.b, at.h, tokens_of<NC>(a, at), pos, bad);
+  spoiled<FMT, D>(a, at.b, at.h, behind(tokens_of<NC>(a, at), clear_of<NC>(a, at.s, at.t).hi, a.window), pos, bad);
 }
 
 // A piece for few columns, its 32-token steps dealt to the four waves.  Measured, with the
@@ -1068,7 +1081,7 @@ __device__ __forceinline__ void attend(const KvAttnArgs& a, const Piece& p, floa
   }
   if (open) {
     uint32_t bad[NQ], nan = 0x7FC00000u;
-    spoiled<FMT, D>(a, p.b, p.h, Span{lo, hi}, pos, bad);
+    spoiled<FMT, D>(a, p.b, p.h, behind(Span{lo, hi}, clear_to, a.window), pos, bad);
     asm volatile("" : "+s"(nan));  // (no register is kept for it either)
 #pragma unroll
     for (int j = 0; j < CH; ++j)
@@ -1267,9 +1280,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       }
   }
   // Tiles that every column of the four waves sees whole need no mask.
-  const int il = (p.t * NC + NC - 1) / a.group;
-  const int clear_to = past + p.t * NC / a.group + 1;
-  const int clear_from = a.window ? past + (il < p.s.count ? il : p.s.count - 1) - a.window + 1 : 0;
+  const Span clear = clear_of<NC>(a, p.s, p.t);
   int open = 0;
   const float scale = score_scale<FMT>(a);
   f32x4 acc[CH][NQ];
@@ -1306,7 +1317,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       }
     }
     if (does_v) {
-      if (t0 < clear_from || t0 + kTile > clear_to) {
+      if (t0 < clear.lo || t0 + kTile > clear.hi) {
         if (clear_v(w, t0, p.lo, p.hi)) open = 1;
       }
       const VScales<FMT> vs = v_scales(w);
@@ -1388,7 +1399,7 @@ __device__ __forceinline__ void attend_prompt(const KvAttnArgs& a, const Piece& 
       });
     }
     __builtin_amdgcn_s_setprio(0);
-    if (!(t0 >= clear_from && t0 + kTile <= clear_to)) mask_scores<NQ>(s, t0, lo, pos, a.window);
+    if (!(t0 >= clear.lo && t0 + kTile <= clear.hi)) mask_scores<NQ>(s, t0, lo, pos, a.window);
     u32x4 pf[NQ];
     softmax_step<FMT, NQ, CH>(s, scale, m, l, acc, pf);
     __builtin_amdgcn_s_setprio(1);
